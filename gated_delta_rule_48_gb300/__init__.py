@@ -9,12 +9,16 @@ use; importing this package does not require a GPU.
 from .binding import (  # noqa: F401
     KdaError,
     build,
+    kda_add_rms_norm,
+    kda_add_rms_norm_quant,
     kda_chunk_fwd,
     kda_decode_step,
     kda_get_device_error,
+    kda_short_conv_fwd,
+    kda_short_conv_step,
     library_path,
     load,
 )
 
-__all__ = ["KdaError", "build", "kda_chunk_fwd", "kda_decode_step",
-           "kda_get_device_error", "library_path", "load"]
+__all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_chunk_fwd", "kda_decode_step",
+           "kda_get_device_error", "kda_short_conv_fwd", "kda_short_conv_step", "library_path", "load"]

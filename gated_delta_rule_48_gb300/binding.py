@@ -105,7 +105,7 @@ class KdaTensor(ctypes.Structure):
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
 
 
-KDA_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.int32: 2}
+KDA_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.int32: 2, torch.float8_e4m3fn: 3}
 
 
 def describe(t):
@@ -183,6 +183,16 @@ def load():
             lib.kda_selftest_bounds_check.argtypes = [vp]
             lib.kda_bounds_checked.restype = ctypes.c_int
             lib.kda_bounds_checked.argtypes = []
+            f32, i = ctypes.c_float, ctypes.c_int
+            lib.kda_add_rms_norm.restype = i
+            lib.kda_add_rms_norm.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64,
+                                             i32, f32, i, i, i, vp]
+            lib.kda_short_conv_fwd.restype = i
+            lib.kda_short_conv_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32,
+                                               i32, i32, i, i, vp]
+            lib.kda_short_conv_step.restype = i
+            lib.kda_short_conv_step.argtypes = [vp, i64, vp, vp, vp, vp, i64, i32, i32, i32, i32, i,
+                                                i, vp]
             lib.kda_profile_enable.restype = None
             lib.kda_profile_enable.argtypes = [ctypes.c_int]
             lib.kda_profile_read.restype = ctypes.c_int
@@ -502,3 +512,176 @@ def kda_decode_tokens_fused(q_raw, k_raw, v, gate, beta, S_inout, commit=None, o
                                           _ptr(beta), _ptr(S_inout), _ptr(out), _ptr(commit),
                                           N, K, H, dk, dv, _stream(stream)))
     return out
+
+
+# ---- operators around the recurrent layer.  Tensors may be column slices of wider ones: rows
+# with a unit last stride, any row stride.  Outputs that are not given are allocated on the
+# stream of the call.
+
+def _rows(t, name, dtypes):
+    """(address, distance between rows, dtype code) of a [rows, columns] CUDA tensor, or of one
+    with more leading dimensions that are one row stride apart."""
+    if t is None:
+        return None, 0, 0
+    if not t.is_cuda:
+        raise KdaError(1, f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise KdaError(1, f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    d = t.dim()
+    if d < 2:
+        raise KdaError(1, f"{name} must have at least 2 dimensions")
+    shape, stride = t.shape, t.stride()
+    cols = shape[-1]
+    if stride[-1] != 1 and cols > 1:
+        raise KdaError(1, f"{name}: the last dimension must be contiguous")
+    ld = stride[-2] if shape[-2] > 1 else (stride[-3] if d > 2 and shape[-3] > 1 else max(cols, 1))
+    rows = shape[-2]
+    for k in range(d - 3, -1, -1):
+        if shape[k] > 1 and stride[k] != ld * rows:
+            raise KdaError(1, f"{name}: the leading dimensions must be one row stride apart")
+        rows *= shape[k]
+    return t.data_ptr(), ld, KDA_DTYPE[t.dtype]
+
+
+def _same_shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise KdaError(1, f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _out(given, name, shape, dtype, like, stream):
+    """The output `given`, its shape checked, or a new tensor that belongs to the call's stream."""
+    if given is not None:
+        _same_shape(given, shape, name)
+        return given
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _vector(t, n, name):
+    """(address, dtype code) of a contiguous bf16 or f32 vector of n elements, or of None."""
+    if t is None:
+        return None, 1
+    if not t.is_cuda or t.dtype not in _FLOATS:
+        raise KdaError(1, f"{name} must be a bfloat16 or float32 CUDA tensor")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise KdaError(1, f"{name} must be a contiguous vector of {n} elements")
+    return t.data_ptr(), KDA_DTYPE[t.dtype]
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_E4M3 = (torch.float8_e4m3fn,)
+_F32 = (torch.float32,)
+
+
+def _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, quant):
+    dim, shape = x.shape[-1], x.shape
+    rows = x.numel() // max(dim, 1)
+    xp, ld_x, dt = _rows(x, "x", _FLOATS)
+    rp, ld_r, _ = _rows(residual, "residual", (x.dtype,))
+    _same_shape(residual, shape, "residual")
+    wp, w_dt = _vector(weight, dim, "weight")
+    if residual is not None or h is not None:
+        h = _out(h, "h", shape, x.dtype, x, stream)
+    hp, ld_h, _ = _rows(h, "h", (x.dtype,))
+    sp, ld_s = None, 0
+    if quant:
+        if y is None:  # rows at multiples of 16 bytes, as kda_matmul_fp8 reads them
+            y = _out(None, "y", (rows, dim + -dim % 16), _E4M3[0], x, stream)[:, :dim]
+            y = y.unflatten(0, shape[:-1]) if len(shape) > 2 else y
+        y_scale = _out(y_scale, "y_scale", (*shape[:-1], (dim + 127) // 128), torch.float32, x,
+                       stream)
+        sp, ld_s, _ = _rows(y_scale, "y_scale", _F32)
+    y = _out(y, "y", shape, x.dtype, x, stream)
+    yp, ld_y, y_dt = _rows(y, "y", _E4M3 if quant else (x.dtype,))
+    _check(load().kda_add_rms_norm(xp, ld_x, rp, ld_r, wp, hp, ld_h, yp, ld_y, sp, ld_s, rows, dim,
+                                   eps, dt, w_dt, y_dt, _stream(stream)))
+    return y, y_scale, h
+
+
+def kda_add_rms_norm(x, weight, residual=None, *, eps=1e-6, y=None, h=None, stream=None):
+    """The residual's addition and the root-mean-square norm of the rows of x.
+
+    x, residual: bf16 or f32 [..., dim], rows may be strided; weight: bf16 or f32 [dim].
+    Returns (y, h): h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, both in x's
+    dtype; h is None without a residual (unless given).  y and h may be x or the residual.
+    """
+    y, _, h = _add_rms_norm(x, weight, residual, eps, h, y, None, stream, False)
+    return y, h
+
+
+def kda_add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, y=None, y_scale=None, h=None,
+                           stream=None):
+    """:func:`kda_add_rms_norm` with y in 8 bits: returns (y, y_scale, h), y float8_e4m3fn
+    [..., dim] and y_scale f32 [..., ceil(dim / 128)] with y * y_scale (per 128 columns)
+    standing for the normalised rows, as :func:`kda_matmul_fp8` reads them."""
+    return _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, True)
+
+
+def _dense(t, shape, dtype, name):
+    """The address of a contiguous CUDA tensor of that shape and dtype, or None."""
+    if t is None:
+        return None
+    _require(t, dtype, name)
+    _same_shape(t, shape, name)
+    return t.data_ptr()
+
+
+def _conv_weights(x, weight, bias):
+    dim = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[0] != dim:
+        raise KdaError(1, f"weight must have the shape ({dim}, width), got {tuple(weight.shape)}")
+    if weight.dtype not in _FLOATS:
+        raise KdaError(1, f"weight must be bfloat16 or float32, got {weight.dtype}")
+    _require(weight, weight.dtype, "weight")
+    return (weight.data_ptr(), _dense(bias, (dim,), weight.dtype, "bias"), weight.shape[1],
+            KDA_DTYPE[weight.dtype])
+
+
+def _sequences(x, cu_seqlens, n_seqs):
+    """(tokens, sequences, address of cu_seqlens) of packed [T, dim] or uniform [B, T_b, dim] x."""
+    tokens = x.numel() // max(x.shape[-1], 1)
+    if cu_seqlens is not None:
+        _require(cu_seqlens, torch.int32, "cu_seqlens")
+        return tokens, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
+    return tokens, n_seqs if n_seqs is not None else (x.shape[0] if x.dim() > 2 else 1), None
+
+
+def kda_short_conv_fwd(x, weight, bias=None, conv_state=None, cu_seqlens=None, *, n_seqs=None,
+                       silu=True, want_state=True, y=None, state_out=None, stream=None):
+    """Short causal convolution per channel over packed sequences.
+
+    x: bf16 or f32 [T, dim] (or [B, T_b, dim], a uniform batch), rows may be strided; weight:
+    bf16 or f32 [dim, width]; bias: [dim] in weight's dtype or None; conv_state: [N, width - 1,
+    dim] in x's dtype or None (zeros); cu_seqlens: int32 [N + 1] (CUDA) or None.  Returns
+    (y, state): the state continues the sequences; ``state_out`` may be ``conv_state`` itself.
+    """
+    T, N, cu = _sequences(x, cu_seqlens, n_seqs)
+    xp, ld_x, dt = _rows(x, "x", _FLOATS)
+    wp, bp, width, w_dt = _conv_weights(x, weight, bias)
+    shape = (N, width - 1, x.shape[-1])
+    y = _out(y, "y", x.shape, x.dtype, x, stream)
+    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    if want_state or state_out is not None:
+        state_out = _out(state_out, "state_out", shape, x.dtype, x, stream)
+    _check(load().kda_short_conv_fwd(xp, ld_x, wp, bp, _dense(conv_state, shape, x.dtype, "conv_state"),
+                                     _dense(state_out, shape, x.dtype, "state_out"), cu, yp, ld_y,
+                                     T, N, x.shape[-1], width, 1 if silu else 0, dt, w_dt,
+                                     _stream(stream)))
+    return y, state_out
+
+
+def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, stream=None):
+    """One token of each sequence: x [N, dim]; ``conv_state`` [N, width - 1, dim] is updated in
+    place.  Otherwise as :func:`kda_short_conv_fwd`.  Returns y [N, dim]."""
+    N, dim = x.shape
+    xp, ld_x, dt = _rows(x, "x", _FLOATS)
+    wp, bp, width, w_dt = _conv_weights(x, weight, bias)
+    y = _out(y, "y", x.shape, x.dtype, x, stream)
+    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    _check(load().kda_short_conv_step(xp, ld_x, wp, bp,
+                                      _dense(conv_state, (N, width - 1, dim), x.dtype, "conv_state"),
+                                      yp, ld_y, N, dim, width, 1 if silu else 0, dt, w_dt,
+                                      _stream(stream)))
+    return y

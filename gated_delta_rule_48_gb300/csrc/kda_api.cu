@@ -12,6 +12,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_ops.h"
 
 namespace kda {
 
@@ -131,6 +132,33 @@ kda_status device_error_word(int** out) {
   kda_status st = device_state(&dev);
   if (st == KDA_OK) *out = dev->err;
   return st;
+}
+
+kda_status device_sm_count(int* out) {
+  DeviceState* dev = nullptr;
+  kda_status st = device_state(&dev);
+  if (st == KDA_OK) *out = dev->sm_count;
+  return st;
+}
+
+// Stream capture turns the allocation into a graph memory node, which takes
+// the default pool; otherwise the library's own pool keeps workspace cached.
+static cudaError_t pool_alloc(const DeviceState* dev, bool capturing, size_t bytes, cudaStream_t s,
+                              void** out) {
+  return capturing ? cudaMallocAsync(out, bytes, s)
+                   : cudaMallocFromPoolAsync(out, bytes, dev->pool, s);
+}
+
+kda_status workspace_alloc(size_t bytes, cudaStream_t s, void** out) {
+  DeviceState* dev = nullptr;
+  kda_status st = device_state(&dev, /*want_pool=*/true);
+  if (st != KDA_OK) return st;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  e = pool_alloc(dev, cap != cudaStreamCaptureStatusNone, bytes, s, out);
+  if (e != cudaSuccess) return cuda_fail(e, "workspace allocation");
+  return KDA_OK;
 }
 
 void prof_begin(cudaStream_t s, const char* name) {
@@ -367,15 +395,12 @@ static kda_status chunk_fwd_impl(const void* q, const void* k, const void* v,
   if (!direct) {
     st = device_state(&dev, /*want_pool=*/true);
     if (st != KDA_OK) return st;
-    // Stream capture turns the allocation into a graph memory node, which takes
-    // the default pool; otherwise the library's own pool keeps workspace cached.
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     e = cudaStreamIsCapturing(s, &cap);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
     auto alloc = [&](size_t bytes) {
-      return cap == cudaStreamCaptureStatusNone
-                 ? cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), bytes, dev->pool, s)
-                 : cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, s);
+      return pool_alloc(dev, cap != cudaStreamCaptureStatusNone, bytes, s,
+                        reinterpret_cast<void**>(&ws));
     };
     e = alloc(ws_bytes);
     if (e == cudaErrorMemoryAllocation && t_bytes > 0) {

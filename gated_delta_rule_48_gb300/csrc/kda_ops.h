@@ -1,0 +1,195 @@
+// Internal declarations of the operators around the recurrent layer (norm,
+// 8-bit product, short convolution, selective scan): the arguments their
+// kernels take, already checked by the entry points (kda_ops_api.cu), and the
+// device helpers the kernels share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda.h"
+#include "kda_internal.h"
+
+namespace kda {
+
+constexpr int kScaleGroup = 128;         // columns (or rows and columns) that share a scale
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxMin = 0x1p-64f;     // a group's largest magnitude counts as at least this
+constexpr int kMaxNormDim = 65536;
+
+// ---- kda_add_rms_norm (kda_norm.cu).  Leading dimensions in elements.
+struct NormArgs {
+  const void* x;
+  const void* residual;   // null: h = x
+  const void* weight;     // [dim]
+  void* h;                // x + residual in x's type, or null
+  void* y;                // x's type, or e4m3 with y_scale
+  float* y_scale;         // [rows, ceil(dim / 128)] when y is e4m3
+  int64_t ld_x, ld_res, ld_h, ld_y, ld_scale;
+  int64_t rows;
+  int32_t dim;
+  float eps;
+  bool bf16, w_bf16, quant;
+  bool vec;               // every row starts on a 16-byte boundary and dim % 8 == 0
+  int sm_count;
+  int* err;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
+
+// ---- kda_short_conv_fwd, kda_short_conv_step (kda_conv.cu)
+constexpr int kMaxConvWidth = 8;
+struct ConvArgs {
+  const void* x;          // [T, dim]; the step: [N, dim], one token of each sequence
+  const void* weight;     // [dim, width]
+  const void* bias;       // [dim] or null
+  const void* state_in;   // [N, width - 1, dim] or null (zeros)
+  void* state_out;        // [N, width - 1, dim] or null; the step: state_in itself
+  const int32_t* cu;      // [N + 1] or null (N sequences of T / N tokens)
+  void* y;                // [T, dim]
+  int64_t ld_x, ld_y, T;
+  int32_t N, dim, width;
+  bool bf16, w_bf16, silu;
+  bool vec;               // rows start on 16-byte boundaries and hold whole vectors
+  int sm_count;
+  int* err;
+};
+cudaError_t launch_conv(const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
+
+// ---- host-side state shared with the other entry points (kda_api.cu)
+kda_status device_sm_count(int* out);
+// Stream-ordered workspace from the library's pool (while `s` is being
+// captured: from the device's default pool, as a graph memory node).
+kda_status workspace_alloc(size_t bytes, cudaStream_t s, void** out);
+
+// ---- device helpers
+struct Bf16 { uint16_t bits; };
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(Bf16 v) { return bf16_to_f32(v.bits); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ Bf16 from_f32<Bf16>(float v) {
+  Bf16 r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r.bits) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight consecutive elements, 16-byte aligned.
+__device__ __forceinline__ void load8(const Bf16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(Bf16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]),
+                                            pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// N consecutive elements, aligned to their total size (at most 16 bytes a load).
+template <int N, typename T>
+__device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = to_f32(*p);
+  } else if constexpr (N == 8) {
+    load8(p, v);
+  } else {
+    static_assert(N == 4 && sizeof(T) == 4, "four 32-bit elements");
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    *p = from_f32<T>(v[0]);
+  } else if constexpr (N == 8) {
+    store8(p, v);
+  } else {
+    static_assert(N == 4 && sizeof(T) == 4, "four 32-bit elements");
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// The sequence of packed token t: the first n with cu[n + 1] > t (at most N - 1).
+// Whatever cu holds, the result is in [0, N - 1].
+__device__ __forceinline__ int32_t sequence_of(const int32_t* cu, int32_t N, int64_t t, int* err) {
+  int32_t lo = 0, hi = N - 1;
+  while (lo < hi) {
+    const int32_t mid = lo + ((hi - lo) >> 1);
+    if (!kda_guard(mid + 1, 1, static_cast<int64_t>(N) + 1, err)) break;
+    if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// cu_seqlens checked by one block: cu[0] = 0, no decrease, cu[N] = T.
+__device__ __forceinline__ void check_cu_seqlens(const int32_t* cu, int32_t N, int64_t T, int tid,
+                                                 int n_threads, int* err) {
+  bool ok = true;
+  for (int64_t n = tid; n < N; n += n_threads) {
+    if (!kda_guard(n, 2, static_cast<int64_t>(N) + 1, err)) break;
+    ok = ok && cu[n + 1] >= cu[n];
+    if (n == 0) ok = ok && cu[0] == 0;
+    if (n == N - 1) ok = ok && cu[N] == T;
+  }
+  if (!ok) atomicOr(err, kDevErrCuSeqlens);
+}
+
+// Tokens [start, end) of sequence n: from cu, clamped to [0, T], or of T / N tokens.
+__device__ __forceinline__ void sequence_span(const int32_t* cu, int32_t N, int64_t T, int32_t n,
+                                              int64_t& start, int64_t& end, int* err) {
+  if (cu) {
+    start = end = 0;
+    if (!kda_guard(n, 2, static_cast<int64_t>(N) + 1, err)) return;
+    start = min(max(static_cast<int64_t>(cu[n]), int64_t{0}), T);
+    end = min(max(static_cast<int64_t>(cu[n + 1]), start), T);
+  } else {
+    const int64_t len = T / N;
+    start = len * n;
+    end = start + len;
+  }
+}
+
+// The larger of two values; NaN if either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Two values to e4m3, round to nearest even, clamped to +-448 (NaN stays NaN).
+__device__ __forceinline__ uint16_t pack2_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// v * sigmoid(v).  The approximate exponential and quotient are within a few
+// units of the last place of the 32-bit result.
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
+}  // namespace kda

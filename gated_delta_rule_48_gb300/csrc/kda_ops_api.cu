@@ -1,0 +1,249 @@
+// Entry points of the operators around the recurrent layer (include/kda.h):
+// argument checks on the host, then the launches.
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+
+#include "kda.h"
+#include "kda_internal.h"
+#include "kda_ops.h"
+
+namespace kda {
+namespace {
+
+kda_status bad(kda_status st, const char* fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof msg, fmt, ap);
+  va_end(ap);
+  return report_error(st, msg);
+}
+
+kda_status launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return KDA_OK;
+  return bad(e == cudaErrorMemoryAllocation ? KDA_ERR_OUT_OF_MEMORY : KDA_ERR_CUDA, "%s: %s", what,
+             cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+int64_t size_of(kda_dtype t) { return t == KDA_BF16 ? 2 : t == KDA_E4M3 ? 1 : 4; }
+
+// Rows of `width` bytes, `pitch` bytes apart.  A null pointer has no rows.
+struct Rows {
+  const char* name;
+  const void* p;
+  int64_t rows, pitch, width;
+};
+
+Rows rows_of(const char* name, const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t esize) {
+  return Rows{name, p, p ? rows : 0, ld * esize, cols * esize};
+}
+
+bool same_rows(const Rows& a, const Rows& b) {
+  return a.p == b.p && a.width == b.width && (a.pitch == b.pitch || a.rows <= 1);
+}
+
+// Whether two sets of rows share a byte.  Rows of one pitch may interleave
+// (column slices of one buffer); rows of different pitches count as
+// overlapping where their spans do.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>((a.rows - 1) * a.pitch + a.width);
+  const uintptr_t b1 = b0 + static_cast<uintptr_t>((b.rows - 1) * b.pitch + b.width);
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.pitch == b.pitch && a.pitch > 0) {
+    const int64_t pitch = a.pitch;
+    int64_t d = static_cast<int64_t>(b0 - a0) % pitch;  // b's first column in a's rows
+    if (d < 0) d += pitch;
+    if (d >= a.width && pitch - d >= b.width) return false;
+  }
+  return true;
+}
+
+// An output against inputs and the other outputs; `may_be`: the one it may equal exactly.
+kda_status check_output(const Rows& out, const Rows* others, int n, const Rows* may_be,
+                        const Rows* may_be2 = nullptr) {
+  for (int i = 0; i < n; ++i) {
+    if (!overlap(out, others[i])) continue;
+    const bool allowed = (&others[i] == may_be || &others[i] == may_be2) && same_rows(out, others[i]);
+    if (!allowed) return bad(KDA_ERR_INVALID_ARGUMENT, "%s overlaps %s", out.name, others[i].name);
+  }
+  return KDA_OK;
+}
+
+bool float_type(kda_dtype t) { return t == KDA_BF16 || t == KDA_F32; }
+
+// Pointer alignment to its element, and a leading dimension that holds a row.
+kda_status check_rows(const char* name, const void* p, int64_t ld, int64_t cols, int64_t esize) {
+  if (!aligned(p, static_cast<uintptr_t>(esize)))
+    return bad(KDA_ERR_INVALID_ARGUMENT, "%s is not aligned to its element", name);
+  if (p && ld < cols)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "%s: leading dimension %lld is less than the %lld columns",
+               name, (long long)ld, (long long)cols);
+  if (p && ld > (1LL << 40))
+    return bad(KDA_ERR_INVALID_ARGUMENT, "%s: leading dimension %lld", name, (long long)ld);
+  return KDA_OK;
+}
+
+#define KDA_TRY(call)                      \
+  do {                                     \
+    const kda_status st_ = (call);         \
+    if (st_ != KDA_OK) return st_;         \
+  } while (0)
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_add_rms_norm(const void* x, int64_t ld_x, const void* residual,
+                                       int64_t ld_residual, const void* weight, void* h,
+                                       int64_t ld_h, void* y, int64_t ld_y, float* y_scale,
+                                       int64_t ld_scale, int64_t rows, int32_t dim, float eps,
+                                       kda_dtype dtype, kda_dtype weight_dtype, kda_dtype y_dtype,
+                                       void* stream) {
+  NvtxRange nvtx_range("kda_add_rms_norm");
+  if (rows < 0 || dim <= 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "rows=%lld dim=%d", (long long)rows, dim);
+  if (!float_type(dtype) || !float_type(weight_dtype))
+    return bad(KDA_ERR_INVALID_ARGUMENT, "x and weight must be bf16 or f32");
+  if (y_dtype != dtype && y_dtype != KDA_E4M3)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "y must have x's dtype or be e4m3");
+  if (!(eps >= 0.0f)) return bad(KDA_ERR_INVALID_ARGUMENT, "eps=%g must not be negative", eps);
+  if (dim > kMaxNormDim)
+    return bad(KDA_ERR_UNSUPPORTED, "dim=%d exceeds %d", dim, kMaxNormDim);
+  if (rows > 0x7fffffffLL)
+    return bad(KDA_ERR_UNSUPPORTED, "rows=%lld exceed the grid", (long long)rows);
+  if (rows == 0) return KDA_OK;
+  const bool quant = y_dtype == KDA_E4M3;
+  if (!x || !weight || !y)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", !x ? "x" : !weight ? "weight" : "y");
+  if (quant != (y_scale != nullptr))
+    return bad(KDA_ERR_INVALID_ARGUMENT,
+               quant ? "y_scale is NULL but y is e4m3" : "y_scale is given but y is not e4m3");
+  if (residual && !h) return bad(KDA_ERR_INVALID_ARGUMENT, "residual is given but h is NULL");
+  const int64_t es = size_of(dtype), ws = size_of(weight_dtype), ys = size_of(y_dtype);
+  const int64_t groups = (dim + kScaleGroup - 1) / kScaleGroup;
+  KDA_TRY(check_rows("x", x, ld_x, dim, es));
+  KDA_TRY(check_rows("residual", residual, ld_residual, dim, es));
+  KDA_TRY(check_rows("weight", weight, dim, dim, ws));
+  KDA_TRY(check_rows("h", h, ld_h, dim, es));
+  KDA_TRY(check_rows("y", y, ld_y, dim, ys));
+  KDA_TRY(check_rows("y_scale", y_scale, ld_scale, groups, 4));
+  const Rows in[] = {rows_of("x", x, rows, ld_x, dim, es),
+                     rows_of("residual", residual, rows, ld_residual, dim, es),
+                     rows_of("weight", weight, 1, dim, dim, ws)};
+  const Rows out[] = {rows_of("h", h, rows, ld_h, dim, es), rows_of("y", y, rows, ld_y, dim, ys),
+                      rows_of("y_scale", y_scale, rows, ld_scale, groups, 4)};
+  // a row is read whole before its h or y is written: both may replace x or the residual
+  KDA_TRY(check_output(out[0], in, 3, &in[0], &in[1]));
+  KDA_TRY(check_output(out[1], in, 3, quant ? nullptr : &in[0], quant ? nullptr : &in[1]));
+  KDA_TRY(check_output(out[2], in, 3, nullptr));
+  KDA_TRY(check_output(out[1], &out[0], 1, nullptr));
+  KDA_TRY(check_output(out[2], &out[0], 2, nullptr));
+
+  NormArgs a;
+  a.x = x; a.residual = residual; a.weight = weight; a.h = h; a.y = y; a.y_scale = y_scale;
+  a.ld_x = ld_x;
+  a.ld_res = residual ? ld_residual : 0;
+  a.ld_h = ld_h; a.ld_y = ld_y; a.ld_scale = ld_scale;
+  a.rows = rows; a.dim = dim; a.eps = eps;
+  a.bf16 = dtype == KDA_BF16; a.w_bf16 = weight_dtype == KDA_BF16; a.quant = quant;
+  auto wide = [&](const void* p, int64_t ld, int64_t size, int64_t bytes) {
+    return !p || (aligned(p, static_cast<uintptr_t>(bytes)) && (rows == 1 || ld * size % bytes == 0));
+  };
+  a.vec = dim % 8 == 0 && wide(x, ld_x, es, 16) && wide(residual, ld_residual, es, 16) &&
+          wide(h, ld_h, es, 16) && wide(y, ld_y, ys, quant ? 8 : 16) && aligned(weight, 16);
+  KDA_TRY(device_sm_count(&a.sm_count));
+  KDA_TRY(device_error_word(&a.err));
+  return launched(launch_norm(a, static_cast<cudaStream_t>(stream)), "norm launch");
+}
+
+// The checks that the convolution's two entry points share.
+static kda_status check_conv(const void* x, int64_t ld_x, const void* weight, const void* bias,
+                             const void* state_in, const void* state_out, const int32_t* cu,
+                             const void* y, int64_t ld_y, int64_t T, int32_t N, int32_t dim,
+                             int32_t width, kda_dtype dtype, kda_dtype w_dtype, ConvArgs& a) {
+  if (T < 0 || N < 0 || dim <= 0 || width <= 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "total_tokens=%lld n_seqs=%d dim=%d width=%d", (long long)T,
+               N, dim, width);
+  if (!float_type(dtype) || !float_type(w_dtype))
+    return bad(KDA_ERR_INVALID_ARGUMENT, "x and weight must be bf16 or f32");
+  if (width < 2 || width > kMaxConvWidth)
+    return bad(KDA_ERR_UNSUPPORTED, "width=%d is not in [2, %d]", width, kMaxConvWidth);
+  if (dim > (1 << 24)) return bad(KDA_ERR_UNSUPPORTED, "dim=%d exceeds %d", dim, 1 << 24);
+  if (T > 0x7fffffffLL) return bad(KDA_ERR_UNSUPPORTED, "total_tokens=%lld", (long long)T);
+  if (N == 0 && T > 0) return bad(KDA_ERR_INVALID_ARGUMENT, "tokens given but n_seqs = 0");
+  if (!cu && N > 0 && T % N != 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT,
+               "cu_seqlens is NULL but total_tokens=%lld is not a multiple of n_seqs=%d",
+               (long long)T, N);
+  if (N == 0) return KDA_OK;
+  const struct { const void* p; const char* n; } req[] = {{x, "x"}, {weight, "weight"}, {y, "y"}};
+  if (T > 0)
+    for (auto& r : req)
+      if (!r.p) return bad(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", r.n);
+  const int64_t es = size_of(dtype), ws = size_of(w_dtype), rows = static_cast<int64_t>(N) * (width - 1);
+  KDA_TRY(check_rows("x", x, ld_x, dim, es));
+  KDA_TRY(check_rows("weight", weight, width, width, ws));
+  KDA_TRY(check_rows("bias", bias, dim, dim, ws));
+  KDA_TRY(check_rows("state_in", state_in, dim, dim, es));
+  KDA_TRY(check_rows("state_out", state_out, dim, dim, es));
+  KDA_TRY(check_rows("cu_seqlens", cu, 1, 1, 4));
+  KDA_TRY(check_rows("y", y, ld_y, dim, es));
+  const Rows in[] = {rows_of("x", x, T, ld_x, dim, es),
+                     rows_of("weight", weight, 1, static_cast<int64_t>(dim) * width,
+                             static_cast<int64_t>(dim) * width, ws),
+                     rows_of("bias", bias, 1, dim, dim, ws),
+                     rows_of("state_in", state_in, 1, rows * dim, rows * dim, es),
+                     rows_of("cu_seqlens", cu, 1, N + 1LL, N + 1LL, 4)};
+  const Rows out[] = {rows_of("state_out", state_out, 1, rows * dim, rows * dim, es),
+                      rows_of("y", y, T, ld_y, dim, es)};
+  KDA_TRY(check_output(out[0], in, 5, &in[3]));  // the state may be continued in place
+  KDA_TRY(check_output(out[1], in, 5, nullptr));
+  KDA_TRY(check_output(out[1], &out[0], 1, nullptr));
+  a.x = x; a.weight = weight; a.bias = bias; a.state_in = state_in;
+  a.state_out = const_cast<void*>(state_out);
+  a.cu = cu; a.y = const_cast<void*>(y);
+  a.ld_x = ld_x; a.ld_y = ld_y; a.T = T; a.N = N; a.dim = dim; a.width = width;
+  a.bf16 = dtype == KDA_BF16; a.w_bf16 = w_dtype == KDA_BF16;
+  a.vec = static_cast<int64_t>(dim) * es % 16 == 0 && ld_x * es % 16 == 0 && ld_y * es % 16 == 0 &&
+          aligned(x, 16) && aligned(y, 16) && aligned(weight, 16) && aligned(state_in, 16) &&
+          aligned(state_out, 16);
+  KDA_TRY(device_sm_count(&a.sm_count));
+  return device_error_word(&a.err);
+}
+
+extern "C" kda_status kda_short_conv_fwd(const void* x, int64_t ld_x, const void* weight,
+                                         const void* bias, const void* state_in, void* state_out,
+                                         const int32_t* cu_seqlens, void* y, int64_t ld_y,
+                                         int64_t total_tokens, int32_t n_seqs, int32_t dim,
+                                         int32_t width, int32_t activation, kda_dtype dtype,
+                                         kda_dtype weight_dtype, void* stream) {
+  NvtxRange nvtx_range("kda_short_conv_fwd");
+  ConvArgs a;
+  KDA_TRY(check_conv(x, ld_x, weight, bias, state_in, state_out, cu_seqlens, y, ld_y, total_tokens,
+                     n_seqs, dim, width, dtype, weight_dtype, a));
+  if (n_seqs == 0) return KDA_OK;
+  a.silu = activation != 0;
+  return launched(launch_conv(a, static_cast<cudaStream_t>(stream)), "convolution launch");
+}
+
+extern "C" kda_status kda_short_conv_step(const void* x, int64_t ld_x, const void* weight,
+                                          const void* bias, void* state, void* y, int64_t ld_y,
+                                          int32_t n_seqs, int32_t dim, int32_t width,
+                                          int32_t activation, kda_dtype dtype,
+                                          kda_dtype weight_dtype, void* stream) {
+  NvtxRange nvtx_range("kda_short_conv_step");
+  if (n_seqs > 0 && !state) return bad(KDA_ERR_INVALID_ARGUMENT, "state is NULL");
+  ConvArgs a;
+  KDA_TRY(check_conv(x, ld_x, weight, bias, state, state, nullptr, y, ld_y, n_seqs, n_seqs, dim,
+                     width, dtype, weight_dtype, a));
+  if (n_seqs == 0) return KDA_OK;
+  a.silu = activation != 0;
+  return launched(launch_conv_step(a, static_cast<cudaStream_t>(stream)), "convolution launch");
+}

@@ -18,6 +18,7 @@ const char* dtype_name(kda_dtype t) {
     case KDA_BF16: return "bf16";
     case KDA_F32: return "f32";
     case KDA_I32: return "i32";
+    case KDA_E4M3: return "e4m3";
   }
   return "unknown";
 }

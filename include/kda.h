@@ -141,7 +141,7 @@ kda_status kda_chunk_fwd(const void *q, const void *k, const void *v,
  * [N, H]; S_inout [N, H, dk, dv].
  * The descriptors are read during the call only.
  */
-typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_I32 = 2 } kda_dtype;
+typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_I32 = 2, KDA_E4M3 = 3 } kda_dtype;
 
 typedef struct {
     void *data;         /* device pointer to element [0, 0, ...] */
@@ -423,6 +423,90 @@ kda_status kda_decode_step_fused(const void *q_raw, const void *k_raw, const voi
                                  float *S_inout, void *out, int32_t n_seqs,
                                  int32_t n_heads, int32_t dk, int32_t dv,
                                  void *stream);
+
+/*
+ * Operators around the recurrent layer.
+ *
+ * In a model, a projection of the normalised residual stream feeds the layer
+ * through a short causal convolution, and another projection takes its output
+ * back.  The calls below are those steps.  They follow the conventions at the
+ * top of this file (streams, ownership, errors), with two differences: rows
+ * may be strided (an `ld_*` argument is the distance between rows, in
+ * elements, so a tensor may be some columns of a wider one), and a pointer
+ * needs only its element's alignment unless its call says otherwise (rows
+ * that all start on 16-byte boundaries run faster).
+ *
+ * kda_add_rms_norm -- the residual's addition and the root-mean-square norm.
+ *
+ *     h = x + residual
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * The sum, the mean and the scaling are in 32 bits; the norm is taken of the
+ * 32-bit sum, and h and y are each rounded once, when stored.
+ *
+ * Tensors (R = rows):
+ *   x, residual  bf16 or f32 (`dtype`) [R, dim]  read; residual may be NULL
+ *                                                (h = x)
+ *   weight       bf16 or f32 (`weight_dtype`) [dim]  read
+ *   h            `dtype` [R, dim]   written; required with a residual, else
+ *                                   may be NULL.  May be x or the residual
+ *                                   itself (same pointer and ld).
+ *   y            `y_dtype` [R, dim] written: `dtype`, or KDA_E4M3.  In
+ *                                   `dtype` it may be x or the residual itself.
+ *   y_scale      f32 [R, ceil(dim / 128)]  written with an e4m3 y, else NULL
+ * 8-bit output: each row's columns 128 g .. 128 g + 127 share the scale
+ * s_g = max(max |y|, 2^-64) / 448 and y stores e4m3(y * (448 / max |y|)),
+ * rounded to nearest even, so that y * y_scale stands for the row.  A NaN in a
+ * row makes the row's y and scales NaN.
+ * dim <= 65536.  rows = 0 is a no-op.  Allocates nothing.
+ */
+kda_status kda_add_rms_norm(const void *x, int64_t ld_x, const void *residual,
+                            int64_t ld_residual, const void *weight, void *h,
+                            int64_t ld_h, void *y, int64_t ld_y, float *y_scale,
+                            int64_t ld_scale, int64_t rows, int32_t dim,
+                            float eps, kda_dtype dtype, kda_dtype weight_dtype,
+                            kda_dtype y_dtype, void *stream);
+
+/*
+ * kda_short_conv_fwd, kda_short_conv_step -- a short causal convolution per
+ * channel, for packed prompts and for one token of each sequence.
+ *
+ *     y[t, d] = act(bias[d] + sum_j weight[d, j] x[t - width + 1 + j, d])
+ *
+ * act is SiLU (`activation` != 0) or nothing.  The width - 1 rows before a
+ * sequence's first token are those of its state, or zeros; the last
+ * width - 1 rows of state and tokens together are its state afterwards.  Sums
+ * are in 32 bits, y is rounded once, the state is copied.
+ *
+ * Tensors (T = total_tokens, N = n_seqs; the step: one token per sequence, T = N):
+ *   x          bf16 or f32 (`dtype`) [T, dim]        read
+ *   weight     bf16 or f32 (`weight_dtype`) [dim, width]  read, dense
+ *   bias       `weight_dtype` [dim]                  read; NULL = none
+ *   state_in   `dtype` [N, width - 1, dim], dense    read; NULL = zeros
+ *   state_out  `dtype` [N, width - 1, dim], dense    written; NULL = not
+ *                                                    produced; may be state_in
+ *                                                    itself
+ *   cu_seqlens i32 [N + 1] as in kda_chunk_fwd (checked on the GPU: a
+ *              malformed array is reported by kda_get_device_error, and y
+ *              and the states are then unspecified), or NULL
+ *   y          `dtype` [T, dim]                      written
+ * The step reads and overwrites `state` ([N, width - 1, dim]).
+ * width in [2, 8], else KDA_ERR_UNSUPPORTED.  T = 0 or N = 0 are valid.
+ * Allocates nothing.
+ */
+kda_status kda_short_conv_fwd(const void *x, int64_t ld_x, const void *weight,
+                              const void *bias, const void *state_in,
+                              void *state_out, const int32_t *cu_seqlens,
+                              void *y, int64_t ld_y, int64_t total_tokens,
+                              int32_t n_seqs, int32_t dim, int32_t width,
+                              int32_t activation, kda_dtype dtype,
+                              kda_dtype weight_dtype, void *stream);
+kda_status kda_short_conv_step(const void *x, int64_t ld_x, const void *weight,
+                               const void *bias, void *state, void *y,
+                               int64_t ld_y, int32_t n_seqs, int32_t dim,
+                               int32_t width, int32_t activation,
+                               kda_dtype dtype, kda_dtype weight_dtype,
+                               void *stream);
 
 /*
  * kda_get_device_error -- synchronise `stream`, then return and clear the
