@@ -16,9 +16,12 @@ from .binding import (  # noqa: F401
     kda_get_device_error,
     kda_short_conv_fwd,
     kda_short_conv_step,
+    kda_ssm_scan_fwd,
+    kda_ssm_scan_step,
     library_path,
     load,
 )
 
-__all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_chunk_fwd", "kda_decode_step",
-           "kda_get_device_error", "kda_short_conv_fwd", "kda_short_conv_step", "library_path", "load"]
+__all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_chunk_fwd",
+           "kda_decode_step", "kda_get_device_error", "kda_short_conv_fwd", "kda_short_conv_step",
+           "kda_ssm_scan_fwd", "kda_ssm_scan_step", "library_path", "load"]

@@ -193,6 +193,13 @@ def load():
             lib.kda_short_conv_step.restype = i
             lib.kda_short_conv_step.argtypes = [vp, i64, vp, vp, vp, vp, i64, i32, i32, i32, i32, i,
                                                 i, vp]
+            lib.kda_ssm_scan_fwd.restype = i
+            lib.kda_ssm_scan_fwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp,
+                                             vp, vp, vp, i64, vp, i64, i32, i32, i32, i32, i32, i,
+                                             vp]
+            lib.kda_ssm_scan_step.restype = i
+            lib.kda_ssm_scan_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64,
+                                              vp, vp, vp, i64, i32, i32, i32, i32, i32, i, vp]
             lib.kda_profile_enable.restype = None
             lib.kda_profile_enable.argtypes = [ctypes.c_int]
             lib.kda_profile_read.restype = ctypes.c_int
@@ -684,4 +691,70 @@ def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, 
                                       _dense(conv_state, (N, width - 1, dim), x.dtype, "conv_state"),
                                       yp, ld_y, N, dim, width, 1 if silu else 0, dt, w_dt,
                                       _stream(stream)))
+    return y
+
+
+def _groups_of(t, x, name):
+    """(address, distance between tokens) of B or C, [..., groups, state] with a dense token."""
+    if t.dim() != x.dim() + 1 or t.shape[:-2] != x.shape[:-1]:
+        raise KdaError(1, f"{name} must have the shape {(*x.shape[:-1], 'groups', 'state')}, got "
+                          f"{tuple(t.shape)}")
+    groups, state = t.shape[-2:]
+    if groups > 1 and t.stride(-2) != state:
+        raise KdaError(1, f"{name}: the groups of a token must be dense")
+    return _rows(t.select(-2, 0) if groups > 0 else t, name, (x.dtype,))[:2]
+
+
+def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
+    """The arguments that the scan and its step share, and (dim, state, groups, dtype)."""
+    xp, ld_x, code = _rows(x, "x", _FLOATS)
+    dim = x.shape[-1]
+    for t, name in ((dt, "dt"), (z, "z")):
+        _same_shape(t, x.shape, name)
+    dtp, ld_dt, _ = _rows(dt, "dt", (x.dtype,))
+    zp, ld_z, _ = _rows(z, "z", (x.dtype,))
+    bp, ld_b = _groups_of(B, x, "B")
+    cp, ld_c = _groups_of(C, x, "C")
+    _same_shape(C, B.shape, "C")
+    groups, state = B.shape[-2:]
+    f32 = torch.float32
+    return ([xp, ld_x, dtp, ld_dt, _dense(A, (dim, state), f32, "A"), bp, ld_b, cp, ld_c,
+             _dense(D, (dim,), f32, "D"), zp, ld_z, _dense(dt_bias, (dim,), f32, "dt_bias")],
+            dim, state, groups, code)
+
+
+def kda_ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, *,
+                     n_seqs=None, softplus=True, want_state=True, y=None, h_final=None,
+                     stream=None):
+    """Selective state space scan over packed sequences (see include/kda.h).
+
+    x, dt, z: bf16 or f32 [T, dim] (or [B, T_b, dim], a uniform batch), rows may be strided;
+    A: f32 [dim, state], negative; B, C: [T, groups, state] in x's dtype; D, dt_bias: f32 [dim]
+    or None; h0: f32 [N, dim, state] or None (zeros); cu_seqlens: int32 [N + 1] (CUDA) or None.
+    Returns (y, h_final); ``h_final`` may be ``h0`` itself.
+    """
+    T, N, cu = _sequences(x, cu_seqlens, n_seqs)
+    args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
+    y = _out(y, "y", x.shape, x.dtype, x, stream)
+    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    shape = (N, dim, state)
+    if want_state or h_final is not None:
+        h_final = _out(h_final, "h_final", shape, torch.float32, x, stream)
+    _check(load().kda_ssm_scan_fwd(*args, _dense(h0, shape, torch.float32, "h0"), cu, yp, ld_y,
+                                   _dense(h_final, shape, torch.float32, "h_final"), T, N, dim,
+                                   state, groups, 1 if softplus else 0, code, _stream(stream)))
+    return y, h_final
+
+
+def kda_ssm_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softplus=True, y=None,
+                      stream=None):
+    """One token of each sequence: x, dt, z [N, dim], B, C [N, groups, state]; ``h`` f32
+    [N, dim, state] is updated in place.  Otherwise as :func:`kda_ssm_scan_fwd`.  Returns y."""
+    args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
+    N = x.shape[0]
+    y = _out(y, "y", x.shape, x.dtype, x, stream)
+    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    _check(load().kda_ssm_scan_step(*args, _dense(h, (N, dim, state), torch.float32, "h"), yp, ld_y,
+                                    N, dim, state, groups, 1 if softplus else 0, code,
+                                    _stream(stream)))
     return y

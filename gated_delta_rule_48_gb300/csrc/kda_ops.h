@@ -56,6 +56,36 @@ struct ConvArgs {
 cudaError_t launch_conv(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_conv_step(const ConvArgs& a, cudaStream_t s);
 
+// ---- kda_ssm_scan_fwd, kda_ssm_scan_step (kda_ssm.cu)
+struct SsmArgs {
+  const void* x;          // [T, dim]; the step: [N, dim], one token of each sequence
+  const void* dt;         // [T, dim]
+  const void* z;          // [T, dim] or null
+  const void* B;          // [T, groups, state]
+  const void* C;          // [T, groups, state]
+  const float* A;         // [dim, state]
+  const float* D;         // [dim] or null
+  const float* dt_bias;   // [dim] or null
+  const float* h0;        // [N, dim, state] or null; the step: h itself
+  float* h_out;           // [N, dim, state] or null
+  const int32_t* cu;      // [N + 1] or null (N sequences of T / N tokens)
+  void* y;                // [T, dim]
+  int64_t ld_x, ld_dt, ld_z, ld_b, ld_c, ld_y, T;
+  int32_t N, dim, state, groups;
+  bool bf16, softplus;
+  int sm_count;
+  int* err;
+  // prompts cut into chunks: the summaries of the chunks (null without)
+  int64_t chunk = 0, n_chunks = 1;
+  float* chunk_h = nullptr;    // [n_chunks, dim, state]
+  float* chunk_dt = nullptr;   // [n_chunks, dim]
+};
+// Tokens per chunk of a prompt's scan; `cut`: whether sequences may be cut by
+// a chunk's end, so that summaries are needed.
+void ssm_chunks(SsmArgs& a, bool& cut);
+cudaError_t launch_ssm_scan(const SsmArgs& a, bool cut, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t s);
+
 // ---- host-side state shared with the other entry points (kda_api.cu)
 kda_status device_sm_count(int* out);
 // Stream-ordered workspace from the library's pool (while `s` is being

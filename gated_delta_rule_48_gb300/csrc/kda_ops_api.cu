@@ -247,3 +247,117 @@ extern "C" kda_status kda_short_conv_step(const void* x, int64_t ld_x, const voi
   a.silu = activation != 0;
   return launched(launch_conv_step(a, static_cast<cudaStream_t>(stream)), "convolution launch");
 }
+
+// The checks that the scan's two entry points share; h_in may be h_out itself.
+static kda_status check_ssm(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt,
+                            const float* A, const void* B, int64_t ld_b, const void* C,
+                            int64_t ld_c, const float* D, const void* z, int64_t ld_z,
+                            const float* dt_bias, const float* h_in, const char* h_in_name,
+                            float* h_out, const int32_t* cu, void* y, int64_t ld_y, int64_t T,
+                            int32_t N, int32_t dim, int32_t state, int32_t groups, kda_dtype dtype,
+                            SsmArgs& a) {
+  if (T < 0 || N < 0 || dim <= 0 || state <= 0 || groups <= 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "total_tokens=%lld n_seqs=%d dim=%d state=%d groups=%d",
+               (long long)T, N, dim, state, groups);
+  if (!float_type(dtype)) return bad(KDA_ERR_INVALID_ARGUMENT, "x must be bf16 or f32");
+  if (state != 16 && state != 32 && state != 64 && state != 128)
+    return bad(KDA_ERR_UNSUPPORTED, "state=%d is not 16, 32, 64 or 128", state);
+  if (dim % groups != 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT, "dim=%d is not a multiple of groups=%d", dim, groups);
+  if (dim > (1 << 24)) return bad(KDA_ERR_UNSUPPORTED, "dim=%d exceeds %d", dim, 1 << 24);
+  if (T > 0x7fffffffLL) return bad(KDA_ERR_UNSUPPORTED, "total_tokens=%lld", (long long)T);
+  if (N == 0 && T > 0) return bad(KDA_ERR_INVALID_ARGUMENT, "tokens given but n_seqs = 0");
+  if (!cu && N > 0 && T % N != 0)
+    return bad(KDA_ERR_INVALID_ARGUMENT,
+               "cu_seqlens is NULL but total_tokens=%lld is not a multiple of n_seqs=%d",
+               (long long)T, N);
+  if (N == 0) return KDA_OK;
+  const struct { const void* p; const char* n; } req[] = {
+      {x, "x"}, {dt, "dt"}, {A, "A"}, {B, "B"}, {C, "C"}, {y, "y"}};
+  if (T > 0)
+    for (auto& r : req)
+      if (!r.p) return bad(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", r.n);
+  const int64_t es = size_of(dtype), gs = static_cast<int64_t>(groups) * state;
+  const int64_t rates = static_cast<int64_t>(dim) * state, states = rates * N;
+  const Rows in[] = {rows_of("x", x, T, ld_x, dim, es), rows_of("dt", dt, T, ld_dt, dim, es),
+                     rows_of("A", A, 1, rates, rates, 4), rows_of("B", B, T, ld_b, gs, es),
+                     rows_of("C", C, T, ld_c, gs, es), rows_of("D", D, 1, dim, dim, 4),
+                     rows_of("z", z, T, ld_z, dim, es), rows_of("dt_bias", dt_bias, 1, dim, dim, 4),
+                     rows_of(h_in_name, h_in, 1, states, states, 4),
+                     rows_of("cu_seqlens", cu, 1, N + 1LL, N + 1LL, 4)};
+  const Rows out[] = {rows_of("h_final", h_out, 1, states, states, 4), rows_of("y", y, T, ld_y, dim, es)};
+  const int64_t lds[] = {ld_x, ld_dt, rates, ld_b, ld_c, dim, ld_z, dim, states, N + 1LL, states, ld_y};
+  const int64_t cols[] = {dim, dim, rates, gs, gs, dim, dim, dim, states, N + 1LL, states, dim};
+  for (int i = 0; i < 12; ++i) {
+    const Rows& r = i < 10 ? in[i] : out[i - 10];
+    KDA_TRY(check_rows(r.name, r.p, lds[i], cols[i], cols[i] > 0 ? r.width / cols[i] : 1));
+  }
+  if (!aligned(h_in, 16) || !aligned(h_out, 16))
+    return bad(KDA_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned",
+               !aligned(h_in, 16) ? h_in_name : "h_final");
+  KDA_TRY(check_output(out[0], in, 10, &in[8]));  // the states may be continued in place
+  KDA_TRY(check_output(out[1], in, 10, nullptr));
+  KDA_TRY(check_output(out[1], &out[0], 1, nullptr));
+  a.x = x; a.dt = dt; a.z = z; a.B = B; a.C = C; a.A = A; a.D = D; a.dt_bias = dt_bias;
+  a.h0 = h_in; a.h_out = h_out; a.cu = cu; a.y = y;
+  a.ld_x = ld_x; a.ld_dt = ld_dt; a.ld_z = ld_z; a.ld_b = ld_b; a.ld_c = ld_c; a.ld_y = ld_y;
+  a.T = T; a.N = N; a.dim = dim; a.state = state; a.groups = groups;
+  a.bf16 = dtype == KDA_BF16;
+  KDA_TRY(device_sm_count(&a.sm_count));
+  return device_error_word(&a.err);
+}
+
+extern "C" kda_status kda_ssm_scan_fwd(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt,
+                                       const float* A, const void* B, int64_t ld_b, const void* C,
+                                       int64_t ld_c, const float* D, const void* z, int64_t ld_z,
+                                       const float* dt_bias, const float* h0,
+                                       const int32_t* cu_seqlens, void* y, int64_t ld_y,
+                                       float* h_final, int64_t total_tokens, int32_t n_seqs,
+                                       int32_t dim, int32_t state, int32_t groups,
+                                       int32_t dt_softplus, kda_dtype dtype, void* stream) {
+  NvtxRange nvtx_range("kda_ssm_scan_fwd");
+  SsmArgs a;
+  KDA_TRY(check_ssm(x, ld_x, dt, ld_dt, A, B, ld_b, C, ld_c, D, z, ld_z, dt_bias, h0, "h0", h_final,
+                    cu_seqlens, y, ld_y, total_tokens, n_seqs, dim, state, groups, dtype, a));
+  if (n_seqs == 0) return KDA_OK;
+  a.softplus = dt_softplus != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool cut = false;
+  ssm_chunks(a, cut);
+  if (!cut) return launched(launch_ssm_scan(a, false, s), "scan launch");
+  // Workspace: the chunks' states and step sums, and, where the states are
+  // continued in place, a copy of h0: a block that ends a sequence may write
+  // its state before the block that begins it has read the old one.
+  const int64_t row = a.dim, chunk_h = a.n_chunks * row * a.state;
+  const int64_t dts = (a.n_chunks * row + 3) / 4 * 4;
+  const int64_t copy = h0 && h0 == h_final ? static_cast<int64_t>(a.N) * row * a.state : 0;
+  void* ws = nullptr;
+  KDA_TRY(workspace_alloc(static_cast<size_t>(chunk_h + dts + copy) * sizeof(float), s, &ws));
+  a.chunk_h = static_cast<float*>(ws);
+  a.chunk_dt = a.chunk_h + chunk_h;
+  cudaError_t e = cudaSuccess;
+  if (copy) {
+    float* old = a.chunk_dt + dts;
+    e = cudaMemcpyAsync(old, h0, static_cast<size_t>(copy) * sizeof(float), cudaMemcpyDeviceToDevice, s);
+    a.h0 = old;
+  }
+  if (e == cudaSuccess) e = launch_ssm_scan(a, true, s);
+  const cudaError_t ef = cudaFreeAsync(ws, s);
+  return launched(e != cudaSuccess ? e : ef, "scan launch");
+}
+
+extern "C" kda_status kda_ssm_scan_step(const void* x, int64_t ld_x, const void* dt, int64_t ld_dt,
+                                        const float* A, const void* B, int64_t ld_b, const void* C,
+                                        int64_t ld_c, const float* D, const void* z, int64_t ld_z,
+                                        const float* dt_bias, float* h, void* y, int64_t ld_y,
+                                        int32_t n_seqs, int32_t dim, int32_t state, int32_t groups,
+                                        int32_t dt_softplus, kda_dtype dtype, void* stream) {
+  NvtxRange nvtx_range("kda_ssm_scan_step");
+  if (n_seqs > 0 && !h) return bad(KDA_ERR_INVALID_ARGUMENT, "h is NULL");
+  SsmArgs a;
+  KDA_TRY(check_ssm(x, ld_x, dt, ld_dt, A, B, ld_b, C, ld_c, D, z, ld_z, dt_bias, h, "h", h, nullptr,
+                    y, ld_y, n_seqs, n_seqs, dim, state, groups, dtype, a));
+  if (n_seqs == 0) return KDA_OK;
+  a.softplus = dt_softplus != 0;
+  return launched(launch_ssm_step(a, static_cast<cudaStream_t>(stream)), "scan step launch");
+}

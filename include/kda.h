@@ -509,6 +509,61 @@ kda_status kda_short_conv_step(const void *x, int64_t ld_x, const void *weight,
                                void *stream);
 
 /*
+ * kda_ssm_scan_fwd, kda_ssm_scan_step -- selective state space scan, for
+ * packed prompts and for one token of each sequence.
+ *
+ * Per channel d, with a state h of `state` values:
+ *     dt' = softplus(dt + dt_bias[d])    (`dt_softplus` != 0; else dt + dt_bias[d])
+ *     h   = exp(dt' A[d, :]) h + dt' x B
+ *     y   = sum(h C) + D[d] x;   with a gate z, y = y * z sigmoid(z)
+ * B and C of a token are shared by the dim / groups channels of a group
+ * (channel d is in group d / (dim / groups)).  Everything is in 32 bits; y is
+ * rounded once.
+ *
+ * Tensors (T = total_tokens, N = n_seqs; the step: one token per sequence, T = N):
+ *   x, dt, z   bf16 or f32 (`dtype`) [T, dim]    read; z may be NULL (no gate)
+ *   A          f32 [dim, state], dense           read; negative for a decay
+ *   B, C       `dtype` [T, groups, state]        read; a token's groups * state
+ *                                                values are dense, tokens
+ *                                                ld_b, ld_c elements apart
+ *   D, dt_bias f32 [dim]                         read; NULL = 0
+ *   h0         f32 [N, dim, state], 16-byte aligned  read; NULL = zeros
+ *   cu_seqlens i32 [N + 1] as in kda_chunk_fwd (checked on the GPU: a
+ *              malformed array is reported by kda_get_device_error, and y
+ *              and the states are then unspecified), or NULL
+ *   y          `dtype` [T, dim]                  written
+ *   h_final    f32 [N, dim, state], 16-byte aligned  written; NULL = not
+ *                                                produced; may be h0 itself
+ * The step reads and overwrites h ([N, dim, state]).
+ * state is 16, 32, 64 or 128, else KDA_ERR_UNSUPPORTED.  T = 0 or N = 0 are valid.
+ *
+ * Prompts with few sequences and channels are cut into chunks of tokens that
+ * run side by side; results are the same up to rounding.  That takes a
+ * workspace, allocated and freed stream-ordered on `stream`, of
+ * (state + 1) * dim * 4 bytes per chunk, and a copy of h0 where h_final is h0.
+ * The step allocates nothing.
+ */
+kda_status kda_ssm_scan_fwd(const void *x, int64_t ld_x, const void *dt,
+                            int64_t ld_dt, const float *A, const void *B,
+                            int64_t ld_b, const void *C, int64_t ld_c,
+                            const float *D, const void *z, int64_t ld_z,
+                            const float *dt_bias, const float *h0,
+                            const int32_t *cu_seqlens, void *y, int64_t ld_y,
+                            float *h_final, int64_t total_tokens,
+                            int32_t n_seqs, int32_t dim, int32_t state,
+                            int32_t groups, int32_t dt_softplus,
+                            kda_dtype dtype, void *stream);
+kda_status kda_ssm_scan_step(const void *x, int64_t ld_x, const void *dt,
+                             int64_t ld_dt, const float *A, const void *B,
+                             int64_t ld_b, const void *C, int64_t ld_c,
+                             const float *D, const void *z, int64_t ld_z,
+                             const float *dt_bias, float *h, void *y,
+                             int64_t ld_y, int32_t n_seqs, int32_t dim,
+                             int32_t state, int32_t groups,
+                             int32_t dt_softplus, kda_dtype dtype,
+                             void *stream);
+
+/*
  * kda_get_device_error -- synchronise `stream`, then return and clear the
  * device error word of the current device: KDA_OK, or KDA_ERR_DEVICE_INPUT
  * when a kernel rejected an input (kda_last_error_message() names it), or
