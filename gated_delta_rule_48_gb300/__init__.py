@@ -14,6 +14,7 @@ from .binding import (  # noqa: F401
     kda_chunk_fwd,
     kda_decode_step,
     kda_get_device_error,
+    kda_matmul_fp8,
     kda_short_conv_fwd,
     kda_short_conv_step,
     kda_ssm_scan_fwd,
@@ -23,5 +24,6 @@ from .binding import (  # noqa: F401
 )
 
 __all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_chunk_fwd",
-           "kda_decode_step", "kda_get_device_error", "kda_short_conv_fwd", "kda_short_conv_step",
-           "kda_ssm_scan_fwd", "kda_ssm_scan_step", "library_path", "load"]
+           "kda_decode_step", "kda_get_device_error", "kda_matmul_fp8", "kda_short_conv_fwd",
+           "kda_short_conv_step", "kda_ssm_scan_fwd",
+           "kda_ssm_scan_step", "library_path", "load"]

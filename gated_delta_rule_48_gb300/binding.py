@@ -200,6 +200,9 @@ def load():
             lib.kda_ssm_scan_step.restype = i
             lib.kda_ssm_scan_step.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64,
                                               vp, vp, vp, i64, i32, i32, i32, i32, i32, i, vp]
+            lib.kda_matmul_fp8.restype = i
+            lib.kda_matmul_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32,
+                                           i32, i, vp]
             lib.kda_profile_enable.restype = None
             lib.kda_profile_enable.argtypes = [ctypes.c_int]
             lib.kda_profile_read.restype = ctypes.c_int
@@ -624,6 +627,30 @@ def kda_add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, y=None, y_scal
     [..., dim] and y_scale f32 [..., ceil(dim / 128)] with y * y_scale (per 128 columns)
     standing for the normalised rows, as :func:`kda_matmul_fp8` reads them."""
     return _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, True)
+
+
+def kda_matmul_fp8(a, a_scale, b, b_scale, out=None, *, out_dtype=torch.bfloat16, stream=None):
+    """a [..., K] times the transpose of b [N, K], both float8_e4m3fn with rows on 16-byte
+    boundaries; a_scale: f32 [..., ceil(K / 128)], b_scale: f32 [ceil(N / 128), ceil(K / 128)].
+    Returns out [..., N] in ``out_dtype`` (bf16 or f32), rounded once from 32-bit sums."""
+    K, (N, k_b) = a.shape[-1], b.shape
+    if k_b != K:
+        raise KdaError(1, f"a has {K} columns and b has {k_b}")
+    blocks = (K + 127) // 128
+    ap, ld_a, _ = _rows(a, "a", _E4M3)
+    _same_shape(a_scale, (*a.shape[:-1], blocks), "a_scale")
+    _same_shape(b_scale, ((N + 127) // 128, blocks), "b_scale")
+    asp, ld_as, _ = _rows(a_scale, "a_scale", _F32)
+    bp, ld_b, _ = _rows(b, "b", _E4M3)
+    bsp, ld_bs, _ = _rows(b_scale, "b_scale", _F32)
+    M = a.numel() // max(K, 1)
+    # a single row needs no distance to a next one
+    ld_a, ld_b = (ld + -ld % 16 if rows == 1 else ld for ld, rows in ((ld_a, M), (ld_b, N)))
+    out = _out(out, "out", (*a.shape[:-1], N), out_dtype, a, stream)
+    op, ld_o, o_dt = _rows(out, "out", _FLOATS)
+    _check(load().kda_matmul_fp8(ap, ld_a, asp, ld_as, bp, ld_b, bsp, ld_bs, op, ld_o, M, N, K,
+                                 o_dt, _stream(stream)))
+    return out
 
 
 def _dense(t, shape, dtype, name):

@@ -86,6 +86,21 @@ void ssm_chunks(SsmArgs& a, bool& cut);
 cudaError_t launch_ssm_scan(const SsmArgs& a, bool cut, cudaStream_t s);
 cudaError_t launch_ssm_step(const SsmArgs& a, cudaStream_t s);
 
+// ---- kda_matmul_fp8 (kda_matmul_fp8.cu)
+struct MatmulArgs {
+  const void* a;          // e4m3 [M, K], rows on 16-byte boundaries
+  const float* a_scale;   // [M, ceil(K / 128)]
+  const void* b;          // e4m3 [N, K], rows on 16-byte boundaries
+  const float* b_scale;   // [ceil(N / 128), ceil(K / 128)]
+  void* out;              // bf16 or f32 [M, N]
+  int64_t ld_a, ld_as, ld_b, ld_bs, ld_out;
+  int32_t M, N, K;
+  bool bf16;              // out's type
+  int sm_count;
+  int* err;
+};
+cudaError_t launch_matmul_fp8(const MatmulArgs& a, cudaStream_t s);
+
 // ---- host-side state shared with the other entry points (kda_api.cu)
 kda_status device_sm_count(int* out);
 // Stream-ordered workspace from the library's pool (while `s` is being

@@ -361,3 +361,41 @@ extern "C" kda_status kda_ssm_scan_step(const void* x, int64_t ld_x, const void*
   a.softplus = dt_softplus != 0;
   return launched(launch_ssm_step(a, static_cast<cudaStream_t>(stream)), "scan step launch");
 }
+
+extern "C" kda_status kda_matmul_fp8(const void* a, int64_t ld_a, const float* a_scale,
+                                     int64_t ld_a_scale, const void* b, int64_t ld_b,
+                                     const float* b_scale, int64_t ld_b_scale, void* out,
+                                     int64_t ld_out, int32_t M, int32_t N, int32_t K,
+                                     kda_dtype out_dtype, void* stream) {
+  NvtxRange nvtx_range("kda_matmul_fp8");
+  if (M < 0 || N < 0 || K <= 0) return bad(KDA_ERR_INVALID_ARGUMENT, "M=%d N=%d K=%d", M, N, K);
+  if (!float_type(out_dtype)) return bad(KDA_ERR_INVALID_ARGUMENT, "out must be bf16 or f32");
+  if (M == 0 || N == 0) return KDA_OK;
+  const struct { const void* p; const char* n; } req[] = {
+      {a, "a"}, {a_scale, "a_scale"}, {b, "b"}, {b_scale, "b_scale"}, {out, "out"}};
+  for (auto& r : req)
+    if (!r.p) return bad(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", r.n);
+  const int64_t kb = (K + kScaleGroup - 1) / kScaleGroup, nb = (N + kScaleGroup - 1) / kScaleGroup;
+  const int64_t os = size_of(out_dtype);
+  KDA_TRY(check_rows("a", a, ld_a, K, 1));
+  KDA_TRY(check_rows("a_scale", a_scale, ld_a_scale, kb, 4));
+  KDA_TRY(check_rows("b", b, ld_b, K, 1));
+  KDA_TRY(check_rows("b_scale", b_scale, ld_b_scale, kb, 4));
+  KDA_TRY(check_rows("out", out, ld_out, N, os));
+  const struct { const void* p; int64_t ld; const char* n; } wide[] = {{a, ld_a, "a"}, {b, ld_b, "b"}};
+  for (auto& w : wide)  // the tensor copies' rule
+    if (!aligned(w.p, 16) || w.ld % 16 != 0)
+      return bad(KDA_ERR_INVALID_ARGUMENT, "%s: every row must start on a 16-byte boundary", w.n);
+  const Rows in[] = {rows_of("a", a, M, ld_a, K, 1), rows_of("a_scale", a_scale, M, ld_a_scale, kb, 4),
+                     rows_of("b", b, N, ld_b, K, 1),
+                     rows_of("b_scale", b_scale, nb, ld_b_scale, kb, 4)};
+  KDA_TRY(check_output(rows_of("out", out, M, ld_out, N, os), in, 4, nullptr));
+  MatmulArgs m;
+  m.a = a; m.a_scale = a_scale; m.b = b; m.b_scale = b_scale; m.out = out;
+  m.ld_a = ld_a; m.ld_as = ld_a_scale; m.ld_b = ld_b; m.ld_bs = ld_b_scale; m.ld_out = ld_out;
+  m.M = M; m.N = N; m.K = K;
+  m.bf16 = out_dtype == KDA_BF16;
+  KDA_TRY(device_sm_count(&m.sm_count));
+  KDA_TRY(device_error_word(&m.err));
+  return launched(launch_matmul_fp8(m, static_cast<cudaStream_t>(stream)), "product launch");
+}

@@ -468,6 +468,30 @@ kda_status kda_add_rms_norm(const void *x, int64_t ld_x, const void *residual,
                             kda_dtype y_dtype, void *stream);
 
 /*
+ * kda_matmul_fp8 -- the product of 8-bit rows with 8-bit weights, with a scale
+ * for each row and 128 columns of A and each 128 x 128 block of B (a
+ * projection of what kda_add_rms_norm writes):
+ *
+ *     out[m, n] = sum over k-blocks b of
+ *                 a_scale[m, b] * b_scale[n / 128, b] * sum_{k in b} a[m, k] b[n, k]
+ *
+ * Each block's sum and the sum over blocks are in 32 bits; out is rounded once.
+ *
+ * Tensors:
+ *   a        e4m3 [M, K]   read; every row on a 16-byte boundary
+ *   a_scale  f32  [M, ceil(K / 128)]              read
+ *   b        e4m3 [N, K]   read; every row on a 16-byte boundary
+ *   b_scale  f32  [ceil(N / 128), ceil(K / 128)]  read
+ *   out      bf16 or f32 (`out_dtype`) [M, N]     written
+ * M = 0 or N = 0 is a no-op; K >= 1.  Allocates nothing.
+ */
+kda_status kda_matmul_fp8(const void *a, int64_t ld_a, const float *a_scale,
+                          int64_t ld_a_scale, const void *b, int64_t ld_b,
+                          const float *b_scale, int64_t ld_b_scale, void *out,
+                          int64_t ld_out, int32_t M, int32_t N, int32_t K,
+                          kda_dtype out_dtype, void *stream);
+
+/*
  * kda_short_conv_fwd, kda_short_conv_step -- a short causal convolution per
  * channel, for packed prompts and for one token of each sequence.
  *
