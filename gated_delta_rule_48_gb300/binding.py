@@ -130,6 +130,9 @@ class _KernelTime(ctypes.Structure):
 
 def load():
     """Load (building first if needed) the library; returns the ctypes handle."""
+    lib = _libs.get(_checked)
+    if lib is not None:
+        return lib
     with _lock:
         if _checked not in _libs:
             path = library_path()
@@ -533,28 +536,29 @@ def _rows(t, name, dtypes):
     with more leading dimensions that are one row stride apart."""
     if t is None:
         return None, 0, 0
+    dtype = t.dtype
     if not t.is_cuda:
         raise KdaError(1, f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise KdaError(1, f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    d = t.dim()
+    if dtype not in dtypes:
+        raise KdaError(1, f"{name} must be {' or '.join(map(str, dtypes))}, got {dtype}")
+    shape, stride = t.shape, t.stride()
+    d = len(stride)
     if d < 2:
         raise KdaError(1, f"{name} must have at least 2 dimensions")
-    shape, stride = t.shape, t.stride()
     cols = shape[-1]
     if stride[-1] != 1 and cols > 1:
         raise KdaError(1, f"{name}: the last dimension must be contiguous")
-    ld = stride[-2] if shape[-2] > 1 else (stride[-3] if d > 2 and shape[-3] > 1 else max(cols, 1))
     rows = shape[-2]
+    ld = stride[-2] if rows > 1 else stride[-3] if d > 2 and shape[-3] > 1 else max(cols, 1)
     for k in range(d - 3, -1, -1):
         if shape[k] > 1 and stride[k] != ld * rows:
             raise KdaError(1, f"{name}: the leading dimensions must be one row stride apart")
         rows *= shape[k]
-    return t.data_ptr(), ld, KDA_DTYPE[t.dtype]
+    return t.data_ptr(), ld, KDA_DTYPE[dtype]
 
 
 def _same_shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise KdaError(1, f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -569,13 +573,20 @@ def _out(given, name, shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _handle(stream, like):
+    """The stream's handle; without one, that of the current stream (of the inputs' device)."""
+    if stream is None:  # the handle alone: a Stream object takes longer than a small launch
+        return torch._C._cuda_getCurrentRawStream(like.device.index)
+    return stream.cuda_stream
+
+
 def _vector(t, n, name):
     """(address, dtype code) of a contiguous bf16 or f32 vector of n elements, or of None."""
     if t is None:
         return None, 1
     if not t.is_cuda or t.dtype not in _FLOATS:
         raise KdaError(1, f"{name} must be a bfloat16 or float32 CUDA tensor")
-    if t.shape != (n,) or not t.is_contiguous():
+    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
         raise KdaError(1, f"{name} must be a contiguous vector of {n} elements")
     return t.data_ptr(), KDA_DTYPE[t.dtype]
 
@@ -598,15 +609,16 @@ def _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, quant):
     sp, ld_s = None, 0
     if quant:
         if y is None:  # rows at multiples of 16 bytes, as kda_matmul_fp8 reads them
-            y = _out(None, "y", (rows, dim + -dim % 16), _E4M3[0], x, stream)[:, :dim]
-            y = y.unflatten(0, shape[:-1]) if len(shape) > 2 else y
+            pad = -dim % 16
+            y = _out(None, "y", (*shape[:-1], dim + pad), _E4M3[0], x, stream)
+            y = y[..., :dim] if pad else y
         y_scale = _out(y_scale, "y_scale", (*shape[:-1], (dim + 127) // 128), torch.float32, x,
                        stream)
         sp, ld_s, _ = _rows(y_scale, "y_scale", _F32)
     y = _out(y, "y", shape, x.dtype, x, stream)
     yp, ld_y, y_dt = _rows(y, "y", _E4M3 if quant else (x.dtype,))
     _check(load().kda_add_rms_norm(xp, ld_x, rp, ld_r, wp, hp, ld_h, yp, ld_y, sp, ld_s, rows, dim,
-                                   eps, dt, w_dt, y_dt, _stream(stream)))
+                                   eps, dt, w_dt, y_dt, _handle(stream, x)))
     return y, y_scale, h
 
 
@@ -649,7 +661,7 @@ def kda_matmul_fp8(a, a_scale, b, b_scale, out=None, *, out_dtype=torch.bfloat16
     out = _out(out, "out", (*a.shape[:-1], N), out_dtype, a, stream)
     op, ld_o, o_dt = _rows(out, "out", _FLOATS)
     _check(load().kda_matmul_fp8(ap, ld_a, asp, ld_as, bp, ld_b, bsp, ld_bs, op, ld_o, M, N, K,
-                                 o_dt, _stream(stream)))
+                                 o_dt, _handle(stream, a)))
     return out
 
 
@@ -702,7 +714,7 @@ def kda_short_conv_fwd(x, weight, bias=None, conv_state=None, cu_seqlens=None, *
     _check(load().kda_short_conv_fwd(xp, ld_x, wp, bp, _dense(conv_state, shape, x.dtype, "conv_state"),
                                      _dense(state_out, shape, x.dtype, "state_out"), cu, yp, ld_y,
                                      T, N, x.shape[-1], width, 1 if silu else 0, dt, w_dt,
-                                     _stream(stream)))
+                                     _handle(stream, x)))
     return y, state_out
 
 
@@ -717,7 +729,7 @@ def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, 
     _check(load().kda_short_conv_step(xp, ld_x, wp, bp,
                                       _dense(conv_state, (N, width - 1, dim), x.dtype, "conv_state"),
                                       yp, ld_y, N, dim, width, 1 if silu else 0, dt, w_dt,
-                                      _stream(stream)))
+                                      _handle(stream, x)))
     return y
 
 
@@ -769,7 +781,7 @@ def kda_ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_s
         h_final = _out(h_final, "h_final", shape, torch.float32, x, stream)
     _check(load().kda_ssm_scan_fwd(*args, _dense(h0, shape, torch.float32, "h0"), cu, yp, ld_y,
                                    _dense(h_final, shape, torch.float32, "h_final"), T, N, dim,
-                                   state, groups, 1 if softplus else 0, code, _stream(stream)))
+                                   state, groups, 1 if softplus else 0, code, _handle(stream, x)))
     return y, h_final
 
 
@@ -783,5 +795,5 @@ def kda_ssm_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softpl
     yp, ld_y, _ = _rows(y, "y", (x.dtype,))
     _check(load().kda_ssm_scan_step(*args, _dense(h, (N, dim, state), torch.float32, "h"), yp, ld_y,
                                     N, dim, state, groups, 1 if softplus else 0, code,
-                                    _stream(stream)))
+                                    _handle(stream, x)))
     return y

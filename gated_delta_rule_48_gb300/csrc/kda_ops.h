@@ -73,6 +73,8 @@ struct SsmArgs {
   int64_t ld_x, ld_dt, ld_z, ld_b, ld_c, ld_y, T;
   int32_t N, dim, state, groups;
   bool bf16, softplus;
+  bool vec;               // A, B and C can be read four values at a time
+  bool pairs;             // so, and x, dt, z and y can be read and written two channels at a time
   int sm_count;
   int* err;
   // prompts cut into chunks: the summaries of the chunks (null without)
@@ -225,6 +227,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+
+// Four consecutive elements, aligned to their total size.
+__device__ __forceinline__ void load4(const Bf16* p, float (&v)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(u.x << 16);
+  v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16);
+  v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) { load_n<4>(p, v); }
 
 // Two values to e4m3, round to nearest even, clamped to +-448 (NaN stays NaN).
 __device__ __forceinline__ uint16_t pack2_e4m3(float lo, float hi) {

@@ -303,6 +303,12 @@ static kda_status check_ssm(const void* x, int64_t ld_x, const void* dt, int64_t
   a.ld_x = ld_x; a.ld_dt = ld_dt; a.ld_z = ld_z; a.ld_b = ld_b; a.ld_c = ld_c; a.ld_y = ld_y;
   a.T = T; a.N = N; a.dim = dim; a.state = state; a.groups = groups;
   a.bf16 = dtype == KDA_BF16;
+  a.vec = aligned(A, 16) && aligned(B, static_cast<uintptr_t>(4 * es)) && ld_b % 4 == 0 &&
+          aligned(C, static_cast<uintptr_t>(4 * es)) && ld_c % 4 == 0;
+  auto even = [&](const void* p, int64_t ld) {
+    return !p || (aligned(p, static_cast<uintptr_t>(2 * es)) && ld % 2 == 0);
+  };
+  a.pairs = a.vec && dim / groups % 2 == 0 && even(x, ld_x) && even(dt, ld_dt) && even(z, ld_z) && even(y, ld_y);
   KDA_TRY(device_sm_count(&a.sm_count));
   return device_error_word(&a.err);
 }

@@ -12,15 +12,21 @@
 // Everything is in 32 bits; exp(dt' A) is 2^(dt' (A log2 e)) by the hardware's
 // approximate exponential.
 //
-// Bound: instruction issue and the exponentials (one per token, channel and
-// state value, against 8 bytes per token and channel), then HBM.  Four lanes
-// share a channel, a quarter of its state each, and take four tokens at a
-// time: the work that a token needs once (softplus, gate, loads, the store)
-// is done by the lane whose number is the token's, and handed round by
-// shuffles, so nothing is computed four times.  The state's recurrence and the
-// read-out run on pairs of 32-bit values in one instruction.  B and C come
-// from shared memory, converted once per block; the next tile of tokens is
-// fetched into registers while one is computed.
+// Bound: instruction issue (per token, channel and state value one exponential
+// and four multiply-adds, against 8 bytes per token and channel).  Four lanes
+// share two neighbouring channels, a quarter of their states each, and take a
+// tile of tokens at a time.  What a token needs once (softplus, gate, loads,
+// the store) is done by the lane whose number is the token's, and (dt', dt' x)
+// handed round through shared memory, so nothing is computed four times; B and
+// C are converted once per block, and a lane's read of them serves both
+// channels (with one channel per lane the reads bound the kernel, and it was
+// 15 % slower).  The recurrence runs on pairs of 32-bit values in one
+// instruction (12 % faster than single ones), and a token's decays are
+// computed three tokens ahead of its turn.  Three tiles are under way: one in
+// the recurrence, one staged beside it, one in flight to registers.
+//
+// 16,384 tokens x 4096 channels x 16 states, bf16 with gate: 0.42 ms (1.3 TB/s
+// of inputs and outputs); the tokens' own work is a third of the instructions.
 //
 // Prompts are cut into chunks of the packed axis, whatever the sequences'
 // lengths, so that blocks are equally long.  A sequence cut by a chunk's end
@@ -41,7 +47,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLanes = 4;            // lanes per channel, and tokens taken together
 constexpr int kScanThreads = 128;
-constexpr int kScanChannels = kScanThreads / kLanes;
+// Channels per lane: each value of B and C read from shared memory serves them
+// all.  (At 128 states two channels' states do not fit in registers.)
+constexpr int kChannelsOf(int state) { return state <= 64 ? 2 : 1; }
+// Blocks per SM that the registers are divided among.
+constexpr int scan_blocks_per_sm(int state) { return state <= 16 ? 3 : 2; }
 
 // ---- pairs of 32-bit values
 typedef unsigned long long f32x2;
@@ -74,82 +84,213 @@ __device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
   return pack2(ex2(lo), ex2(hi));
 }
 
-// log(1 + e^v)
-__device__ __forceinline__ float softplus(float v) {
-  return fmaxf(v, 0.0f) + log1pf(__expf(-fabsf(v)));
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// Where state value s of a channel lives: lane (s / 4) % 4, its piece s / 16.
-template <int S>
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1].  With
+// s = e / (2 + e) <= 1/3, log(1 + e) = 2 artanh(s) = 2 (s + s^3/3 + s^5/5 + ...)
+// (Gregory's series); the first term left out, 2 s^15/15, is below 1e-8.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = ex2(-fabsf(v) * kLog2e);
+  const float s = e * rcp(2.0f + e), q = s * s;
+  float p = fmaf(q, 2.0f / 13.0f, 2.0f / 11.0f);
+  p = fmaf(q, p, 2.0f / 9.0f);
+  p = fmaf(q, p, 2.0f / 7.0f);
+  p = fmaf(q, p, 2.0f / 5.0f);
+  p = fmaf(q, p, 2.0f / 3.0f);
+  return fmaxf(v, 0.0f) + fmaf(s * q, p, s + s);
+}
+// v sigmoid(v)
+__device__ __forceinline__ float gate(float v) { return v * rcp(1.0f + ex2(v * -kLog2e)); }
+
+// Four values of B (and of C behind them) from shared memory.
+template <bool BOTH>
+__device__ __forceinline__ void row_values(const float* p, f32x2* b, f32x2* c) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  b[0] = v.x;
+  b[1] = v.y;
+  if constexpr (BOTH) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p + 4);
+    c[0] = w.x;
+    c[1] = w.y;
+  }
+}
+
+// The states of a lane's NC channels (c, c + 1, ...).  Value s of a channel is
+// in lane (s / 4) % 4, its piece s / 16.
+template <int S, int NC>
 struct State {
-  static constexpr int kQuads = S / (4 * kLanes);  // groups of four values per lane
-  f32x2 h[2 * kQuads], a[2 * kQuads];              // the state, and A log2 e
+  static constexpr int kPairs = S / (2 * kLanes);  // pairs of values per lane and channel
+  f32x2 h[NC][kPairs], a[NC][kPairs];              // the states, and A log2 e
 
   __device__ __forceinline__ static int64_t at(int lane4, int q) { return 16 * q + 4 * lane4; }
 
-  // `live`: the channel exists
+  // `live`: how many of the channels exist
   __device__ __forceinline__ void load_rates(const float* A, int64_t c, int64_t dim, int lane4,
-                                             bool live, int* err) {
+                                             int live, int* err) {
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int64_t e = c * S + at(lane4, q);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live && kda_guard(e, 4, dim * S, err)) v = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
-      a[2 * q] = pack2(v.x * kLog2e, v.y * kLog2e);
-      a[2 * q + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
-    }
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < kPairs / 2; ++q) {
+        const int64_t e = (c + k) * S + at(lane4, q);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < live && kda_guard(e, 4, dim * S, err)) v = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
+        a[k][2 * q] = pack2(v.x * kLog2e, v.y * kLog2e);
+        a[k][2 * q + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
+      }
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 2 * kQuads; ++i) h[i] = 0;
-  }
-  // row: the channel's row of a [rows, S] buffer (dense, 16-byte aligned)
-  __device__ __forceinline__ void load(const float* p, int64_t row, int64_t rows, int lane4,
-                                       bool live, int* err) {
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int64_t e = row * S + at(lane4, q);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p && live && kda_guard(e, 4, rows * S, err)) v = *reinterpret_cast<const float4*>(p + e);
-      h[2 * q] = pack2(v.x, v.y);
-      h[2 * q + 1] = pack2(v.z, v.w);
-    }
+      for (int i = 0; i < kPairs; ++i) h[k][i] = 0;
   }
-  __device__ __forceinline__ void store(float* p, int64_t row, int64_t rows, int lane4, bool live,
+  // row: the first channel's row of a [rows, S] buffer (dense, 16-byte aligned)
+  __device__ __forceinline__ void load(const float* p, int64_t row, int64_t rows, int lane4, int live,
+                                       int* err) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < kPairs / 2; ++q) {
+        const int64_t e = (row + k) * S + at(lane4, q);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p && k < live && kda_guard(e, 4, rows * S, err)) v = *reinterpret_cast<const float4*>(p + e);
+        h[k][2 * q] = pack2(v.x, v.y);
+        h[k][2 * q + 1] = pack2(v.z, v.w);
+      }
+  }
+  __device__ __forceinline__ void store(float* p, int64_t row, int64_t rows, int lane4, int live,
                                         int* err) const {
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int64_t e = row * S + at(lane4, q);
-      float4 v;
-      unpack2(h[2 * q], v.x, v.y);
-      unpack2(h[2 * q + 1], v.z, v.w);
-      if (live && kda_guard(e, 4, rows * S, err)) *reinterpret_cast<float4*>(p + e) = v;
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int q = 0; q < kPairs / 2; ++q) {
+        const int64_t e = (row + k) * S + at(lane4, q);
+        float4 v;
+        unpack2(h[k][2 * q], v.x, v.y);
+        unpack2(h[k][2 * q + 1], v.z, v.w);
+        if (k < live && kda_guard(e, 4, rows * S, err)) *reinterpret_cast<float4*>(p + e) = v;
+      }
+  }
+  // h = exp(sum A) h + later's h: one chunk's map applied
+  __device__ __forceinline__ void chain(const float (&sum)[NC], const State& later) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        h[k][i] = fma2(ex2_2(mul2(pack2(sum[k], sum[k]), a[k][i])), h[k][i], later.h[k][i]);
+  }
+  // What a token adds to the recurrence, all of it independent of the state:
+  // exp(dt A), u B, and the token's C.
+  struct Terms {
+    f32x2 decay[NC][kPairs], add[NC][kPairs], c[kPairs];
+  };
+  // row: the token's B and C in shared memory, four of B then four of C for each
+  // four state values (without READ, B alone); du: (dt, u) of the lane's channels
+  template <typename T, bool READ>
+  __device__ __forceinline__ void terms(const T* row, const float* du, int lane4, Terms& t) const {
+    float d[NC], u[NC];
+    if constexpr (NC == 2) {
+      const float4 v = *reinterpret_cast<const float4*>(du);
+      d[0] = v.x; u[0] = v.y; d[1] = v.z; u[1] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(du);
+      d[0] = v.x; u[0] = v.y;
+    }
+#pragma unroll
+    for (int q = 0; q < kPairs / 2; ++q) {
+      f32x2 b[2];
+      row_values<READ>(row + (READ ? 2 : 1) * at(lane4, q), b, t.c + 2 * q);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const f32x2 dd = pack2(d[k], d[k]), uu = pack2(u[k], u[k]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          t.decay[k][2 * q + i] = ex2_2(mul2(dd, a[k][2 * q + i]));
+          t.add[k][2 * q + i] = mul2(uu, b[i]);
+        }
+      }
     }
   }
-  // h = exp(dt A) h + u B, B the token's row in shared memory
-  __device__ __forceinline__ void step(float dt, float u, const float* B, int lane4) {
-    const f32x2 dd = pack2(dt, dt), uu = pack2(u, u);
+  // h = exp(dt A) h + u B; part[k]: this lane's part of sum(h C)
+  template <bool READ>
+  __device__ __forceinline__ void advance(const Terms& t, float (&part)[NC]) {
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(B + at(lane4, q));
-      h[2 * q] = fma2(ex2_2(mul2(dd, a[2 * q])), h[2 * q], mul2(uu, b.x));
-      h[2 * q + 1] = fma2(ex2_2(mul2(dd, a[2 * q + 1])), h[2 * q + 1], mul2(uu, b.y));
-    }
-  }
-  // this lane's part of sum(h C)
-  __device__ __forceinline__ float read(const float* C, int lane4) const {
-    f32x2 acc = 0;
+    for (int k = 0; k < NC; ++k) {
+      f32x2 acc = 0;
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(C + at(lane4, q));
-      acc = fma2(h[2 * q], c.x, acc);
-      acc = fma2(h[2 * q + 1], c.y, acc);
+      for (int i = 0; i < kPairs; ++i) {
+        h[k][i] = fma2(t.decay[k][i], h[k][i], t.add[k][i]);
+        if (READ) acc = i ? fma2(h[k][i], t.c[i], acc) : mul2(h[k][i], t.c[i]);
+      }
+      if (READ) {
+        float lo, hi;
+        unpack2(acc, lo, hi);
+        part[k] = lo + hi;
+      }
     }
-    float lo, hi;
-    unpack2(acc, lo, hi);
-    return lo + hi;
   }
 };
+
+// NC consecutive elements in the registers they were loaded into.  Two bf16
+// values that came in one load stay in one register until they are used:
+// taking them apart would wait for the load.
+template <typename T, int NC, bool WIDE>
+struct Raw {
+  T v[NC];
+  __device__ __forceinline__ float get(int k) const { return to_f32(v[k]); }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) v[k] = p[k];
+  }
+};
+template <>
+struct Raw<Bf16, 2, true> {
+  uint32_t w;
+  __device__ __forceinline__ float get(int k) const {
+    return __uint_as_float(k ? w & 0xffff0000u : w << 16);
+  }
+  __device__ __forceinline__ void load(const Bf16* p) { w = *reinterpret_cast<const uint32_t*>(p); }
+};
+template <>
+struct Raw<float, 2, true> {
+  float2 w;
+  __device__ __forceinline__ float get(int k) const { return k ? w.y : w.x; }
+  __device__ __forceinline__ void load(const float* p) { w = *reinterpret_cast<const float2*>(p); }
+};
+// N consecutive elements (1, or 4 aligned to their size) on their way from
+// global to shared memory.
+template <typename T, int N>
+struct Four {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void store(float* p) const { *p = to_f32(v); }
+};
+template <>
+struct Four<Bf16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const Bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) =
+        make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                    __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+};
+template <>
+struct Four<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
+};
+__device__ __forceinline__ void store_pair(Bf16* p, float lo, float hi) {
+  *reinterpret_cast<uint32_t*>(p) = pack2_bf16(lo, hi);
+}
+__device__ __forceinline__ void store_pair(float* p, float lo, float hi) {
+  *reinterpret_cast<float2*>(p) = make_float2(lo, hi);
+}
 
 // One element of a [T, dim] tensor, or 0 past the end.
 template <typename T>
@@ -161,128 +302,247 @@ __device__ __forceinline__ float element(const void* p, int64_t t, int64_t ld, i
 }
 
 // Sum over the four lanes of a channel, for four tokens at once: lane j ends
-// with the sum of v[j].
-__device__ __forceinline__ float sum_to_own(const float (&v)[4], int lane4) {
+// with the sum of token j's parts.
+__device__ __forceinline__ float sum_to_own(float v0, float v1, float v2, float v3, int lane4) {
   const bool odd = lane4 & 1, high = lane4 & 2;
-  float lo = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-  float hi = (odd ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[3], 1);
+  float lo = (odd ? v1 : v0) + __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  float hi = (odd ? v3 : v2) + __shfl_xor_sync(0xffffffffu, odd ? v2 : v3, 1);
   return (high ? hi : lo) + __shfl_xor_sync(0xffffffffu, high ? lo : hi, 2);
 }
 
 // SUMMARY: the piece's final state from zero (or the sequence's start) and its
 // sum of step sizes; otherwise outputs and final states.
-template <typename T, int S, bool SUMMARY>
+// WIDE: a lane's channels come in one load.
+template <typename T, int S, bool SUMMARY, bool WIDE>
 struct Scan {
+  static constexpr int NC = kChannelsOf(S);
   static constexpr int kTile = S <= 32 ? 16 : 8;       // tokens per tile
   static constexpr int kBatches = kTile / kLanes;
   static constexpr int kRow = (SUMMARY ? 1 : 2) * S;   // B (and C) of a token in shared memory
-  static constexpr int kLoads = kTile * kRow / kScanThreads;
-  static_assert(kTile * kRow % kScanThreads == 0, "whole loads");
+  // fetching B and C: `kUnit` values at a time (WIDE: four), units of a tile
+  // dealt to the threads
+  static constexpr int kUnit = WIDE ? 4 : 1;
+  static constexpr int kUnits = kTile * kRow / kUnit;
+  static constexpr int kLoads = (kUnits + kScanThreads - 1) / kScanThreads;
+  using Unit = Four<T, kUnit>;
+  // (dt, u) of the block's channels for a token, in floats; 32 bytes more, so
+  // that the four tokens that a channel's lanes write fall in different banks
+  static constexpr int kDuRow = 2 * NC * (kScanThreads / kLanes) + 8;
+  static constexpr int kBcBytes = kTile * kRow * 4;
+  static constexpr int kBufBytes = kBcBytes + kTile * kDuRow * 4;
+  using Pair = Raw<T, NC, WIDE>;
 
   const SsmArgs& a;
-  float* smem;  // [2][kTile][kRow]
-  int64_t c;    // channel
-  int lane4, group;
-  bool live;
-  float bias, skip;
-  State<S> st;
-  float sum_dt = 0.f;
-  float nx[kBatches], ndt[kBatches], nz[kBatches], nbc[kLoads];  // the next tile
+  unsigned char* smem;  // two buffers of kTile rows of B and C, then kTile rows of (dt, u)
+  int64_t c;    // first channel
+  int lane4, group, live;  // live: how many of the lane's channels exist
+  float bias[NC], skip[NC], sum_dt[NC];
+  State<S, NC> st;
+  // the next tile, as loaded (converting here would wait for the loads)
+  Pair nx[kBatches], ndt[kBatches], nz[kBatches];
+  Unit nbc[kLoads];
+  float ny[kBatches][NC], ng[kBatches][NC];  // D x and the gate of the tile staged last
+  T* py;                    // this lane's token of the tile
+  const T *px, *pdt, *pz;   // of this lane's first token of the next tile
+  int64_t t_bc;             // first token of the next tile
 
-  __device__ __forceinline__ void fetch(int64_t t, int64_t t1) {
+  __device__ __forceinline__ Pair get(const T* p, const void* base, int64_t ld, bool in) const {
+    Pair r{};
+    const int64_t e = p - static_cast<const T*>(base), extent = (a.T - 1) * ld + a.dim;
+    if constexpr (WIDE || NC == 1) {
+      if (in && live == NC && kda_guard(e, NC, extent, a.err)) r.load(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        if (in && k < live && kda_guard(e + k, 1, extent, a.err)) r.v[k] = p[k];
+    }
+    return r;
+  }
+
+  // The `n` tokens left from the pointers on, at most a tile of them.
+  __device__ __forceinline__ void fetch(int64_t n) {
+    const int left = static_cast<int>(min(n, static_cast<int64_t>(kTile)));
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) {
-      const int64_t own = t + kLanes * b + lane4;
-      const bool in = live && own < t1;
-      nx[b] = element<T>(a.x, own, a.ld_x, c, in, a);
-      ndt[b] = element<T>(a.dt, own, a.ld_dt, c, in, a);
-      if (!SUMMARY) nz[b] = a.z ? element<T>(a.z, own, a.ld_z, c, in, a) : 0.f;
+      const bool in = kLanes * b + lane4 < left;
+      nx[b] = get(px + b * kLanes * a.ld_x, a.x, a.ld_x, in);
+      ndt[b] = get(pdt + b * kLanes * a.ld_dt, a.dt, a.ld_dt, in);
+      if (!SUMMARY) nz[b] = get(pz + b * kLanes * a.ld_z, a.z, a.ld_z, in && a.z);
+    }
+    px += kTile * a.ld_x;
+    pdt += kTile * a.ld_dt;
+    pz += kTile * a.ld_z;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = (i * kScanThreads + static_cast<int>(threadIdx.x)) * kUnit, row = e / kRow;
+      const int s = e % kRow;
+      const bool is_b = SUMMARY || s < S;
+      const int64_t ld = is_b ? a.ld_b : a.ld_c;
+      const int64_t at = (t_bc + row) * ld + static_cast<int64_t>(group) * S + (is_b ? s : s - S);
+      Unit v{};
+      if (row < left &&
+          kda_guard(at, kUnit, (a.T - 1) * ld + static_cast<int64_t>(a.groups) * S, a.err))
+        v.load(static_cast<const T*>(is_b ? a.B : a.C) + at);
+      nbc[i] = v;
+    }
+    t_bc += kTile;
+  }
+
+  __device__ __forceinline__ void point(int64_t t) {
+    px = static_cast<const T*>(a.x) + (t + lane4) * a.ld_x + c;
+    pdt = static_cast<const T*>(a.dt) + (t + lane4) * a.ld_dt + c;
+    pz = static_cast<const T*>(a.z) + (t + lane4) * a.ld_z + c;
+    py = static_cast<T*>(a.y) + (t + lane4) * a.ld_y + c;
+    t_bc = t;
+  }
+
+  // What the fetched tile's `n` tokens need once: dt and u into shared memory,
+  // D x and the gate into registers; B and C into shared memory.
+  __device__ __forceinline__ void stage(unsigned char* buf, int n) {
+    float* du = reinterpret_cast<float*>(buf + kBcBytes) + 2 * NC * (threadIdx.x / kLanes);
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) {
+      float d[NC], u[NC];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        d[k] = ndt[b].get(k) + bias[k];
+        if (a.softplus) d[k] = softplus(d[k]);
+        const float x = nx[b].get(k);
+        u[k] = d[k] * x;
+        if (SUMMARY) {
+          if (kLanes * b + lane4 < n) sum_dt[k] += d[k];
+        } else {
+          ny[b][k] = skip[k] * x;
+          ng[b][k] = a.z ? gate(nz[b].get(k)) : 1.0f;
+        }
+      }
+      float* to = du + (kLanes * b + lane4) * kDuRow;
+      if constexpr (NC == 2) *reinterpret_cast<float4*>(to) = make_float4(d[0], u[0], d[1], u[1]);
+      else *reinterpret_cast<float2*>(to) = make_float2(d[0], u[0]);
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int e = i * kScanThreads + threadIdx.x, s = e % kRow;
-      const int64_t own = t + e / kRow;
-      const bool is_b = SUMMARY || s < S;
-      const int64_t ld = is_b ? a.ld_b : a.ld_c;
-      const int64_t at = own * ld + static_cast<int64_t>(group) * S + (is_b ? s : s - S);
-      const T* p = static_cast<const T*>(is_b ? a.B : a.C);
-      nbc[i] = own < t1 && kda_guard(at, 1, (a.T - 1) * ld + static_cast<int64_t>(a.groups) * S, a.err)
-                   ? to_f32(p[at]) : 0.f;
+      const int e = (i * kScanThreads + static_cast<int>(threadIdx.x)) * kUnit, s = e % kRow;
+      // B's value s at (s / 4) * 8 + s % 4, C's four places behind
+      const int at = SUMMARY ? s : s < S ? s / 4 * 8 + s % 4 : (s - S) / 4 * 8 + 4 + s % 4;
+      if (kUnits % kScanThreads == 0 || e < kTile * kRow)
+        nbc[i].store(reinterpret_cast<float*>(buf) + e / kRow * kRow + at);
     }
   }
 
+  // The recurrence over a staged tile; FULL: all of its tokens exist.
+  template <bool FULL>
+  __device__ __forceinline__ void tile(const unsigned char* buf, int n, float (&y)[kBatches][NC],
+                                       const float (&g)[kBatches][NC]) {
+    constexpr int kAhead = S == 16 ? 3 : 1;  // tokens whose decays are ready before their turn
+    const float* bc = reinterpret_cast<const float*>(buf);
+    const float* du = reinterpret_cast<const float*>(buf + kBcBytes) + 2 * NC * (threadIdx.x / kLanes);
+    float part[kTile][NC];
+    typename State<S, NC>::Terms terms[kAhead + 1];
+    if (FULL) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        st.template terms<float, !SUMMARY>(bc + j * kRow, du + j * kDuRow, lane4, terms[j]);
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        if (j + kAhead < kTile)
+          st.template terms<float, !SUMMARY>(bc + (j + kAhead) * kRow, du + (j + kAhead) * kDuRow, lane4,
+                                         terms[(j + kAhead) % (kAhead + 1)]);
+        st.template advance<!SUMMARY>(terms[j % (kAhead + 1)], part[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) part[j][k] = 0.f;
+        if (j < n) {
+          st.template terms<float, !SUMMARY>(bc + j * kRow, du + j * kDuRow, lane4, terms[0]);
+          st.template advance<!SUMMARY>(terms[0], part[j]);
+        }
+      }
+    }
+    if (SUMMARY) return;
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b)
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        y[b][k] = (y[b][k] + sum_to_own(part[4 * b][k], part[4 * b + 1][k], part[4 * b + 2][k],
+                                        part[4 * b + 3][k], lane4)) * g[b][k];
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) {
+      if (!FULL && kLanes * b + lane4 >= n) break;
+      T* p = py + b * kLanes * a.ld_y;
+      const int64_t e = p - static_cast<T*>(a.y), extent = (a.T - 1) * a.ld_y + a.dim;
+      if constexpr (WIDE && NC == 2) {
+        if (live == NC && kda_guard(e, NC, extent, a.err)) store_pair(p, y[b][0], y[b][1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+          if (k < live && kda_guard(e + k, 1, extent, a.err)) p[k] = from_f32<T>(y[b][k]);
+      }
+    }
+    py += kTile * a.ld_y;
+  }
+
   // Tokens [t, t1) of one sequence, st carried along.  Called by every thread
-  // of the block with the same t, t1.
+  // of the block with the same t, t1.  Three tiles are under way: one in the
+  // recurrence, the next one staged beside it, the one after in flight.
   __device__ __forceinline__ void run(int64_t t, int64_t t1) {
-    fetch(t, t1);
+    auto left = [&](int64_t from) { return static_cast<int>(min(t1 - from, static_cast<int64_t>(kTile))); };
+    point(t);
+    fetch(t1 - t);
     __syncthreads();  // the buffers' last readers (of an earlier piece) are done
+    stage(smem, left(t));
+    if (t + kTile < t1) fetch(t1 - t - kTile);
+    __syncthreads();
     for (int buf = 0; t < t1; t += kTile, buf ^= 1) {
-      float* rows = smem + buf * kTile * kRow;
-      float x[kBatches], dt[kBatches], z[kBatches];
+      float y[kBatches][NC], g[kBatches][NC];
 #pragma unroll
-      for (int b = 0; b < kBatches; ++b) {
-        x[b] = nx[b];
-        dt[b] = ndt[b] + bias;
-        if (!SUMMARY) z[b] = nz[b];
-      }
+      for (int b = 0; b < kBatches; ++b)
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) rows[i * kScanThreads + threadIdx.x] = nbc[i];
-      // Two buffers: a tile's rows are overwritten two tiles later, after the
-      // barrier between.
-      __syncthreads();
-      if (t + kTile < t1) fetch(t + kTile, t1);
-      const int n = static_cast<int>(min(t1 - t, static_cast<int64_t>(kTile)));
-#pragma unroll
-      for (int b = 0; b < kBatches; ++b) {
-        const int left = n - kLanes * b;  // tokens of this batch that exist
-        if (left <= 0) break;
-        if (a.softplus) dt[b] = softplus(dt[b]);
-        const float u = dt[b] * x[b];
-        if (SUMMARY && lane4 < left) sum_dt += dt[b];
-        float part[kLanes];
-#pragma unroll
-        for (int j = 0; j < kLanes; ++j) {
-          const float dj = __shfl_sync(0xffffffffu, dt[b], j, kLanes);
-          const float uj = __shfl_sync(0xffffffffu, u, j, kLanes);
-          part[j] = 0.f;
-          if (j < left) {
-            const float* row = rows + (kLanes * b + j) * kRow;
-            st.step(dj, uj, row, lane4);
-            if (!SUMMARY) part[j] = st.read(row + S, lane4);
-          }
+        for (int k = 0; k < NC; ++k) {
+          y[b][k] = ny[b][k];
+          g[b][k] = ng[b][k];
         }
-        if (!SUMMARY) {
-          float y = fmaf(skip, x[b], sum_to_own(part, lane4));
-          if (a.z) y *= silu(z[b]);
-          const int64_t own = t + kLanes * b + lane4, e = own * a.ld_y + c;
-          if (live && lane4 < left && kda_guard(e, 1, (a.T - 1) * a.ld_y + a.dim, a.err))
-            static_cast<T*>(a.y)[e] = from_f32<T>(y);
-        }
+      if (t + kTile < t1) {
+        tile<true>(smem + buf * kBufBytes, kTile, y, g);
+        stage(smem + (buf ^ 1) * kBufBytes, left(t + kTile));
+        if (t + 2 * kTile < t1) fetch(t1 - t - 2 * kTile);
+      } else {
+        tile<false>(smem + buf * kBufBytes, left(t), y, g);
       }
+      __syncthreads();  // the staged buffer is written, the read one is free
     }
   }
 };
 
-// Blocks, channel block fastest: each one chunk of the packed axis and up to 32
-// channels of one group.
-template <typename T, int S, bool SUMMARY>
-__global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, int n_cb, int cb_per_group) {
-  using K = Scan<T, S, SUMMARY>;
-  __shared__ __align__(16) float smem[2 * K::kTile * K::kRow];
+// Blocks, channel block fastest: each one chunk of the packed axis and up to
+// 32 NC channels of one group.
+template <typename T, int S, bool SUMMARY, bool WIDE>
+__global__ void __launch_bounds__(kScanThreads, scan_blocks_per_sm(S))
+ssm_scan_kernel(SsmArgs a, int n_cb, int cb_per_group) {
+  using K = Scan<T, S, SUMMARY, WIDE>;
+  constexpr int NC = K::NC;
+  __shared__ __align__(16) unsigned char smem[2 * K::kBufBytes];
   const int cb = blockIdx.x % n_cb;
   const int64_t chunk = blockIdx.x / n_cb;
   if (!SUMMARY && blockIdx.x == 0 && a.cu)
     check_cu_seqlens(a.cu, a.N, a.T, threadIdx.x, kScanThreads, a.err);
   const int per_group = a.dim / a.groups;
-  const int in_group = (cb % cb_per_group) * kScanChannels + threadIdx.x / kLanes;
+  const int in_group = NC * ((cb % cb_per_group) * (kScanThreads / kLanes) + threadIdx.x / kLanes);
   K k{a, smem};
   k.lane4 = threadIdx.x % kLanes;
   k.group = cb / cb_per_group;
-  k.live = in_group < per_group;
+  k.live = min(max(per_group - in_group, 0), NC);
   k.c = static_cast<int64_t>(k.group) * per_group + in_group;
   k.st.load_rates(a.A, k.c, a.dim, k.lane4, k.live, a.err);
-  k.bias = a.dt_bias && k.live && kda_guard(k.c, 1, a.dim, a.err) ? a.dt_bias[k.c] : 0.f;
-  k.skip = a.D && k.live && kda_guard(k.c, 1, a.dim, a.err) ? a.D[k.c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const bool in = i < k.live && kda_guard(k.c + i, 1, a.dim, a.err);
+    k.bias[i] = a.dt_bias && in ? a.dt_bias[k.c + i] : 0.f;
+    k.skip[i] = a.D && in ? a.D[k.c + i] : 0.f;
+    k.sum_dt[i] = 0.f;
+  }
   const int64_t rows = static_cast<int64_t>(a.N) * a.dim;     // of h0 and h_out
   const int64_t chunk_rows = a.n_chunks * a.dim;
   int64_t t = chunk * a.chunk;
@@ -299,10 +559,13 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, int n
     else k.st.zero();
     k.run(max(t, start), t_end);
     k.st.store(a.chunk_h, chunk * a.dim + k.c, chunk_rows, k.lane4, k.live, a.err);
-    float sum = k.sum_dt + __shfl_xor_sync(0xffffffffu, k.sum_dt, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (k.live && k.lane4 == 0 && kda_guard(chunk * a.dim + k.c, 1, chunk_rows, a.err))
-      a.chunk_dt[chunk * a.dim + k.c] = sum;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float sum = k.sum_dt[i] + __shfl_xor_sync(0xffffffffu, k.sum_dt[i], 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int64_t e = chunk * a.dim + k.c + i;
+      if (i < k.live && k.lane4 == 0 && kda_guard(e, 1, chunk_rows, a.err)) a.chunk_dt[e] = sum;
+    }
     return;
   }
 
@@ -315,14 +578,15 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, int n
     const int64_t first = start / a.chunk;
     k.st.load(a.chunk_h, first * a.dim + k.c, chunk_rows, k.lane4, k.live, a.err);
     for (int64_t i = first + 1; i < chunk; ++i) {
-      State<S> local;
+      State<S, NC> local;
       local.load(a.chunk_h, i * a.dim + k.c, chunk_rows, k.lane4, k.live, a.err);
-      const float sum = k.live && kda_guard(i * a.dim + k.c, 1, chunk_rows, a.err)
-                            ? a.chunk_dt[i * a.dim + k.c] : 0.f;
-      const f32x2 dd = pack2(sum, sum);
+      float sum[NC];
 #pragma unroll
-      for (int q = 0; q < 2 * State<S>::kQuads; ++q)
-        k.st.h[q] = fma2(ex2_2(mul2(dd, k.st.a[q])), k.st.h[q], local.h[q]);
+      for (int m = 0; m < NC; ++m) {
+        const int64_t e = i * a.dim + k.c + m;
+        sum[m] = m < k.live && kda_guard(e, 1, chunk_rows, a.err) ? a.chunk_dt[e] : 0.f;
+      }
+      k.st.chain(sum, local);
     }
   } else {
     k.st.load(a.h0, n * static_cast<int64_t>(a.dim) + k.c, rows, k.lane4, k.live, a.err);
@@ -346,7 +610,7 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(SsmArgs a, int n
 // One token of each sequence, h in place.  S / 4 lanes per channel, four
 // values each, so that the states are read and written in whole rows; bound by
 // those bytes.
-template <typename T, int S>
+template <typename T, int S, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   constexpr int kPer = S / 4;  // lanes per channel
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -360,16 +624,18 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
   if (kda_guard(at, 4, states, a.err)) h = *reinterpret_cast<const float4*>(a.h0 + at);
   float A[4], B[4], C[4];
-  const int64_t gs = static_cast<int64_t>(a.groups) * S;
+  const int64_t gs = static_cast<int64_t>(a.groups) * S, in_row = g * S + 4 * lane;
+  auto load = [&](const auto* p, int64_t e, int64_t extent, float(&v)[4]) {
+    if (VEC && kda_guard(e, 4, extent, a.err)) {
+      load4(p + e, v);
+    } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t s = 4 * lane + j;
-    A[j] = kda_guard(c * S + s, 1, static_cast<int64_t>(a.dim) * S, a.err) ? a.A[c * S + s] : 0.f;
-    B[j] = kda_guard(n * a.ld_b + g * S + s, 1, (a.N - 1) * a.ld_b + gs, a.err)
-               ? to_f32(static_cast<const T*>(a.B)[n * a.ld_b + g * S + s]) : 0.f;
-    C[j] = kda_guard(n * a.ld_c + g * S + s, 1, (a.N - 1) * a.ld_c + gs, a.err)
-               ? to_f32(static_cast<const T*>(a.C)[n * a.ld_c + g * S + s]) : 0.f;
-  }
+      for (int j = 0; j < 4; ++j) v[j] = !VEC && kda_guard(e + j, 1, extent, a.err) ? to_f32(p[e + j]) : 0.f;
+    }
+  };
+  load(a.A, c * S + 4 * lane, static_cast<int64_t>(a.dim) * S, A);
+  load(static_cast<const T*>(a.B), n * a.ld_b + in_row, (a.N - 1) * a.ld_b + gs, B);
+  load(static_cast<const T*>(a.C), n * a.ld_c + in_row, (a.N - 1) * a.ld_c + gs, C);
   const float x = element<T>(a.x, n, a.ld_x, c, true, a);
   float dt = element<T>(a.dt, n, a.ld_dt, c, true, a);
   if (a.dt_bias && kda_guard(c, 1, a.dim, a.err)) dt += a.dt_bias[c];
@@ -385,7 +651,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
   for (int o = kPer / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
   if (live && lane == 0) {
     if (a.D && kda_guard(c, 1, a.dim, a.err)) y = fmaf(a.D[c], x, y);
-    if (a.z) y *= silu(element<T>(a.z, n, a.ld_z, c, true, a));
+    if (a.z) y *= gate(element<T>(a.z, n, a.ld_z, c, true, a));
     const int64_t e = n * a.ld_y + c;
     if (kda_guard(e, 1, (a.N - 1) * a.ld_y + a.dim, a.err)) static_cast<T*>(a.y)[e] = from_f32<T>(y);
   }
@@ -395,22 +661,23 @@ struct Blocks {
   int per_group, n_cb;
 };
 Blocks channel_blocks(const SsmArgs& a) {
-  const int per = (a.dim / a.groups + kScanChannels - 1) / kScanChannels;
+  const int channels = kScanThreads / kLanes * kChannelsOf(a.state);  // of a block
+  const int per = (a.dim / a.groups + channels - 1) / channels;
   return Blocks{per, per * a.groups};
 }
 
-template <typename T, int S>
+template <typename T, int S, bool WIDE>
 cudaError_t run_scan(const SsmArgs& a, bool cut, cudaStream_t s) {
   const Blocks b = channel_blocks(a);
   if (a.n_chunks * b.n_cb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (cut) {
     prof_begin(s, "kda_ssm_summary");
-    ssm_scan_kernel<T, S, true><<<static_cast<unsigned>((a.n_chunks - 1) * b.n_cb), kScanThreads, 0, s>>>(
+    ssm_scan_kernel<T, S, true, WIDE><<<static_cast<unsigned>((a.n_chunks - 1) * b.n_cb), kScanThreads, 0, s>>>(
         a, b.n_cb, b.per_group);
     prof_end(s, "kda_ssm_summary");
   }
   prof_begin(s, "kda_ssm_scan");
-  ssm_scan_kernel<T, S, false><<<static_cast<unsigned>(a.n_chunks * b.n_cb), kScanThreads, 0, s>>>(
+  ssm_scan_kernel<T, S, false, WIDE><<<static_cast<unsigned>(a.n_chunks * b.n_cb), kScanThreads, 0, s>>>(
       a, b.n_cb, b.per_group);
   prof_end(s, "kda_ssm_scan");
   return cudaGetLastError();
@@ -421,17 +688,18 @@ cudaError_t run_step(const SsmArgs& a, cudaStream_t s) {
   const int64_t threads = static_cast<int64_t>(a.N) * a.dim * (S / 4);
   const int64_t blocks = (threads + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  ssm_step_kernel<T, S><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
+  if (a.vec) ssm_step_kernel<T, S, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
+  else ssm_step_kernel<T, S, false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t scan_of(const SsmArgs& a, bool cut, cudaStream_t s) {
   switch (a.state) {
-    case 16: return run_scan<T, 16>(a, cut, s);
-    case 32: return run_scan<T, 32>(a, cut, s);
-    case 64: return run_scan<T, 64>(a, cut, s);
-    case 128: return run_scan<T, 128>(a, cut, s);
+    case 16: return a.pairs ? run_scan<T, 16, true>(a, cut, s) : run_scan<T, 16, false>(a, cut, s);
+    case 32: return a.pairs ? run_scan<T, 32, true>(a, cut, s) : run_scan<T, 32, false>(a, cut, s);
+    case 64: return a.pairs ? run_scan<T, 64, true>(a, cut, s) : run_scan<T, 64, false>(a, cut, s);
+    case 128: return a.pairs ? run_scan<T, 128, true>(a, cut, s) : run_scan<T, 128, false>(a, cut, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -449,24 +717,27 @@ cudaError_t step_of(const SsmArgs& a, cudaStream_t s) {
 }  // namespace
 
 void ssm_chunks(SsmArgs& a, bool& cut) {
-  // A block of 4 warps walks its chunk's tokens one after another; about four
-  // such blocks per SM keep its issue slots busy.  Cutting sequences costs the
-  // first launch, about 3/4 of the second, for the cut pieces.
-  const int64_t n_cb = channel_blocks(a).n_cb, slots = 4LL * a.sm_count;
+  // Whole sequences take one launch of N n_cb blocks.  Cutting them costs the
+  // first launch, about 3/4 of the second, but fills the GPU: worth it below
+  // about 1.35 blocks per SM (a second block on some SMs and none on the others
+  // already takes as long as two on all).  At 256 blocks (4 sequences of 4096
+  // tokens, 4096 channels) whole sequences take 0.42 ms, cut ones 0.57 ms.
+  const int64_t n_cb = channel_blocks(a).n_cb;
   cut = false;
   a.n_chunks = 1;
   a.chunk = std::max<int64_t>(a.T, 1);
   if (a.T == 0) return;
   if (!a.cu) {
-    // whole sequences: one launch, N n_cb blocks of T / N tokens
     const int64_t len = a.T / a.N;
-    if (7 * a.N * n_cb >= 4 * slots || len <= 64) {
+    if (20 * a.N * n_cb >= 27LL * a.sm_count || len <= 64) {
       a.chunk = len;
       a.n_chunks = a.N;
       return;
     }
   }
-  const int64_t wanted = std::max<int64_t>(1, (slots + n_cb - 1) / n_cb);
+  // One wave of resident blocks: more chunks only add a partial second wave
+  // (65,536 tokens, 2048 channels: 3 blocks per SM 1.14 ms, 4 per SM 1.25 ms).
+  const int64_t wanted = std::max<int64_t>(1, scan_blocks_per_sm(a.state) * a.sm_count / n_cb);
   int64_t chunk = (a.T + wanted - 1) / wanted;
   chunk = std::max<int64_t>(64, (chunk + 15) / 16 * 16);
   if (chunk >= a.T) return;
