@@ -52,18 +52,58 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// 32 lanes x 32 consecutive columns of tensor memory: thread i gets lane i of
+// its warp's quarter.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 // Waits for this thread's tensor-memory loads; naming the registers keeps
 // their uses behind the wait.
-__device__ __forceinline__ void wait_ld16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               ::"memory");
+  // (at most 30 operands that are read and written: the last three in an empty
+  // statement, which stays behind the wait)
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
                  "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
+// A warp's rows of the output through its own piece of shared memory, 128
+// bytes of each of 32 rows at a time, in the layout of a 128-byte-swizzled
+// tensor copy.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t c0,
+                                             int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(smem_u32(src))
+               : "memory");
+}
+
 template <int BN, bool SWAP>
 struct Shape {
-  static constexpr int kGroups = BN >= 32 ? 2 : 1;         // sets of four adding warps
+  // sets of four adding warps; a thread's columns fill 128 bytes of bf16 (not SWAP)
+  static constexpr int kGroups = BN >= (SWAP ? 32 : 128) ? 2 : 1;
   static constexpr int kCols = BN / kGroups;               // columns of a thread's row
   static constexpr int kWarps = 2 + 4 * kGroups;
   static constexpr int kThreads = 32 * kWarps;
@@ -72,17 +112,24 @@ struct Shape {
   static constexpr uint32_t kRowBytes = kTileRows * kBlockK, kColBytes = BN * kBlockK;
   static constexpr uint32_t kStageBytes = kRowBytes + kColBytes;
   static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;  // the tiles start on 1024 bytes
+  // columns per tensor-memory load (at 128 sums a thread, 32 more do not fit)
+  static constexpr int kLoad = kCols % 32 == 0 && kCols < 128 ? 32 : 16;
+  static constexpr uint32_t kStoreBytes = SWAP ? 0 : 4 * kGroups * 4096;  // a piece per adding warp
+  // the tiles start on 1024 bytes
+  static constexpr uint32_t kSmem = kStages * kStageBytes + kStoreBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kCols % 16 == 0, "whole loads");
 };
 
 struct Maps {
   CUtensorMap rows, cols;  // the operand of a tile's 128 rows, and of its BN columns
+  CUtensorMap out;         // written 32 rows x 128 bytes at a time (where its rows allow it)
 };
 
 template <int BN, bool SWAP, typename OutT>
 __global__ void __launch_bounds__(Shape<BN, SWAP>::kThreads, 1)
-matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int tiles_c, int band) {
+matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int tiles_c, int band,
+              bool tma_out) {
   using G = Shape<BN, SWAP>;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t full[G::kStages], empty[G::kStages], tfull[G::kBufs], tempty[G::kBufs];
@@ -176,45 +223,51 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       tile_at(t, r, c);
       const int64_t row = static_cast<int64_t>(r) * kTileRows + 32 * quad + lane;
       const int64_t col0 = static_cast<int64_t>(c) * BN + G::kCols * group;
-      float acc[G::kCols];
+      f32x2 acc[G::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < G::kCols; ++i) acc[i] = 0.f;
+      for (int i = 0; i < G::kCols / 2; ++i) acc[i] = 0;
+      // The next block's scales, as loaded (multiplying them here would wait for
+      // the loads): that of this thread's row, and that of its columns (SWAP: of
+      // column `lane` of them).
       const int64_t n_as = (a.M - 1) * a.ld_as + kblocks;
       const int64_t n_bs = ((a.N + kScaleGroup - 1) / kScaleGroup - 1) * a.ld_bs + kblocks;
-      auto scale_a = [&](int64_t m, int kb) {
-        return m < a.M && kda_guard(m * a.ld_as + kb, 1, n_as, a.err) ? a.a_scale[m * a.ld_as + kb] : 0.f;
+      const int64_t m_scale = SWAP ? col0 + lane % G::kCols : row;
+      const int64_t n_scale = (SWAP ? static_cast<int64_t>(r) * kTileRows : col0) / kScaleGroup;
+      const bool m_in = m_scale < a.M, n_in = n_scale * kScaleGroup < a.N;
+      const float* pa = a.a_scale + m_scale * a.ld_as;
+      const float* pb = a.b_scale + n_scale * a.ld_bs;
+      float sa = 0.f, sb = 0.f;
+      auto fetch = [&](int kb) {
+        if (m_in && kda_guard(pa - a.a_scale + kb, 1, n_as, a.err)) sa = pa[kb];
+        if (n_in && kda_guard(pb - a.b_scale + kb, 1, n_bs, a.err)) sb = pb[kb];
       };
-      auto scale_b = [&](int64_t n, int kb) {
-        const int64_t e = n / kScaleGroup * a.ld_bs + kb;
-        return n < a.N && kda_guard(e, 1, n_bs, a.err) ? a.b_scale[e] : 0.f;
-      };
-      // the scale of this thread's row, times (not SWAP) that of its columns
-      auto scale_of = [&](int kb) {
-        return SWAP ? scale_b(static_cast<int64_t>(r) * kTileRows, kb) : scale_a(row, kb) * scale_b(col0, kb);
-      };
-      float next = scale_of(0);
+      fetch(0);
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const int buf = static_cast<int>(it % G::kBufs);
-        const float scale = next;
-        if (kb + 1 < kblocks) next = scale_of(kb + 1);
-        bool ok = mbar_wait(&tfull[buf], static_cast<uint32_t>(it / G::kBufs) & 1);
+        const float scale = sa * sb;
+        if (kb + 1 < kblocks) fetch(kb + 1);
+        const bool ok = mbar_wait(&tfull[buf], static_cast<uint32_t>(it / G::kBufs) & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) timeout();
           break;
         }
         tc_fence_after();
         const uint32_t at = tmem_addr(tmem, 32 * quad, buf * BN + G::kCols * group);
-        uint32_t d[2][16];
-        tmem_ld16(at, d[0]);
 #pragma unroll
-        for (int i = 0; i < G::kCols / 16; ++i) {
-          wait_ld16(d[i & 1]);
-          if (i + 1 < G::kCols / 16) tmem_ld16(at + 16 * (i + 1), d[(i + 1) & 1]);
+        for (int i = 0; i < G::kCols / G::kLoad; ++i) {
+          uint32_t d[G::kLoad];
+          tmem_ld(at + G::kLoad * i, d);
+          wait_ld(d);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float s = scale;
-            if (SWAP) s *= scale_a(col0 + 16 * i + j, kb);
-            acc[16 * i + j] = fmaf(__uint_as_float(d[i & 1][j]), s, acc[16 * i + j]);
+          for (int j = 0; j < G::kLoad / 2; ++j) {
+            f32x2 s;
+            if (SWAP)  // lane j of the scales is column j's
+              s = pack2(__shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j, 32),
+                        __shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j + 1, 32));
+            else
+              s = pack2(scale, scale);
+            f32x2& to = acc[G::kLoad / 2 * i + j];
+            to = fma2(pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, to);
           }
         }
         tc_fence_before();
@@ -224,31 +277,64 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       if (s_abort) break;
       OutT* out = static_cast<OutT*>(a.out);
       const int64_t extent = (a.M - 1) * a.ld_out + a.N;
-      if (SWAP) {  // a thread holds one row of B for some rows of A
+      auto value = [&](int i) {
+        float lo, hi;
+        unpack2(acc[i / 2], lo, hi);
+        return i & 1 ? hi : lo;
+      };
+      if constexpr (SWAP) {  // a thread holds one row of B for some rows of A
 #pragma unroll
         for (int i = 0; i < G::kCols; ++i) {
           const int64_t m = col0 + i, e = m * a.ld_out + row;
-          if (m < a.M && row < a.N && kda_guard(e, 1, extent, a.err)) out[e] = from_f32<OutT>(acc[i]);
+          if (m < a.M && row < a.N && kda_guard(e, 1, extent, a.err)) out[e] = from_f32<OutT>(value(i));
         }
-      } else if (row < a.M) {
-        const int64_t e = row * a.ld_out + col0;
-        const bool wide = (reinterpret_cast<uintptr_t>(out + e) & 15) == 0;
+      } else {
+        // 128 bytes of each of the warp's 32 rows at a time, turned in shared
+        // memory: a tensor copy, which leaves out what lies past the last row
+        // or column, or, where out's rows do not allow one, a row at a time
+        constexpr int kPiece = 128 / sizeof(OutT);
+        static_assert(G::kCols % kPiece == 0, "whole pieces");
+        unsigned char* own = tiles + G::kStages * G::kStageBytes + 4096 * (warp - 2);
 #pragma unroll
-        for (int i = 0; i < G::kCols; i += 8) {
-          if (wide && col0 + i + 8 <= a.N) {
-            float v[8];
+        for (int p = 0; p < G::kCols / kPiece; ++p) {
+          if (tma_out && lane == 0) bulk_wait_read();  // the piece before has left
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = acc[i + j];
-            if (kda_guard(e + i, 8, extent, a.err)) store8(out + e + i, v);
+          for (int q = 0; q < 8; ++q) {  // 16 bytes
+            uint32_t w[4];
+            constexpr int kPer = 4 / sizeof(OutT);  // values in 4 bytes
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int i = p * kPiece + (4 * q + k) * kPer;
+              w[k] = kPer == 2 ? pack2_bf16(value(i), value(i + 1)) : __float_as_uint(value(i));
+            }
+            *reinterpret_cast<uint4*>(own + sw128_offset(32, lane, 16 * q)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          const int64_t c_at = col0 + p * kPiece, r_at = row - lane;
+          if (tma_out) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (c_at < a.N && r_at < a.M)
+                tma_store_2d(&maps.out, own, static_cast<int32_t>(c_at), static_cast<int32_t>(r_at));
+              bulk_commit();
+            }
           } else {
+            __syncwarp();
+            for (int i = 0; i < 32 && r_at + i < a.M; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (col0 + i + j < a.N && kda_guard(e + i + j, 1, extent, a.err))
-                out[e + i + j] = from_f32<OutT>(acc[i + j]);
+              for (int k = 0; k < kPiece; k += 32) {
+                const int64_t e = (r_at + i) * a.ld_out + c_at + k + lane;
+                if (c_at + k + lane < a.N && kda_guard(e, 1, extent, a.err))
+                  out[e] = *reinterpret_cast<const OutT*>(
+                      own + sw128_offset(32, i, static_cast<uint32_t>(sizeof(OutT)) * (k + lane)));
+              }
           }
         }
       }
     }
+    if (!SWAP && tma_out && lane == 0) bulk_wait();  // the block's memory outlives its copies
   }
   tc_fence_before();
   __syncthreads();
@@ -272,16 +358,18 @@ EncodeTiledFn find_encode() {
   return nullptr;
 }
 
-// [rows, K] bytes; boxes of 128 bytes x `box` rows, 128-byte swizzle.  Past the
-// last row and the last column, zeros (e4m3 0.0) are read.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, uint32_t box) {
+// [rows, cols] elements of `size` bytes, rows `pitch` bytes apart, in boxes of 128 bytes x
+// `box` rows with the 128-byte swizzle.  Past the last row and column zeros
+// (e4m3 0.0) are read, and nothing is written.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int64_t size, const void* base, int64_t rows,
+              int64_t cols, int64_t pitch, uint32_t box) {
   static const EncodeTiledFn fn = find_encode();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-  const cuuint32_t boxes[2] = {kBlockK, box};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / size), box};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, boxes, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -293,8 +381,16 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   const int64_t rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;
   Maps maps;
   memset(&maps, 0, sizeof maps);
-  if (!make_map(&maps.rows, SWAP ? a.b : a.a, rows, a.K, SWAP ? a.ld_b : a.ld_a, kTileRows) ||
-      !make_map(&maps.cols, SWAP ? a.a : a.b, cols, a.K, SWAP ? a.ld_a : a.ld_b, BN))
+  constexpr CUtensorMapDataType kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!make_map(&maps.rows, kBytes, 1, SWAP ? a.b : a.a, rows, a.K, SWAP ? a.ld_b : a.ld_a, kTileRows) ||
+      !make_map(&maps.cols, kBytes, 1, SWAP ? a.a : a.b, cols, a.K, SWAP ? a.ld_a : a.ld_b, BN))
+    return cudaErrorInvalidValue;
+  constexpr int64_t kOut = sizeof(OutT);
+  const bool tma_out = !SWAP && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+                       a.ld_out * kOut % 16 == 0;
+  if (tma_out && !make_map(&maps.out, kOut == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                           kOut, a.out, a.M, a.N, a.ld_out * kOut, 32))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(G::kSmem));
@@ -304,7 +400,7 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   const int64_t n = static_cast<int64_t>(tiles_r) * tiles_c;
   const int band = 12;  // of 152 tiles in flight, 12 x 12.7
   kern<<<static_cast<unsigned>(std::min<int64_t>(n, a.sm_count)), G::kThreads, G::kSmem, s>>>(
-      maps, a, tiles_r, tiles_c, band);
+      maps, a, tiles_r, tiles_c, band, tma_out);
   return cudaGetLastError();
 }
 
