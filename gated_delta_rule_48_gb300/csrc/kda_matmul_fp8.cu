@@ -121,6 +121,19 @@ struct Shape {
   static_assert(kCols % 16 == 0, "whole loads");
 };
 
+// A place in a ring of N barriers, and the parity of its present phase.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 struct Maps {
   CUtensorMap rows, cols;  // the operand of a tile's 128 rows, and of its BN columns
   CUtensorMap out;         // written 32 rows x 128 bytes at a time (where its rows allow it)
@@ -169,55 +182,77 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
     c = static_cast<int>(in / height);
   };
 
+  // The copying and the multiplying thread are on every block's path, one
+  // instruction after another: their loops hold little but the waits and the
+  // issues (with 64-bit counters and descriptors built per product a block
+  // took 0.5 us whatever its size).
   if (warp == 0) {
     if (lane == 0) {
-      int64_t it = 0;
-      for (int64_t t = blockIdx.x; t < n_tiles && !s_abort; t += gridDim.x) {
+      Ring<G::kStages> ring;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
         int r, c;
         tile_at(t, r, c);
-        for (int kb = 0; kb < kblocks && !s_abort; ++kb, ++it) {
-          const int st = static_cast<int>(it % G::kStages);
-          const uint32_t round = static_cast<uint32_t>(it / G::kStages);
-          if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1)) { timeout(); break; }
-          unsigned char* p = tiles + st * G::kStageBytes;
-          mbar_arrive_expect_tx(&full[st], G::kStageBytes);
-          tma_load_2d(p, &maps.rows, kb * kBlockK, r * kTileRows, &full[st]);
-          tma_load_2d(p + G::kRowBytes, &maps.cols, kb * kBlockK, c * BN, &full[st]);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          // (a wait for the round before the first one passes at once)
+          if (!(ok = mbar_wait(&empty[ring.at], ring.phase ^ 1))) break;
+          unsigned char* p = tiles + ring.at * G::kStageBytes;
+          mbar_arrive_expect_tx(&full[ring.at], G::kStageBytes);
+          tma_load_2d(p, &maps.rows, kb * kBlockK, r * kTileRows, &full[ring.at]);
+          tma_load_2d(p + G::kRowBytes, &maps.cols, kb * kBlockK, c * BN, &full[ring.at]);
+          ring.next();
         }
       }
-      // after an error: the copies in flight land before the block's memory goes
-      if (s_abort)
-        for (int64_t i = it < G::kStages ? 0 : it - G::kStages; i < it; ++i)
-          mbar_wait(&full[i % G::kStages], static_cast<uint32_t>(i / G::kStages) & 1, 1u << 16);
+      if (!ok) {
+        timeout();
+        // the copies in flight land before the block's memory goes: each stage's
+        // last one is in the phase before its next
+        for (int i = 0; i < G::kStages; ++i) {
+          mbar_wait(&full[ring.at], ring.phase ^ 1, 1u << 16);
+          ring.next();
+        }
+      }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = make_idesc(0 /* e4m3 */, kTileRows, BN, false, false);
-      int64_t it = 0;
-      for (int64_t t = blockIdx.x; t < n_tiles && !s_abort; t += gridDim.x) {
-        for (int kb = 0; kb < kblocks && !s_abort; ++kb, ++it) {
-          const int st = static_cast<int>(it % G::kStages), buf = static_cast<int>(it % G::kBufs);
-          const uint32_t turn = static_cast<uint32_t>(it / G::kBufs);
-          if (turn > 0 && !mbar_wait(&tempty[buf], (turn - 1) & 1)) { timeout(); break; }
-          if (!mbar_wait(&full[st], static_cast<uint32_t>(it / G::kStages) & 1)) { timeout(); break; }
-          tc_fence_after();
-          const uint32_t rows = smem_u32(tiles + st * G::kStageBytes), cols = rows + G::kRowBytes;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_e4m3_ss(tmem + buf * BN, smem_desc_sw128(rows + 32 * kk, 16, 1024),
-                        smem_desc_sw128(cols + 32 * kk, 16, 1024), idesc, kk > 0);
-          mma_commit(&empty[st]);
-          mma_commit(&tfull[buf]);
+      const uint64_t rows0 = smem_desc_sw128(smem_u32(tiles), 16, 1024);
+      Ring<G::kStages> ring;
+      Ring<G::kBufs> bufs;
+      const uint32_t n_blocks =
+          static_cast<uint32_t>((n_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * kblocks;
+      bool ok = true;
+      uint32_t i = 0;
+      for (; i < n_blocks; ++i) {
+        if (!(ok = mbar_wait(&tempty[bufs.at], bufs.phase ^ 1) &&
+                   mbar_wait(&full[ring.at], ring.phase)))
+          break;
+        tc_fence_after();
+        // descriptors count in 16 bytes
+        const uint64_t rows = rows0 + ring.at * (G::kStageBytes >> 4), cols = rows + (G::kRowBytes >> 4);
+        const uint32_t to = tmem + bufs.at * BN;
+        mma_e4m3_ss(to, rows, cols, idesc, 0);
+        mma_e4m3_ss(to, rows + 2, cols + 2, idesc, 1);
+        mma_e4m3_ss(to, rows + 4, cols + 4, idesc, 1);
+        mma_e4m3_ss(to, rows + 6, cols + 6, idesc, 1);
+        mma_commit(&empty[ring.at]);
+        mma_commit(&tfull[bufs.at]);
+        ring.next();
+        bufs.next();
+      }
+      if (!ok) {
+        timeout();
+        // the last products end before tensor memory is freed (otherwise the
+        // adding warps have waited for them)
+        if (i > 0) {
+          const int last = (bufs.at + G::kBufs - 1) % G::kBufs;
+          mbar_wait(&tfull[last], bufs.at ? bufs.phase : bufs.phase ^ 1, 1u << 16);
         }
       }
-      // the last products end before tensor memory is freed (the adding warps
-      // have waited for them, unless there was an error)
-      if (s_abort && it > 0)
-        mbar_wait(&tfull[(it - 1) % G::kBufs], static_cast<uint32_t>((it - 1) / G::kBufs) & 1, 1u << 16);
     }
   } else {
     const int quad = warp & 3, group = (warp - 2) >> 2;
-    int64_t it = 0;
+    Ring<G::kBufs> bufs;
     for (int64_t t = blockIdx.x; t < n_tiles && !s_abort; t += gridDim.x) {
       int r, c;
       tile_at(t, r, c);
@@ -226,9 +261,9 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       f32x2 acc[G::kCols / 2];
 #pragma unroll
       for (int i = 0; i < G::kCols / 2; ++i) acc[i] = 0;
-      // The next block's scales, as loaded (multiplying them here would wait for
-      // the loads): that of this thread's row, and that of its columns (SWAP: of
-      // column `lane` of them).
+      // Scales, fetched four blocks ahead (a fetch takes longer than a block):
+      // that of this thread's row (SWAP: of column `lane` of its columns), and,
+      // one block in each lane, that of the 128 rows of B that they all share.
       const int64_t n_as = (a.M - 1) * a.ld_as + kblocks;
       const int64_t n_bs = ((a.N + kScaleGroup - 1) / kScaleGroup - 1) * a.ld_bs + kblocks;
       const int64_t m_scale = SWAP ? col0 + lane % G::kCols : row;
@@ -236,23 +271,44 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       const bool m_in = m_scale < a.M, n_in = n_scale * kScaleGroup < a.N;
       const float* pa = a.a_scale + m_scale * a.ld_as;
       const float* pb = a.b_scale + n_scale * a.ld_bs;
-      float sa = 0.f, sb = 0.f;
-      auto fetch = [&](int kb) {
-        if (m_in && kda_guard(pa - a.a_scale + kb, 1, n_as, a.err)) sa = pa[kb];
-        if (n_in && kda_guard(pb - a.b_scale + kb, 1, n_bs, a.err)) sb = pb[kb];
+      float sa[4], next[4], sb = 0.f, sb_next = 0.f;
+      auto fetch_a = [&](int kb) {
+        if (a.scale_vec && m_in && kb + 4 <= kblocks && kda_guard(pa - a.a_scale + kb, 4, n_as, a.err)) {
+          const float4 v = *reinterpret_cast<const float4*>(pa + kb);
+          next[0] = v.x; next[1] = v.y; next[2] = v.z; next[3] = v.w;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            next[u] = m_in && kb + u < kblocks && kda_guard(pa - a.a_scale + kb + u, 1, n_as, a.err)
+                          ? pa[kb + u] : 0.f;
+        }
       };
-      fetch(0);
-      for (int kb = 0; kb < kblocks; ++kb, ++it) {
-        const int buf = static_cast<int>(it % G::kBufs);
-        const float scale = sa * sb;
-        if (kb + 1 < kblocks) fetch(kb + 1);
-        const bool ok = mbar_wait(&tfull[buf], static_cast<uint32_t>(it / G::kBufs) & 1);
+      auto fetch_b = [&](int kb) {
+        sb_next = n_in && kb + lane < kblocks && kda_guard(pb - a.b_scale + kb + lane, 1, n_bs, a.err)
+                      ? pb[kb + lane] : 0.f;
+      };
+      fetch_a(0);
+      fetch_b(0);
+      for (int kb4 = 0; kb4 < kblocks && !s_abort; kb4 += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sa[u] = next[u];
+        if (kb4 + 4 < kblocks) fetch_a(kb4 + 4);
+        if (kb4 % 32 == 0) {
+          sb = sb_next;
+          if (kb4 + 32 < kblocks) fetch_b(kb4 + 32);
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int kb = kb4 + u;
+        if (kb >= kblocks) break;
+        const float scale = sa[u] * __shfl_sync(0xffffffffu, sb, kb & 31);
+        const bool ok = mbar_wait(&tfull[bufs.at], bufs.phase);
         if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) timeout();
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem_addr(tmem, 32 * quad, buf * BN + G::kCols * group);
+        const uint32_t at = tmem_addr(tmem, 32 * quad, bufs.at * BN + G::kCols * group);
 #pragma unroll
         for (int i = 0; i < G::kCols / G::kLoad; ++i) {
           uint32_t d[G::kLoad];
@@ -272,7 +328,9 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (lane == 0) mbar_arrive(&tempty[bufs.at]);
+        bufs.next();
+      }
       }
       if (s_abort) break;
       OutT* out = static_cast<OutT*>(a.out);
@@ -322,6 +380,7 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
             }
           } else {
             __syncwarp();
+#pragma unroll 1
             for (int i = 0; i < 32 && r_at + i < a.M; ++i)
 #pragma unroll
               for (int k = 0; k < kPiece; k += 32) {
