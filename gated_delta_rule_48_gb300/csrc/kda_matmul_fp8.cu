@@ -43,13 +43,13 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1,
-                                            uint64_t* bar) {
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
+      "{\n .reg .pred p;\n .reg .b32 r;\n elect.sync r|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(is));
+  return is != 0;
 }
 
 // 32 lanes x 32 consecutive columns of tensor memory: thread i gets lane i of
@@ -66,28 +66,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// Waits for this thread's tensor-memory loads; naming the registers keeps
-// their uses behind the wait.
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
-               ::"memory");
-  // (at most 30 operands that are read and written: the last three in an empty
-  // statement, which stays behind the wait)
-  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+// Waits for this thread's tensor-memory loads and passes `v` on: what is
+// computed with the result comes after the wait.  (Naming the loaded registers
+// instead cost a move for each.)
+__device__ __forceinline__ float wait_ld(float v) {
+  float r;
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n mov.b32 %0, %1;" : "=f"(r) : "f"(v) : "memory");
+  return r;
 }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
 
 // A warp's rows of the output through its own piece of shared memory, 128
 // bytes of each of 32 rows at a time, in the layout of a 128-byte-swizzled
@@ -105,19 +93,29 @@ struct Shape {
   // sets of four adding warps; a thread's columns fill 128 bytes of bf16 (not SWAP)
   static constexpr int kGroups = BN >= (SWAP ? 32 : 128) ? 2 : 1;
   static constexpr int kCols = BN / kGroups;               // columns of a thread's row
-  static constexpr int kWarps = 2 + 4 * kGroups;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kBufs = BN == 256 ? 2 : 4;          // of tensor memory
-  static constexpr uint32_t kTmemCols = BN * kBufs < 32 ? 32 : BN * kBufs;
-  static constexpr uint32_t kRowBytes = kTileRows * kBlockK, kColBytes = BN * kBlockK;
+  // the copying, the multiplying and the scale-fetching warp, one that only
+  // fills up their set of four (register shares go by sets), then the adding warps
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  // 128 sums a thread: the first set gives registers to the others (launched
+  // with 168 each, 3 * 168 = 56 + 2 * 224)
+  static constexpr bool kShares = kCols == 128;
+  static constexpr int kLaunchRegs = 168, kAddRegs = 224, kRestRegs = 56;
+  static_assert(!kShares || 128 * (kRestRegs + kGroups * kAddRegs) <= kThreads * kLaunchRegs,
+                "register shares exceed the launch's");
+  // k-blocks that are copied, multiplied and handed over together: one block's
+  // products of a narrow tile take less time than the waits around them
+  static constexpr int kUnit = BN == 256 ? 1 : 2;
+  static constexpr int kBufs = BN >= 128 ? 2 : 4;          // of tensor memory, a unit each
+  static constexpr uint32_t kTmemCols = BN * kUnit * kBufs;
+  static constexpr uint32_t kRowBytes = kUnit * kTileRows * kBlockK, kColBytes = kUnit * BN * kBlockK;
   static constexpr uint32_t kStageBytes = kRowBytes + kColBytes;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  // columns per tensor-memory load (at 128 sums a thread, 32 more do not fit)
-  static constexpr int kLoad = kCols % 32 == 0 && kCols < 128 ? 32 : 16;
+  static constexpr int kStages = BN == 128 ? 3 : BN == 256 || BN == 64 ? 4 : 5;
+  static constexpr int kLoad = kCols % 32 == 0 && kCols < 128 ? 32 : 16;  // columns per tensor-memory load
+  static constexpr int kOwn = SWAP ? BN : kTileRows;       // rows of A in a tile
   static constexpr uint32_t kStoreBytes = SWAP ? 0 : 4 * kGroups * 4096;  // a piece per adding warp
-  // the tiles start on 1024 bytes
-  static constexpr uint32_t kSmem = kStages * kStageBytes + kStoreBytes + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kSmem = kStages * kStageBytes + kStoreBytes;
+  // with the scales and barriers in front of it, up to the next 1024 bytes
+  static_assert(kSmem + (4 * kOwn * 4 + 256 + 1023) / 1024 * 1024 <= 227 * 1024, "shared memory");
   static_assert(kCols % 16 == 0, "whole loads");
 };
 
@@ -142,21 +140,23 @@ struct Maps {
 template <int BN, bool SWAP, typename OutT>
 __global__ void __launch_bounds__(Shape<BN, SWAP>::kThreads, 1)
 matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int tiles_c, int band,
-              bool tma_out) {
+              bool whole, bool tma_out) {
   using G = Shape<BN, SWAP>;
-  extern __shared__ unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char tiles[];
   __shared__ uint64_t full[G::kStages], empty[G::kStages], tfull[G::kBufs], tempty[G::kBufs];
+  // scales of A: two k-blocks of the tile's rows to a slot
+  __shared__ uint64_t sfull[2], sempty[2];
+  __shared__ float s_scale[2][2][G::kOwn];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  unsigned char* tiles = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                                                          ~uintptr_t{1023});
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kblocks = (a.K + kBlockK - 1) / kBlockK;
+  const int kblocks = (a.K + kBlockK - 1) / kBlockK, units = (kblocks + G::kUnit - 1) / G::kUnit;
   const int64_t n_tiles = static_cast<int64_t>(tiles_r) * tiles_c;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < G::kBufs; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], 4 * G::kGroups); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&sfull[i], 1); mbar_init(&sempty[i], 4 * G::kGroups); }
     mbar_fence_init();
     s_abort = 0;
   }
@@ -182,24 +182,41 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
     c = static_cast<int>(in / height);
   };
 
-  // The copying and the multiplying thread are on every block's path, one
+  // The copying and the multiplying warp are on every block's path, one
   // instruction after another: their loops hold little but the waits and the
-  // issues (with 64-bit counters and descriptors built per product a block
-  // took 0.5 us whatever its size).
-  if (warp == 0) {
-    if (lane == 0) {
+  // issues, and whole warps run them, so that descriptors and addresses are
+  // computed once per warp, where the issuing instructions take them from.
+  // (With 64-bit counters, one thread and descriptors built per product, a
+  // block of any size took 0.5 us.)
+  if (warp < 4) {
+    if constexpr (G::kShares) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kRestRegs));
+    const bool issues = elect_one();
+    if (warp == 0) {
       Ring<G::kStages> ring;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
         int r, c;
         tile_at(t, r, c);
-        for (int kb = 0; kb < kblocks; ++kb) {
+        for (int u = 0; u < units; ++u) {
           // (a wait for the round before the first one passes at once)
-          if (!(ok = mbar_wait(&empty[ring.at], ring.phase ^ 1))) break;
-          unsigned char* p = tiles + ring.at * G::kStageBytes;
-          mbar_arrive_expect_tx(&full[ring.at], G::kStageBytes);
-          tma_load_2d(p, &maps.rows, kb * kBlockK, r * kTileRows, &full[ring.at]);
-          tma_load_2d(p + G::kRowBytes, &maps.cols, kb * kBlockK, c * BN, &full[ring.at]);
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[ring.at], ring.phase ^ 1));
+          if (!ok) break;
+          if (issues) {
+            unsigned char* p = tiles + ring.at * G::kStageBytes;
+            mbar_arrive_expect_tx(&full[ring.at], G::kStageBytes);
+            if (whole) {
+              tma_load_3d(p, &maps.rows, 0, r * kTileRows, u * G::kUnit, &full[ring.at]);
+              tma_load_3d(p + G::kRowBytes, &maps.cols, 0, c * BN, u * G::kUnit, &full[ring.at]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < G::kUnit; ++e) {
+                const int k = (u * G::kUnit + e) * kBlockK;
+                tma_load_3d(p + e * kTileRows * kBlockK, &maps.rows, k, r * kTileRows, 0, &full[ring.at]);
+                tma_load_3d(p + G::kRowBytes + e * BN * kBlockK, &maps.cols, k, c * BN, 0,
+                            &full[ring.at]);
+              }
+            }
+          }
           ring.next();
         }
       }
@@ -212,31 +229,33 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
           ring.next();
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1) {
       constexpr uint32_t idesc = make_idesc(0 /* e4m3 */, kTileRows, BN, false, false);
       const uint64_t rows0 = smem_desc_sw128(smem_u32(tiles), 16, 1024);
       Ring<G::kStages> ring;
       Ring<G::kBufs> bufs;
-      const uint32_t n_blocks =
-          static_cast<uint32_t>((n_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * kblocks;
+      const uint32_t n_units =
+          static_cast<uint32_t>((n_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * units;
       bool ok = true;
       uint32_t i = 0;
-      for (; i < n_blocks; ++i) {
-        if (!(ok = mbar_wait(&tempty[bufs.at], bufs.phase ^ 1) &&
-                   mbar_wait(&full[ring.at], ring.phase)))
-          break;
+      for (; i < n_units; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&tempty[bufs.at], bufs.phase ^ 1) &&
+                                         mbar_wait(&full[ring.at], ring.phase));
+        if (!ok) break;
         tc_fence_after();
         // descriptors count in 16 bytes
         const uint64_t rows = rows0 + ring.at * (G::kStageBytes >> 4), cols = rows + (G::kRowBytes >> 4);
-        const uint32_t to = tmem + bufs.at * BN;
-        mma_e4m3_ss(to, rows, cols, idesc, 0);
-        mma_e4m3_ss(to, rows + 2, cols + 2, idesc, 1);
-        mma_e4m3_ss(to, rows + 4, cols + 4, idesc, 1);
-        mma_e4m3_ss(to, rows + 6, cols + 6, idesc, 1);
-        mma_commit(&empty[ring.at]);
-        mma_commit(&tfull[bufs.at]);
+        const uint32_t to = tmem + bufs.at * (G::kUnit * BN);
+        if (issues) {
+#pragma unroll
+          for (int e = 0; e < G::kUnit; ++e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3_ss(to + e * BN, rows + e * (kTileRows * kBlockK >> 4) + 2 * k,
+                          cols + e * (BN * kBlockK >> 4) + 2 * k, idesc, k > 0);
+          mma_commit(&empty[ring.at]);
+          mma_commit(&tfull[bufs.at]);
+        }
         ring.next();
         bufs.next();
       }
@@ -249,10 +268,47 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
           mbar_wait(&tfull[last], bufs.at ? bufs.phase : bufs.phase ^ 1, 1u << 16);
         }
       }
+    } else if (warp == 2) {
+      // The rows' scales lie a row apart, one cache line to each: fetched here
+      // once for all the adding warps, up to four blocks ahead of them.
+      const int64_t n_as = (a.M - 1) * a.ld_as + kblocks;
+      Ring<2> slots;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+        int r, c;
+        tile_at(t, r, c);
+        const int64_t m0 = static_cast<int64_t>(SWAP ? c : r) * G::kOwn;
+        for (int kb = 0; kb < kblocks; kb += 2) {
+          constexpr int kRows = (G::kOwn + 31) / 32;  // per lane
+          float v[kRows][2];
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int64_t m = m0 + 32 * i + lane, e = m * a.ld_as + kb;
+            const bool in = m < a.M && 32 * i + lane < G::kOwn;
+            v[i][0] = v[i][1] = 0.f;  // (zeros past the last block)
+            if (in && kda_guard(e, 1, n_as, a.err)) v[i][0] = a.a_scale[e];
+            if (in && kb + 1 < kblocks && kda_guard(e + 1, 1, n_as, a.err)) v[i][1] = a.a_scale[e + 1];
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&sempty[slots.at], slots.phase ^ 1));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (32 * i + lane < G::kOwn) {
+              s_scale[slots.at][0][32 * i + lane] = v[i][0];
+              s_scale[slots.at][1][32 * i + lane] = v[i][1];
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[slots.at]);
+          slots.next();
+        }
+      }
+      if (!ok) timeout();
     }
   } else {
-    const int quad = warp & 3, group = (warp - 2) >> 2;
+    if constexpr (G::kShares) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kAddRegs));
+    const int quad = warp & 3, group = (warp - 4) >> 2;
     Ring<G::kBufs> bufs;
+    Ring<2> slots;
     for (int64_t t = blockIdx.x; t < n_tiles && !s_abort; t += gridDim.x) {
       int r, c;
       tile_at(t, r, c);
@@ -261,76 +317,76 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       f32x2 acc[G::kCols / 2];
 #pragma unroll
       for (int i = 0; i < G::kCols / 2; ++i) acc[i] = 0;
-      // Scales, fetched four blocks ahead (a fetch takes longer than a block):
-      // that of this thread's row (SWAP: of column `lane` of its columns), and,
-      // one block in each lane, that of the 128 rows of B that they all share.
-      const int64_t n_as = (a.M - 1) * a.ld_as + kblocks;
+      // The scale of B's 128 rows that this thread's products share, one block
+      // in each lane, fetched 32 blocks ahead; A's come through shared memory.
       const int64_t n_bs = ((a.N + kScaleGroup - 1) / kScaleGroup - 1) * a.ld_bs + kblocks;
-      const int64_t m_scale = SWAP ? col0 + lane % G::kCols : row;
       const int64_t n_scale = (SWAP ? static_cast<int64_t>(r) * kTileRows : col0) / kScaleGroup;
-      const bool m_in = m_scale < a.M, n_in = n_scale * kScaleGroup < a.N;
-      const float* pa = a.a_scale + m_scale * a.ld_as;
+      const bool n_in = n_scale * kScaleGroup < a.N;
       const float* pb = a.b_scale + n_scale * a.ld_bs;
-      float sa[4], next[4], sb = 0.f, sb_next = 0.f;
-      auto fetch_a = [&](int kb) {
-        if (a.scale_vec && m_in && kb + 4 <= kblocks && kda_guard(pa - a.a_scale + kb, 4, n_as, a.err)) {
-          const float4 v = *reinterpret_cast<const float4*>(pa + kb);
-          next[0] = v.x; next[1] = v.y; next[2] = v.z; next[3] = v.w;
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            next[u] = m_in && kb + u < kblocks && kda_guard(pa - a.a_scale + kb + u, 1, n_as, a.err)
-                          ? pa[kb + u] : 0.f;
-        }
-      };
+      float sb = 0.f, sb_next = 0.f;
       auto fetch_b = [&](int kb) {
-        sb_next = n_in && kb + lane < kblocks && kda_guard(pb - a.b_scale + kb + lane, 1, n_bs, a.err)
-                      ? pb[kb + lane] : 0.f;
+        sb_next = 0.f;
+        if (n_in && kb + lane < kblocks && kda_guard(pb - a.b_scale + kb + lane, 1, n_bs, a.err))
+          sb_next = pb[kb + lane];
       };
-      fetch_a(0);
       fetch_b(0);
-      for (int kb4 = 0; kb4 < kblocks && !s_abort; kb4 += 4) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sa[u] = next[u];
-        if (kb4 + 4 < kblocks) fetch_a(kb4 + 4);
-        if (kb4 % 32 == 0) {
-          sb = sb_next;
-          if (kb4 + 32 < kblocks) fetch_b(kb4 + 32);
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int kb = kb4 + u;
-        if (kb >= kblocks) break;
-        const float scale = sa[u] * __shfl_sync(0xffffffffu, sb, kb & 31);
-        const bool ok = mbar_wait(&tfull[bufs.at], bufs.phase);
-        if (!__all_sync(0xffffffffu, ok)) {
+      // this thread's row of A; SWAP: column `lane` of its columns
+      const int own = SWAP ? G::kCols * group + lane % G::kCols : 32 * quad + lane;
+      for (int kb = 0; kb < kblocks; kb += 2) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slots.at], slots.phase))) {
           if (lane == 0) timeout();
           break;
         }
-        tc_fence_after();
-        const uint32_t at = tmem_addr(tmem, 32 * quad, bufs.at * BN + G::kCols * group);
-#pragma unroll
-        for (int i = 0; i < G::kCols / G::kLoad; ++i) {
-          uint32_t d[G::kLoad];
-          tmem_ld(at + G::kLoad * i, d);
-          wait_ld(d);
-#pragma unroll
-          for (int j = 0; j < G::kLoad / 2; ++j) {
-            f32x2 s;
-            if (SWAP)  // lane j of the scales is column j's
-              s = pack2(__shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j, 32),
-                        __shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j + 1, 32));
-            else
-              s = pack2(scale, scale);
-            f32x2& to = acc[G::kLoad / 2 * i + j];
-            to = fma2(pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, to);
-          }
-        }
-        tc_fence_before();
+        const float sa[2] = {s_scale[slots.at][0][own], s_scale[slots.at][1][own]};
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[bufs.at]);
-        bufs.next();
-      }
+        if (lane == 0) mbar_arrive(&sempty[slots.at]);
+        slots.next();
+        if (kb % 32 == 0) {
+          sb = sb_next;
+          if (kb + 32 < kblocks) fetch_b(kb + 32);
+        }
+        bool ok = true;
+#pragma unroll
+        for (int u = 0; u < 2; u += G::kUnit) {
+          if (kb + u >= kblocks) break;
+          ok = __all_sync(0xffffffffu, mbar_wait(&tfull[bufs.at], bufs.phase));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = tmem_addr(tmem, 32 * quad, bufs.at * (G::kUnit * BN) + G::kCols * group);
+          // one load ahead of the additions
+          constexpr int kPieces = G::kCols / G::kLoad;
+          uint32_t dd[2][G::kLoad];
+          tmem_ld(at, dd[0]);
+#pragma unroll
+          for (int p = 0; p < G::kUnit * kPieces; ++p) {
+            uint32_t(&d)[G::kLoad] = dd[p & 1];
+            const int e = p / kPieces, i = p % kPieces, q = p + 1;  // block of the unit, piece
+            // (past the last block the scales and the products are zeros)
+            const float scale =
+                wait_ld(sa[u + e] * __shfl_sync(0xffffffffu, sb, (kb + u + e) & 31));
+            if (q < G::kUnit * kPieces)
+              tmem_ld(at + BN * (q / kPieces) + G::kLoad * (q % kPieces), dd[q & 1]);
+#pragma unroll
+            for (int j = 0; j < G::kLoad / 2; ++j) {
+              f32x2 s;
+              if (SWAP)  // lane j of the scales is column j's
+                s = pack2(__shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j, 32),
+                          __shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j + 1, 32));
+              else
+                s = pack2(scale, scale);
+              f32x2& to = acc[G::kLoad / 2 * i + j];
+              to = fma2(pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, to);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[bufs.at]);
+          bufs.next();
+        }
+        if (!ok) {
+          if (lane == 0) timeout();
+          break;
+        }
       }
       if (s_abort) break;
       OutT* out = static_cast<OutT*>(a.out);
@@ -352,7 +408,7 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
         // or column, or, where out's rows do not allow one, a row at a time
         constexpr int kPiece = 128 / sizeof(OutT);
         static_assert(G::kCols % kPiece == 0, "whole pieces");
-        unsigned char* own = tiles + G::kStages * G::kStageBytes + 4096 * (warp - 2);
+        unsigned char* own = tiles + G::kStages * G::kStageBytes + 4096 * (warp - 4);
 #pragma unroll
         for (int p = 0; p < G::kCols / kPiece; ++p) {
           if (tma_out && lane == 0) bulk_wait_read();  // the piece before has left
@@ -417,20 +473,29 @@ EncodeTiledFn find_encode() {
   return nullptr;
 }
 
-// [rows, cols] elements of `size` bytes, rows `pitch` bytes apart, in boxes of 128 bytes x
-// `box` rows with the 128-byte swizzle.  Past the last row and column zeros
-// (e4m3 0.0) are read, and nothing is written.
-bool make_map(CUtensorMap* m, CUtensorMapDataType type, int64_t size, const void* base, int64_t rows,
-              int64_t cols, int64_t pitch, uint32_t box) {
+bool encode(CUtensorMap* m, CUtensorMapDataType type, uint32_t rank, const void* base,
+            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   static const EncodeTiledFn fn = find_encode();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / size), box};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, type, 2, const_cast<void*>(base), dims, strides, boxes, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn && fn(m, type, rank, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand's [rows, K] bytes, `box` rows of a k-block to a copy, 128-byte
+// swizzle.  Where K is whole blocks, as (byte of a block, row, block), and one
+// copy takes `unit` blocks; else as (byte of a row, row, 0): past the last row
+// and the last byte zeros (e4m3 0.0) are read.
+bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int64_t ld, uint32_t box,
+                 uint32_t unit) {
+  const bool whole = K % kBlockK == 0;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(whole ? kBlockK : K),
+                              static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(whole ? K / kBlockK : 1)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld),
+                                 static_cast<cuuint64_t>(whole ? kBlockK : 16)};
+  const cuuint32_t boxes[3] = {kBlockK, box, whole ? unit : 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, boxes);
 }
 
 template <int BN, bool SWAP, typename OutT>
@@ -440,17 +505,30 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   const int64_t rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;
   Maps maps;
   memset(&maps, 0, sizeof maps);
-  constexpr CUtensorMapDataType kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!make_map(&maps.rows, kBytes, 1, SWAP ? a.b : a.a, rows, a.K, SWAP ? a.ld_b : a.ld_a, kTileRows) ||
-      !make_map(&maps.cols, kBytes, 1, SWAP ? a.a : a.b, cols, a.K, SWAP ? a.ld_a : a.ld_b, BN))
+  const bool whole = a.K % kBlockK == 0;
+  if (!operand_map(&maps.rows, SWAP ? a.b : a.a, rows, a.K, SWAP ? a.ld_b : a.ld_a, kTileRows, G::kUnit) ||
+      !operand_map(&maps.cols, SWAP ? a.a : a.b, cols, a.K, SWAP ? a.ld_a : a.ld_b, BN, G::kUnit))
     return cudaErrorInvalidValue;
   constexpr int64_t kOut = sizeof(OutT);
   const bool tma_out = !SWAP && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
                        a.ld_out * kOut % 16 == 0;
-  if (tma_out && !make_map(&maps.out, kOut == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                           kOut, a.out, a.M, a.N, a.ld_out * kOut, 32))
-    return cudaErrorInvalidValue;
+  if (tma_out) {  // past the last row and column nothing is written
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.M)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ld_out * kOut)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / kOut), 32};
+    if (!encode(&maps.out, kOut == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                2, a.out, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
+  if (G::kShares) {
+    // a build that launches with fewer registers could never give the adding
+    // warps their share: it is not launched
+    static const int regs = [] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < G::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(G::kSmem));
   if (e != cudaSuccess) return e;
@@ -459,7 +537,7 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   const int64_t n = static_cast<int64_t>(tiles_r) * tiles_c;
   const int band = 12;  // of 152 tiles in flight, 12 x 12.7
   kern<<<static_cast<unsigned>(std::min<int64_t>(n, a.sm_count)), G::kThreads, G::kSmem, s>>>(
-      maps, a, tiles_r, tiles_c, band, tma_out);
+      maps, a, tiles_r, tiles_c, band, whole, tma_out);
   return cudaGetLastError();
 }
 

@@ -98,7 +98,6 @@ struct MatmulArgs {
   int64_t ld_a, ld_as, ld_b, ld_bs, ld_out;
   int32_t M, N, K;
   bool bf16;              // out's type
-  bool scale_vec;         // a_scale's rows start on 16-byte boundaries
   int sm_count;
   int* err;
 };

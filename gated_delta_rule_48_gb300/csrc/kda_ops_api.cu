@@ -401,7 +401,6 @@ extern "C" kda_status kda_matmul_fp8(const void* a, int64_t ld_a, const float* a
   m.ld_a = ld_a; m.ld_as = ld_a_scale; m.ld_b = ld_b; m.ld_bs = ld_b_scale; m.ld_out = ld_out;
   m.M = M; m.N = N; m.K = K;
   m.bf16 = out_dtype == KDA_BF16;
-  m.scale_vec = aligned(a_scale, 16) && (M == 1 || ld_a_scale % 4 == 0);
   KDA_TRY(device_sm_count(&m.sm_count));
   KDA_TRY(device_error_word(&m.err));
   return launched(launch_matmul_fp8(m, static_cast<cudaStream_t>(stream)), "product launch");
