@@ -536,12 +536,13 @@ def _rows(t, name, dtypes):
     with more leading dimensions that are one row stride apart."""
     if t is None:
         return None, 0, 0
-    dtype = t.dtype
-    if not t.is_cuda:
-        raise KdaError(1, f"{name} must be a CUDA tensor")
-    if dtype not in dtypes:
-        raise KdaError(1, f"{name} must be {' or '.join(map(str, dtypes))}, got {dtype}")
+    code = dtypes.get(t.dtype)
+    if code is None or not t.is_cuda:
+        raise KdaError(1, f"{name} must be a CUDA tensor of {' or '.join(map(str, dtypes))}, got "
+                          f"{t.dtype} on {t.device}")
     shape, stride = t.shape, t.stride()
+    if len(stride) == 2 and shape[0] > 1 and stride[1] == 1:  # the usual case
+        return t.data_ptr(), stride[0], code
     d = len(stride)
     if d < 2:
         raise KdaError(1, f"{name} must have at least 2 dimensions")
@@ -554,7 +555,7 @@ def _rows(t, name, dtypes):
         if shape[k] > 1 and stride[k] != ld * rows:
             raise KdaError(1, f"{name}: the leading dimensions must be one row stride apart")
         rows *= shape[k]
-    return t.data_ptr(), ld, KDA_DTYPE[dtype]
+    return t.data_ptr(), ld, code
 
 
 def _same_shape(t, shape, name):
@@ -584,39 +585,55 @@ def _vector(t, n, name):
     """(address, dtype code) of a contiguous bf16 or f32 vector of n elements, or of None."""
     if t is None:
         return None, 1
-    if not t.is_cuda or t.dtype not in _FLOATS:
+    code = _FLOATS.get(t.dtype)
+    if code is None or not t.is_cuda:
         raise KdaError(1, f"{name} must be a bfloat16 or float32 CUDA tensor")
-    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise KdaError(1, f"{name} must be a contiguous vector of {n} elements")
-    return t.data_ptr(), KDA_DTYPE[t.dtype]
+    return t.data_ptr(), code
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
-_E4M3 = (torch.float8_e4m3fn,)
-_F32 = (torch.float32,)
+def _only(dtype):
+    return {dtype: KDA_DTYPE[dtype]}
+
+
+_BF16, _F32, _E4M3 = _only(torch.bfloat16), _only(torch.float32), _only(torch.float8_e4m3fn)
+_FLOATS = _BF16 | _F32
+_SAME = {torch.bfloat16: _BF16, torch.float32: _F32}
+
+
+def _like(x, name="x"):
+    """The dtypes that tensors of x's dtype may have."""
+    same = _SAME.get(x.dtype)
+    if same is None:
+        raise KdaError(1, f"{name} must be bfloat16 or float32, got {x.dtype}")
+    return same
 
 
 def _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, quant):
-    dim, shape = x.shape[-1], x.shape
+    same, shape = _like(x), x.shape
+    dim = shape[-1]
     rows = x.numel() // max(dim, 1)
-    xp, ld_x, dt = _rows(x, "x", _FLOATS)
-    rp, ld_r, _ = _rows(residual, "residual", (x.dtype,))
-    _same_shape(residual, shape, "residual")
+    xp, ld_x, dt = _rows(x, "x", same)
     wp, w_dt = _vector(weight, dim, "weight")
+    rp = hp = sp = None
+    ld_r = ld_h = ld_s = 0
+    if residual is not None:
+        _same_shape(residual, shape, "residual")
+        rp, ld_r, _ = _rows(residual, "residual", same)
     if residual is not None or h is not None:
         h = _out(h, "h", shape, x.dtype, x, stream)
-    hp, ld_h, _ = _rows(h, "h", (x.dtype,))
-    sp, ld_s = None, 0
+        hp, ld_h, _ = _rows(h, "h", same)
     if quant:
         if y is None:  # rows at multiples of 16 bytes, as kda_matmul_fp8 reads them
             pad = -dim % 16
-            y = _out(None, "y", (*shape[:-1], dim + pad), _E4M3[0], x, stream)
+            y = _out(None, "y", (*shape[:-1], dim + pad), torch.float8_e4m3fn, x, stream)
             y = y[..., :dim] if pad else y
         y_scale = _out(y_scale, "y_scale", (*shape[:-1], (dim + 127) // 128), torch.float32, x,
                        stream)
         sp, ld_s, _ = _rows(y_scale, "y_scale", _F32)
     y = _out(y, "y", shape, x.dtype, x, stream)
-    yp, ld_y, y_dt = _rows(y, "y", _E4M3 if quant else (x.dtype,))
+    yp, ld_y, y_dt = _rows(y, "y", _E4M3 if quant else same)
     _check(load().kda_add_rms_norm(xp, ld_x, rp, ld_r, wp, hp, ld_h, yp, ld_y, sp, ld_s, rows, dim,
                                    eps, dt, w_dt, y_dt, _handle(stream, x)))
     return y, y_scale, h
@@ -669,8 +686,9 @@ def _dense(t, shape, dtype, name):
     """The address of a contiguous CUDA tensor of that shape and dtype, or None."""
     if t is None:
         return None
-    _require(t, dtype, name)
-    _same_shape(t, shape, name)
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _require(t, dtype, name)
+        _same_shape(t, shape, name)
     return t.data_ptr()
 
 
@@ -678,11 +696,9 @@ def _conv_weights(x, weight, bias):
     dim = x.shape[-1]
     if weight.dim() != 2 or weight.shape[0] != dim:
         raise KdaError(1, f"weight must have the shape ({dim}, width), got {tuple(weight.shape)}")
-    if weight.dtype not in _FLOATS:
-        raise KdaError(1, f"weight must be bfloat16 or float32, got {weight.dtype}")
-    _require(weight, weight.dtype, "weight")
-    return (weight.data_ptr(), _dense(bias, (dim,), weight.dtype, "bias"), weight.shape[1],
-            KDA_DTYPE[weight.dtype])
+    _like(weight, "weight")
+    return (_dense(weight, weight.shape, weight.dtype, "weight"),
+            _dense(bias, (dim,), weight.dtype, "bias"), weight.shape[1], KDA_DTYPE[weight.dtype])
 
 
 def _sequences(x, cu_seqlens, n_seqs):
@@ -708,7 +724,7 @@ def kda_short_conv_fwd(x, weight, bias=None, conv_state=None, cu_seqlens=None, *
     wp, bp, width, w_dt = _conv_weights(x, weight, bias)
     shape = (N, width - 1, x.shape[-1])
     y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
     if want_state or state_out is not None:
         state_out = _out(state_out, "state_out", shape, x.dtype, x, stream)
     _check(load().kda_short_conv_fwd(xp, ld_x, wp, bp, _dense(conv_state, shape, x.dtype, "conv_state"),
@@ -725,7 +741,7 @@ def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, 
     xp, ld_x, dt = _rows(x, "x", _FLOATS)
     wp, bp, width, w_dt = _conv_weights(x, weight, bias)
     y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
     _check(load().kda_short_conv_step(xp, ld_x, wp, bp,
                                       _dense(conv_state, (N, width - 1, dim), x.dtype, "conv_state"),
                                       yp, ld_y, N, dim, width, 1 if silu else 0, dt, w_dt,
@@ -741,7 +757,8 @@ def _groups_of(t, x, name):
     groups, state = t.shape[-2:]
     if groups > 1 and t.stride(-2) != state:
         raise KdaError(1, f"{name}: the groups of a token must be dense")
-    return _rows(t.select(-2, 0) if groups > 0 else t, name, (x.dtype,))[:2]
+    p, ld, _ = _rows(t.select(-2, 0) if groups != 0 else t, name, _SAME[x.dtype])
+    return p, ld
 
 
 def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
@@ -750,8 +767,9 @@ def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
     dim = x.shape[-1]
     for t, name in ((dt, "dt"), (z, "z")):
         _same_shape(t, x.shape, name)
-    dtp, ld_dt, _ = _rows(dt, "dt", (x.dtype,))
-    zp, ld_z, _ = _rows(z, "z", (x.dtype,))
+    same = _SAME[x.dtype]
+    dtp, ld_dt, _ = _rows(dt, "dt", same)
+    zp, ld_z, _ = _rows(z, "z", same)
     bp, ld_b = _groups_of(B, x, "B")
     cp, ld_c = _groups_of(C, x, "C")
     _same_shape(C, B.shape, "C")
@@ -775,7 +793,7 @@ def kda_ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_s
     T, N, cu = _sequences(x, cu_seqlens, n_seqs)
     args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
     y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
     shape = (N, dim, state)
     if want_state or h_final is not None:
         h_final = _out(h_final, "h_final", shape, torch.float32, x, stream)
@@ -792,7 +810,7 @@ def kda_ssm_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softpl
     args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
     N = x.shape[0]
     y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", (x.dtype,))
+    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
     _check(load().kda_ssm_scan_step(*args, _dense(h, (N, dim, state), torch.float32, "h"), yp, ld_y,
                                     N, dim, state, groups, 1 if softplus else 0, code,
                                     _handle(stream, x)))

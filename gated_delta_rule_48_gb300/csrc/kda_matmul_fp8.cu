@@ -43,6 +43,22 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// All threads of the cluster's blocks; shared memory written before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A float at this block's shared address `at`, but of block `rank` of the cluster.
+__device__ __forceinline__ float load_of_block(uint32_t at, int rank) {
+  float v;
+  asm volatile(
+      "{\n .reg .b32 t;\n mapa.shared::cluster.u32 t, %1, %2;\n ld.shared::cluster.f32 %0, [t];\n}"
+      : "=f"(v)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // One lane of the warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t is;
@@ -77,6 +93,10 @@ __device__ __forceinline__ float wait_ld(float v) {
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]) : "r"(taddr));
+}
+
 // A warp's rows of the output through its own piece of shared memory, 128
 // bytes of each of 32 rows at a time, in the layout of a 128-byte-swizzled
 // tensor copy.
@@ -97,7 +117,7 @@ struct Shape {
   // fills up their set of four (register shares go by sets), then the adding warps
   static constexpr int kThreads = 128 + 128 * kGroups;
   // 128 sums a thread: the first set gives registers to the others (launched
-  // with 168 each, 3 * 168 = 56 + 2 * 224)
+  // with 168 each, 3 * 168 = 40 + 2 * 232)
   static constexpr bool kShares = kCols == 128;
   static constexpr int kLaunchRegs = 168, kAddRegs = 224, kRestRegs = 56;
   static_assert(!kShares || 128 * (kRestRegs + kGroups * kAddRegs) <= kThreads * kLaunchRegs,
@@ -105,17 +125,19 @@ struct Shape {
   // k-blocks that are copied, multiplied and handed over together: one block's
   // products of a narrow tile take less time than the waits around them
   static constexpr int kUnit = BN == 256 ? 1 : 2;
-  static constexpr int kBufs = BN >= 128 ? 2 : 4;          // of tensor memory, a unit each
+  static constexpr int kBufs = BN >= 128 ? 2 : 4;           // of tensor memory, a unit each
   static constexpr uint32_t kTmemCols = BN * kUnit * kBufs;
   static constexpr uint32_t kRowBytes = kUnit * kTileRows * kBlockK, kColBytes = kUnit * BN * kBlockK;
   static constexpr uint32_t kStageBytes = kRowBytes + kColBytes;
-  static constexpr int kStages = BN == 128 ? 3 : BN == 256 || BN == 64 ? 4 : 5;
-  static constexpr int kLoad = kCols % 32 == 0 && kCols < 128 ? 32 : 16;  // columns per tensor-memory load
+  static constexpr int kStages = SWAP ? (BN == 64 ? 4 : 5) : BN == 128 ? 3 : 4;
+  // columns per tensor-memory load: as many as there are registers for
+  static constexpr int kLoad = kCols == 128 ? 64 : kCols % 32 == 0 && !SWAP ? 32 : 16;
   static constexpr int kOwn = SWAP ? BN : kTileRows;       // rows of A in a tile
   static constexpr uint32_t kStoreBytes = SWAP ? 0 : 4 * kGroups * 4096;  // a piece per adding warp
   static constexpr uint32_t kSmem = kStages * kStageBytes + kStoreBytes;
   // with the scales and barriers in front of it, up to the next 1024 bytes
-  static_assert(kSmem + (4 * kOwn * 4 + 256 + 1023) / 1024 * 1024 <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kFront = (4 * kOwn * 4 + 256 + 1023) / 1024 * 1024;
+  static_assert(kSmem + kFront <= 227 * 1024 && kTmemCols <= 512, "memory of an SM");
   static_assert(kCols % 16 == 0, "whole loads");
 };
 
@@ -140,7 +162,7 @@ struct Maps {
 template <int BN, bool SWAP, typename OutT>
 __global__ void __launch_bounds__(Shape<BN, SWAP>::kThreads, 1)
 matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int tiles_c, int band,
-              bool whole, bool tma_out) {
+              int cluster, bool whole, bool tma_out) {
   using G = Shape<BN, SWAP>;
   extern __shared__ __align__(1024) unsigned char tiles[];
   __shared__ uint64_t full[G::kStages], empty[G::kStages], tfull[G::kBufs], tempty[G::kBufs];
@@ -152,6 +174,12 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kblocks = (a.K + kBlockK - 1) / kBlockK, units = (kblocks + G::kUnit - 1) / G::kUnit;
   const int64_t n_tiles = static_cast<int64_t>(tiles_r) * tiles_c;
+  // a cluster of blocks shares a tile's k-blocks (SWAP), each its own units
+  const int splits = SWAP ? cluster : 1, rank = blockIdx.x % splits;
+  const int unit0 = SWAP ? static_cast<int>(static_cast<int64_t>(units) * rank / splits) : 0;
+  const int unit1 = SWAP ? static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / splits) : units;
+  const int kb0 = unit0 * G::kUnit, kb1 = SWAP ? min(unit1 * G::kUnit, kblocks) : kblocks;
+  const int64_t tile0 = blockIdx.x / splits, tile_step = gridDim.x / splits;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
@@ -194,10 +222,10 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
     if (warp == 0) {
       Ring<G::kStages> ring;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+      for (int64_t t = tile0; t < n_tiles && ok; t += tile_step) {
         int r, c;
         tile_at(t, r, c);
-        for (int u = 0; u < units; ++u) {
+        for (int u = unit0; u < unit1; ++u) {
           // (a wait for the round before the first one passes at once)
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[ring.at], ring.phase ^ 1));
           if (!ok) break;
@@ -235,7 +263,7 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       Ring<G::kStages> ring;
       Ring<G::kBufs> bufs;
       const uint32_t n_units =
-          static_cast<uint32_t>((n_tiles - blockIdx.x + gridDim.x - 1) / gridDim.x) * units;
+          static_cast<uint32_t>((n_tiles - tile0 + tile_step - 1) / tile_step) * (unit1 - unit0);
       bool ok = true;
       uint32_t i = 0;
       for (; i < n_units; ++i) {
@@ -274,11 +302,11 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       const int64_t n_as = (a.M - 1) * a.ld_as + kblocks;
       Ring<2> slots;
       bool ok = true;
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+      for (int64_t t = tile0; t < n_tiles && ok; t += tile_step) {
         int r, c;
         tile_at(t, r, c);
         const int64_t m0 = static_cast<int64_t>(SWAP ? c : r) * G::kOwn;
-        for (int kb = 0; kb < kblocks; kb += 2) {
+        for (int kb = kb0; kb < kb1; kb += 2) {
           constexpr int kRows = (G::kOwn + 31) / 32;  // per lane
           float v[kRows][2];
 #pragma unroll
@@ -309,14 +337,14 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
     const int quad = warp & 3, group = (warp - 4) >> 2;
     Ring<G::kBufs> bufs;
     Ring<2> slots;
-    for (int64_t t = blockIdx.x; t < n_tiles && !s_abort; t += gridDim.x) {
+    for (int64_t t = tile0; t < n_tiles && !s_abort; t += tile_step) {
       int r, c;
       tile_at(t, r, c);
       const int64_t row = static_cast<int64_t>(r) * kTileRows + 32 * quad + lane;
       const int64_t col0 = static_cast<int64_t>(c) * BN + G::kCols * group;
-      f32x2 acc[G::kCols / 2];
+      float acc[G::kCols];
 #pragma unroll
-      for (int i = 0; i < G::kCols / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < G::kCols; ++i) acc[i] = 0.f;
       // The scale of B's 128 rows that this thread's products share, one block
       // in each lane, fetched 32 blocks ahead; A's come through shared memory.
       const int64_t n_bs = ((a.N + kScaleGroup - 1) / kScaleGroup - 1) * a.ld_bs + kblocks;
@@ -329,10 +357,10 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
         if (n_in && kb + lane < kblocks && kda_guard(pb - a.b_scale + kb + lane, 1, n_bs, a.err))
           sb_next = pb[kb + lane];
       };
-      fetch_b(0);
+      fetch_b(kb0);
       // this thread's row of A; SWAP: column `lane` of its columns
       const int own = SWAP ? G::kCols * group + lane % G::kCols : 32 * quad + lane;
-      for (int kb = 0; kb < kblocks; kb += 2) {
+      for (int kb = kb0; kb < kb1; kb += 2) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sfull[slots.at], slots.phase))) {
           if (lane == 0) timeout();
           break;
@@ -341,41 +369,45 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[slots.at]);
         slots.next();
-        if (kb % 32 == 0) {
+        if ((kb - kb0) % 32 == 0) {
           sb = sb_next;
           if (kb + 32 < kblocks) fetch_b(kb + 32);
         }
         bool ok = true;
 #pragma unroll
         for (int u = 0; u < 2; u += G::kUnit) {
-          if (kb + u >= kblocks) break;
+          if (kb + u >= kb1) break;
           ok = __all_sync(0xffffffffu, mbar_wait(&tfull[bufs.at], bufs.phase));
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tmem_addr(tmem, 32 * quad, bufs.at * (G::kUnit * BN) + G::kCols * group);
-          // one load ahead of the additions
+          // One set of registers for all the loads: with two, to load ahead of
+          // the additions, the kernel was 20 % slower.
           constexpr int kPieces = G::kCols / G::kLoad;
           uint32_t dd[2][G::kLoad];
           tmem_ld(at, dd[0]);
 #pragma unroll
           for (int p = 0; p < G::kUnit * kPieces; ++p) {
-            uint32_t(&d)[G::kLoad] = dd[p & 1];
-            const int e = p / kPieces, i = p % kPieces, q = p + 1;  // block of the unit, piece
+            const int e = p / kPieces, i = p % kPieces;  // block of the unit, piece of its columns
+            uint32_t(&d)[G::kLoad] = dd[0];
+            if (p > 0) tmem_ld(at + BN * e + G::kLoad * i, d);
             // (past the last block the scales and the products are zeros)
             const float scale =
-                wait_ld(sa[u + e] * __shfl_sync(0xffffffffu, sb, (kb + u + e) & 31));
-            if (q < G::kUnit * kPieces)
-              tmem_ld(at + BN * (q / kPieces) + G::kLoad * (q % kPieces), dd[q & 1]);
+                wait_ld(sa[u + e] * __shfl_sync(0xffffffffu, sb, (kb - kb0 + u + e) & 31));
 #pragma unroll
-            for (int j = 0; j < G::kLoad / 2; ++j) {
-              f32x2 s;
-              if (SWAP)  // lane j of the scales is column j's
-                s = pack2(__shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j, 32),
-                          __shfl_sync(0xffffffffu, scale, G::kLoad * i + 2 * j + 1, 32));
-              else
-                s = pack2(scale, scale);
-              f32x2& to = acc[G::kLoad / 2 * i + j];
-              to = fma2(pack2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1])), s, to);
+            for (int j = 0; j < G::kLoad; j += 2) {
+              // SWAP: lane j of the scales is column j's
+              const float s0 = SWAP ? __shfl_sync(0xffffffffu, scale, G::kLoad * i + j, 32) : scale;
+              const float s1 = SWAP ? __shfl_sync(0xffffffffu, scale, G::kLoad * i + j + 1, 32) : scale;
+              float& lo = acc[G::kLoad * i + j];
+              float& hi = acc[G::kLoad * i + j + 1];
+              const float d0 = __uint_as_float(d[j]), d1 = __uint_as_float(d[j + 1]);
+              if constexpr (G::kCols == 128) {  // (single additions: 6 % faster here)
+                lo = fmaf(d0, s0, lo);
+                hi = fmaf(d1, s1, hi);
+              } else {
+                unpack2(fma2(pack2(d0, d1), pack2(s0, s1), pack2(lo, hi)), lo, hi);
+              }
             }
           }
           tc_fence_before();
@@ -391,12 +423,14 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       if (s_abort) break;
       OutT* out = static_cast<OutT*>(a.out);
       const int64_t extent = (a.M - 1) * a.ld_out + a.N;
-      auto value = [&](int i) {
-        float lo, hi;
-        unpack2(acc[i / 2], lo, hi);
-        return i & 1 ? hi : lo;
-      };
+      auto value = [&](int i) { return acc[i]; };
       if constexpr (SWAP) {  // a thread holds one row of B for some rows of A
+        if (splits > 1) {  // (every copy and product of this block is done)
+#pragma unroll
+          for (int i = 0; i < G::kCols; ++i)
+            reinterpret_cast<float*>(tiles)[(G::kCols * group + i) * kTileRows + 32 * quad + lane] = value(i);
+          break;
+        }
 #pragma unroll
         for (int i = 0; i < G::kCols; ++i) {
           const int64_t m = col0 + i, e = m * a.ld_out + row;
@@ -450,6 +484,29 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       }
     }
     if (!SWAP && tma_out && lane == 0) bulk_wait();  // the block's memory outlives its copies
+  }
+  if constexpr (SWAP) {
+    if (splits > 1) {
+      // The blocks' sums lie in their shared memory; each block adds up some of
+      // the columns, the blocks' parts in order.
+      __syncwarp();
+      cluster_sync();
+      int r, c;
+      tile_at(tile0, r, c);
+      const int first = BN * rank / splits, last = BN * (rank + 1) / splits;
+      const int64_t extent = (a.M - 1) * a.ld_out + a.N;
+      for (int i = first * kTileRows + threadIdx.x; i < last * kTileRows; i += G::kThreads) {
+        const int64_t m = static_cast<int64_t>(c) * BN + i / kTileRows;
+        const int64_t n = static_cast<int64_t>(r) * kTileRows + i % kTileRows, e = m * a.ld_out + n;
+        const uint32_t at = smem_u32(tiles) + 4 * i;
+        float sum = 0.f;
+        for (int q = 0; q < splits; ++q) sum += load_of_block(at, q);
+        if (m < a.M && n < a.N && kda_guard(e, 1, extent, a.err))
+          static_cast<OutT*>(a.out)[e] = from_f32<OutT>(sum);
+      }
+      __syncwarp();
+      cluster_sync();  // no block's memory goes while another reads it
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -535,17 +592,34 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   const int tiles_r = static_cast<int>((rows + kTileRows - 1) / kTileRows);
   const int tiles_c = static_cast<int>((cols + BN - 1) / BN);
   const int64_t n = static_cast<int64_t>(tiles_r) * tiles_c;
+  const int64_t slots = a.sm_count;
   const int band = 12;  // of 152 tiles in flight, 12 x 12.7
-  kern<<<static_cast<unsigned>(std::min<int64_t>(n, a.sm_count)), G::kThreads, G::kSmem, s>>>(
-      maps, a, tiles_r, tiles_c, band, whole, tma_out);
-  return cudaGetLastError();
+  // Few tiles: a cluster of up to 8 blocks shares each one's k-blocks, as long
+  // as all are resident and a block has two copies to overlap.
+  int splits = 1;
+  const int units = ((a.K + kBlockK - 1) / kBlockK + G::kUnit - 1) / G::kUnit;
+  if (SWAP)
+    while (splits < 8 && 2 * splits * n <= slots && units >= 4 * splits) splits *= 2;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? n * splits : std::min(n, slots)));
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = static_cast<unsigned>(splits);
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, tiles_r, tiles_c, band, splits, whole, tma_out);
 }
 
 template <typename OutT>
 cudaError_t choose(const MatmulArgs& a, cudaStream_t s) {
   if (a.M <= 16) return run<16, true, OutT>(a, s);
   if (a.M <= 32) return run<32, true, OutT>(a, s);
-  if (a.M <= 64) return run<64, true, OutT>(a, s);
+  if (a.M <= 128) return run<64, true, OutT>(a, s);
   const int64_t row_tiles = (a.M + kTileRows - 1) / kTileRows;
   // the widest tile of which there are enough for every SM
   if (row_tiles * ((a.N + 255) / 256) >= a.sm_count) return run<256, false, OutT>(a, s);
