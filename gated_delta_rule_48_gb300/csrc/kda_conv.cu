@@ -20,7 +20,7 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvBatch = 4;  // rows whose loads are issued together
+constexpr int kConvBatch = 8;  // rows whose loads are issued together, a batch ahead
 
 template <typename T, int VEC, int W>
 struct Taps {
@@ -31,7 +31,7 @@ struct Taps {
     auto any = [&](const void* p, int64_t i) {
       return a.w_bf16 ? to_f32(static_cast<const Bf16*>(p)[i]) : static_cast<const float*>(p)[i];
     };
-    if (VEC > 1 && a.w_bf16 == (sizeof(T) == 2)) {  // W vectors of VEC consecutive weights
+    if (VEC > 1 && a.w_bf16 == (sizeof(T) == 2)) {  // W vectors of VEC weights
       const T* p = static_cast<const T*>(a.weight) + static_cast<int64_t>(c0) * W;
 #pragma unroll
       for (int j = 0; j < W; ++j) {
@@ -96,7 +96,8 @@ __device__ __forceinline__ void store_y(const ConvArgs& a, int64_t t, int c0, co
 
 // One strip of tokens, for this thread's channels.
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void conv_strip(const ConvArgs& a, int64_t t, int64_t t_end, int c0) {
+__device__ __forceinline__ void conv_strip(const ConvArgs& a, const int64_t t0, int64_t t_end, int c0) {
+  int64_t t = t0;
   Taps<T, VEC, W> taps;
   taps.load(a, c0);
   int32_t n = a.cu ? sequence_of(a.cu, a.N, t, a.err) : static_cast<int32_t>(t / (a.T / a.N));
@@ -109,14 +110,14 @@ __device__ __forceinline__ void conv_strip(const ConvArgs& a, int64_t t, int64_t
     if (pos >= start) load_x<T, VEC>(a, pos, c0, rows[j]);
     else load_before<T, VEC, W>(a, n, static_cast<int>(min(start - pos, int64_t{W - 1})), c0, rows[j]);
   }
-  auto token = [&](int64_t at, const float (&x)[VEC]) {
+  auto token = [&](T* to, const float (&x)[VEC]) {
     float y[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       rows[W - 1][i] = x[i];
       y[i] = taps.at(i, rows, a.silu);
     }
-    store_y<T, VEC>(a, at, c0, y);
+    if (kda_guard(to - static_cast<T*>(a.y), VEC, (a.T - 1) * a.ld_y + a.dim, a.err)) store_n<VEC>(to, y);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -124,19 +125,38 @@ __device__ __forceinline__ void conv_strip(const ConvArgs& a, int64_t t, int64_t
   };
   while (true) {
     const int64_t stop = min(end, t_end);
+    // Whole batches, a batch's loads ahead; their rows' places by addition.
+    RawVec<T, VEC> next[kConvBatch];
+    const T* px = static_cast<const T*>(a.x) + t * a.ld_x + c0;
+    T* py = static_cast<T*>(a.y) + t * a.ld_y + c0;
+    auto fetch = [&]() {
+#pragma unroll
+      for (int b = 0; b < kConvBatch; ++b, px += a.ld_x)
+        if (kda_guard(px - static_cast<const T*>(a.x), VEC, (a.T - 1) * a.ld_x + a.dim, a.err))
+          next[b].load(px);
+    };
+    if (t + kConvBatch <= stop) fetch();
     for (; t + kConvBatch <= stop; t += kConvBatch) {
-      float x[kConvBatch][VEC];
+      RawVec<T, VEC> now[kConvBatch];
 #pragma unroll
-      for (int b = 0; b < kConvBatch; ++b) load_x<T, VEC>(a, t + b, c0, x[b]);
+      for (int b = 0; b < kConvBatch; ++b) now[b] = next[b];
+      if (t + 2 * kConvBatch <= stop) fetch();
 #pragma unroll
-      for (int b = 0; b < kConvBatch; ++b) token(t + b, x[b]);
+      for (int b = 0; b < kConvBatch; ++b, py += a.ld_y) {
+        float x[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = now[b].get(i);
+        token(py, x);
+      }
     }
-    for (; t < stop; ++t) {
-      float x[VEC];
-      load_x<T, VEC>(a, t, c0, x);
-      token(t, x);
+    for (; t < stop; ++t, px += a.ld_x, py += a.ld_y) {
+      float x[VEC] = {};
+      if (kda_guard(px - static_cast<const T*>(a.x), VEC, (a.T - 1) * a.ld_x + a.dim, a.err))
+        load_n<VEC>(px, x);
+      token(py, x);
     }
-    if (t >= t_end) return;
+    if (stop >= t_end) return;
+    t = max(stop, t0);
     do {  // the next sequence that has tokens
       if (++n >= a.N) return;
       sequence_span(a.cu, a.N, a.T, n, start, end, a.err);
@@ -260,8 +280,11 @@ cudaError_t run_width(const ConvArgs& a, bool step, cudaStream_t s) {
 }
 
 cudaError_t run_types(const ConvArgs& a, bool step, cudaStream_t s) {
-  if (a.bf16) return a.vec ? run_width<Bf16, 8>(a, step, s) : run_width<Bf16, 1>(a, step, s);
-  return a.vec ? run_width<float, 4>(a, step, s) : run_width<float, 1>(a, step, s);
+  switch (a.vec) {
+    case 4: return a.bf16 ? run_width<Bf16, 4>(a, step, s) : run_width<float, 4>(a, step, s);
+    case 2: return a.bf16 ? run_width<Bf16, 2>(a, step, s) : run_width<float, 2>(a, step, s);
+  }
+  return a.bf16 ? run_width<Bf16, 1>(a, step, s) : run_width<float, 1>(a, step, s);
 }
 
 }  // namespace

@@ -470,8 +470,8 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
             }
           } else {
             __syncwarp();
-#pragma unroll 1
-            for (int i = 0; i < 32 && r_at + i < a.M; ++i)
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i)
 #pragma unroll
               for (int k = 0; k < kPiece; k += 32) {
                 const int64_t e = (r_at + i) * a.ld_out + c_at + k + lane;

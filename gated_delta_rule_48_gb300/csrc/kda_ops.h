@@ -49,7 +49,7 @@ struct ConvArgs {
   int64_t ld_x, ld_y, T;
   int32_t N, dim, width;
   bool bf16, w_bf16, silu;
-  bool vec;               // rows start on 16-byte boundaries and hold whole vectors
+  int vec;                // channels that can be read and written at a time: 4, 2 or 1
   int sm_count;
   int* err;
 };
@@ -156,29 +156,72 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// N consecutive elements, aligned to their total size (at most 16 bytes a load).
+// N (1, 2 or 4) consecutive elements, aligned to their total size, in the
+// registers they were loaded into: taking two bf16 values of one register
+// apart, or widening one, would wait for the load.
+template <typename T, int N>
+struct RawVec;
+template <>
+struct RawVec<Bf16, 1> {
+  Bf16 v;
+  __device__ __forceinline__ void load(const Bf16* p) { v = *p; }
+  __device__ __forceinline__ float get(int) const { return to_f32(v); }
+};
+template <>
+struct RawVec<Bf16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const Bf16* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float(i ? v & 0xffff0000u : v << 16);
+  }
+};
+template <>
+struct RawVec<Bf16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const Bf16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct RawVec<float, 1> {
+  float v;
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
+  __device__ __forceinline__ float get(int) const { return v; }
+};
+template <>
+struct RawVec<float, 2> {
+  float2 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+  __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
+};
+template <>
+struct RawVec<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+  }
+};
 template <int N, typename T>
 __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = to_f32(*p);
-  } else if constexpr (N == 8) {
-    load8(p, v);
-  } else {
-    static_assert(N == 4 && sizeof(T) == 4, "four 32-bit elements");
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  }
+  RawVec<T, N> r;
+  r.load(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = r.get(i);
 }
-template <int N, typename T>
-__device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
-  if constexpr (N == 1) {
-    *p = from_f32<T>(v[0]);
-  } else if constexpr (N == 8) {
-    store8(p, v);
-  } else {
-    static_assert(N == 4 && sizeof(T) == 4, "four 32-bit elements");
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
+template <int N>
+__device__ __forceinline__ void store_n(Bf16* p, const float (&v)[N]) {
+  if constexpr (N == 1) *p = from_f32<Bf16>(v[0]);
+  else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack2_bf16(v[0], v[1]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float (&v)[N]) {
+  if constexpr (N == 1) *p = v[0];
+  else if constexpr (N == 2) *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // The sequence of packed token t: the first n with cu[n + 1] > t (at most N - 1).
@@ -228,16 +271,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Four consecutive elements, aligned to their total size.
-__device__ __forceinline__ void load4(const Bf16* p, float (&v)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) { load_n<4>(p, v); }
-
 // Two values to e4m3, round to nearest even, clamped to +-448 (NaN stays NaN).
 __device__ __forceinline__ uint16_t pack2_e4m3(float lo, float hi) {
   uint16_t r;
@@ -266,8 +299,19 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
-// v * sigmoid(v).  The approximate exponential and quotient are within a few
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// v sigmoid(v).  The approximate exponential and reciprocal are within a few
 // units of the last place of the 32-bit result.
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.0f + ex2(v * -kLog2e)); }
 
 }  // namespace kda

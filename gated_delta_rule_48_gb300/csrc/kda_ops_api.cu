@@ -211,9 +211,14 @@ static kda_status check_conv(const void* x, int64_t ld_x, const void* weight, co
   a.cu = cu; a.y = const_cast<void*>(y);
   a.ld_x = ld_x; a.ld_y = ld_y; a.T = T; a.N = N; a.dim = dim; a.width = width;
   a.bf16 = dtype == KDA_BF16; a.w_bf16 = w_dtype == KDA_BF16;
-  a.vec = static_cast<int64_t>(dim) * es % 16 == 0 && ld_x * es % 16 == 0 && ld_y * es % 16 == 0 &&
-          aligned(x, 16) && aligned(y, 16) && aligned(weight, 16) && aligned(state_in, 16) &&
-          aligned(state_out, 16);
+  a.vec = 4;
+  auto fits = [&](int v) {
+    const uintptr_t to = static_cast<uintptr_t>(v * es);
+    return dim % v == 0 && ld_x % v == 0 && ld_y % v == 0 && aligned(x, to) && aligned(y, to) &&
+           aligned(state_in, to) && aligned(state_out, to) &&
+           aligned(weight, static_cast<uintptr_t>(v * ws));
+  };
+  while (a.vec > 1 && !fits(a.vec)) a.vec /= 2;
   KDA_TRY(device_sm_count(&a.sm_count));
   return device_error_word(&a.err);
 }

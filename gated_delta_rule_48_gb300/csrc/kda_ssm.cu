@@ -44,7 +44,6 @@ namespace kda {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLanes = 4;            // lanes per channel, and tokens taken together
 constexpr int kScanThreads = 128;
 // Channels per lane: each value of B and C read from shared memory serves them
@@ -53,21 +52,10 @@ constexpr int kChannelsOf(int state) { return state <= 64 ? 2 : 1; }
 // Blocks per SM that the registers are divided among.
 constexpr int scan_blocks_per_sm(int state) { return state <= 16 ? 3 : 2; }
 
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
   float lo, hi;
   unpack2(v, lo, hi);
   return pack2(ex2(lo), ex2(hi));
-}
-
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1].  With
@@ -83,8 +71,6 @@ __device__ __forceinline__ float softplus(float v) {
   p = fmaf(q, p, 2.0f / 3.0f);
   return fmaxf(v, 0.0f) + fmaf(s * q, p, s + s);
 }
-// v sigmoid(v)
-__device__ __forceinline__ float gate(float v) { return v * rcp(1.0f + ex2(v * -kLog2e)); }
 
 // Four values of B (and of C behind them) from shared memory.
 template <bool BOTH>
@@ -393,7 +379,7 @@ struct Scan {
           if (kLanes * b + lane4 < n) sum_dt[k] += d[k];
         } else {
           ny[b][k] = skip[k] * x;
-          ng[b][k] = a.z ? gate(nz[b].get(k)) : 1.0f;
+          ng[b][k] = a.z ? silu(nz[b].get(k)) : 1.0f;
         }
       }
       float* to = du + (kLanes * b + lane4) * kDuRow;
@@ -589,49 +575,52 @@ ssm_scan_kernel(SsmArgs a, int n_cb, int cb_per_group) {
 
 // One token of each sequence, h in place.  S / 4 lanes per channel, four
 // values each, so that the states are read and written in whole rows; bound by
-// those bytes.
+// those bytes.  A block's sequence comes from the grid: found by division of a
+// 64-bit index, it cost half of the instructions.
+constexpr int kStepThreads = 256;
 template <typename T, int S, bool VEC>
-__global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 2048 / kStepThreads) ssm_step_kernel(SsmArgs a) {
   constexpr int kPer = S / 4;  // lanes per channel
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t units = static_cast<int64_t>(a.N) * a.dim;
-  const bool live = i / kPer < units;
-  const int64_t unit = live ? i / kPer : units - 1;  // (sequence, channel)
-  const int lane = static_cast<int>(i % kPer);
-  const int64_t n = unit / a.dim, c = unit % a.dim;
-  const int64_t g = c / (a.dim / a.groups);
-  const int64_t states = units * S, at = unit * S + 4 * lane;
-  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (kda_guard(at, 4, states, a.err)) h = *reinterpret_cast<const float4*>(a.h0 + at);
-  float A[4], B[4], C[4];
-  const int64_t gs = static_cast<int64_t>(a.groups) * S, in_row = g * S + 4 * lane;
+  const int lane = threadIdx.x % kPer;
+  const int c_own = blockIdx.x * (kStepThreads / kPer) + threadIdx.x / kPer;
+  const bool live = c_own < a.dim;
+  const int c = live ? c_own : a.dim - 1;  // (whole warps take part in the sums)
+  const int g = c / (a.dim / a.groups);
+  const int64_t n = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (n >= a.N) return;  // (the whole block)
+  const int64_t states = static_cast<int64_t>(a.N) * a.dim * S, gs = static_cast<int64_t>(a.groups) * S;
   auto load = [&](const auto* p, int64_t e, int64_t extent, float(&v)[4]) {
     if (VEC && kda_guard(e, 4, extent, a.err)) {
-      load4(p + e, v);
+      load_n<4>(p + e, v);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = !VEC && kda_guard(e + j, 1, extent, a.err) ? to_f32(p[e + j]) : 0.f;
     }
   };
-  load(a.A, c * S + 4 * lane, static_cast<int64_t>(a.dim) * S, A);
-  load(static_cast<const T*>(a.B), n * a.ld_b + in_row, (a.N - 1) * a.ld_b + gs, B);
-  load(static_cast<const T*>(a.C), n * a.ld_c + in_row, (a.N - 1) * a.ld_c + gs, C);
+  const int64_t at = (n * a.dim + c) * S + 4 * lane;
+  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (kda_guard(at, 4, states, a.err)) h = *reinterpret_cast<const float4*>(a.h0 + at);
   const float x = element<T>(a.x, n, a.ld_x, c, true, a);
   float dt = element<T>(a.dt, n, a.ld_dt, c, true, a);
-  if (a.dt_bias && kda_guard(c, 1, a.dim, a.err)) dt += a.dt_bias[c];
+  float A[4], B[4], C[4];
+  load(a.A, static_cast<int64_t>(c) * S + 4 * lane, static_cast<int64_t>(a.dim) * S, A);
+  load(static_cast<const T*>(a.B), n * a.ld_b + g * S + 4 * lane, (a.N - 1) * a.ld_b + gs, B);
+  load(static_cast<const T*>(a.C), n * a.ld_c + g * S + 4 * lane, (a.N - 1) * a.ld_c + gs, C);
+  const bool in = kda_guard(c, 1, a.dim, a.err);
+  if (a.dt_bias && in) dt += a.dt_bias[c];
   if (a.softplus) dt = softplus(dt);
-  const float u = dt * x;
-  h.x = fmaf(ex2(dt * (A[0] * kLog2e)), h.x, u * B[0]);
-  h.y = fmaf(ex2(dt * (A[1] * kLog2e)), h.y, u * B[1]);
-  h.z = fmaf(ex2(dt * (A[2] * kLog2e)), h.z, u * B[2]);
-  h.w = fmaf(ex2(dt * (A[3] * kLog2e)), h.w, u * B[3]);
+  const float u = dt * x, dl = dt * kLog2e;
+  h.x = fmaf(ex2(dl * A[0]), h.x, u * B[0]);
+  h.y = fmaf(ex2(dl * A[1]), h.y, u * B[1]);
+  h.z = fmaf(ex2(dl * A[2]), h.z, u * B[2]);
+  h.w = fmaf(ex2(dl * A[3]), h.w, u * B[3]);
   if (live && kda_guard(at, 4, states, a.err)) *reinterpret_cast<float4*>(a.h_out + at) = h;
   float y = fmaf(h.x, C[0], h.y * C[1]) + fmaf(h.z, C[2], h.w * C[3]);
 #pragma unroll
   for (int o = kPer / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
   if (live && lane == 0) {
-    if (a.D && kda_guard(c, 1, a.dim, a.err)) y = fmaf(a.D[c], x, y);
-    if (a.z) y *= gate(element<T>(a.z, n, a.ld_z, c, true, a));
+    if (a.D && in) y = fmaf(a.D[c], x, y);
+    if (a.z) y *= silu(element<T>(a.z, n, a.ld_z, c, true, a));
     const int64_t e = n * a.ld_y + c;
     if (kda_guard(e, 1, (a.N - 1) * a.ld_y + a.dim, a.err)) static_cast<T*>(a.y)[e] = from_f32<T>(y);
   }
@@ -665,11 +654,13 @@ cudaError_t run_scan(const SsmArgs& a, bool cut, cudaStream_t s) {
 
 template <typename T, int S>
 cudaError_t run_step(const SsmArgs& a, cudaStream_t s) {
-  const int64_t threads = static_cast<int64_t>(a.N) * a.dim * (S / 4);
-  const int64_t blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (a.vec) ssm_step_kernel<T, S, true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
-  else ssm_step_kernel<T, S, false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
+  const int64_t blocks_x = (static_cast<int64_t>(a.dim) * (S / 4) + kStepThreads - 1) / kStepThreads;
+  const int64_t blocks_y = std::min<int64_t>(a.N, 65535), blocks_z = (a.N + blocks_y - 1) / blocks_y;
+  if (blocks_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks_x), static_cast<unsigned>(blocks_y),
+                  static_cast<unsigned>(blocks_z));
+  if (a.vec) ssm_step_kernel<T, S, true><<<grid, kStepThreads, 0, s>>>(a);
+  else ssm_step_kernel<T, S, false><<<grid, kStepThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
