@@ -475,7 +475,7 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
 #pragma unroll
               for (int k = 0; k < kPiece; k += 32) {
                 const int64_t e = (r_at + i) * a.ld_out + c_at + k + lane;
-                if (c_at + k + lane < a.N && kda_guard(e, 1, extent, a.err))
+                if (r_at + i < a.M && c_at + k + lane < a.N && kda_guard(e, 1, extent, a.err))
                   out[e] = *reinterpret_cast<const OutT*>(
                       own + sw128_offset(32, i, static_cast<uint32_t>(sizeof(OutT)) * (k + lane)));
               }

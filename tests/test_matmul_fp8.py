@@ -178,3 +178,19 @@ def test_binding_refusals():
         kb.kda_matmul_fp8(a[:, :128], sa, b, sb)
     with pytest.raises(kb.KdaError, match="float8"):
         kb.kda_matmul_fp8(a[:, :128].float(), sa[:, :1], b, sb)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N", [(1, 130), (40, 129), (65, 300), (129, 257), (200, 1001), (1037, 100),
+                                 (1037, 104), (2600, 2601), (2600, 2600)])
+def test_nothing_is_written_past_the_last_row(M, N, dtype):
+    """Every tile shape, with rows that a tensor copy may and may not write: the rows behind
+    out's last one stay as they were."""
+    g = gen(M + N)
+    a, sa = operand(g, M, 256, 1)
+    b, sb = operand(g, N, 256, 128)
+    behind = torch.full((M + 256, N), 5.0, dtype=dtype, device=DEV)
+    kb.kda_matmul_fp8(a, sa, b, sb, behind[:M])
+    assert (behind[M:] == 5).all()
+    assert torch.equal(behind[:M], kb.kda_matmul_fp8(a, sa, b, sb, out_dtype=dtype))
