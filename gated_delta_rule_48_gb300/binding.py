@@ -749,31 +749,37 @@ def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, 
     return y
 
 
-def _groups_of(t, x, name):
+def _groups_of(t, x, name, same):
     """(address, distance between tokens) of B or C, [..., groups, state] with a dense token."""
-    if t.dim() != x.dim() + 1 or t.shape[:-2] != x.shape[:-1]:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != x.dim() + 1 or shape[:-2] != x.shape[:-1]:
         raise KdaError(1, f"{name} must have the shape {(*x.shape[:-1], 'groups', 'state')}, got "
-                          f"{tuple(t.shape)}")
-    groups, state = t.shape[-2:]
-    if groups > 1 and t.stride(-2) != state:
+                          f"{tuple(shape)}")
+    if shape[-2] > 1 and stride[-2] != shape[-1]:
         raise KdaError(1, f"{name}: the groups of a token must be dense")
-    p, ld, _ = _rows(t.select(-2, 0) if groups != 0 else t, name, _SAME[x.dtype])
+    if len(shape) == 3 and shape[0] > 1 and stride[2] == 1:  # the usual case
+        if t.dtype not in same or not t.is_cuda:
+            raise KdaError(1, f"{name} must be a CUDA tensor of {x.dtype}")
+        return t.data_ptr(), stride[0]
+    p, ld, _ = _rows(t.flatten(-2) if shape[-2] else t, name, same)
     return p, ld
 
 
 def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
     """The arguments that the scan and its step share, and (dim, state, groups, dtype)."""
-    xp, ld_x, code = _rows(x, "x", _FLOATS)
-    dim = x.shape[-1]
-    for t, name in ((dt, "dt"), (z, "z")):
-        _same_shape(t, x.shape, name)
-    same = _SAME[x.dtype]
+    same, shape = _like(x), x.shape
+    xp, ld_x, code = _rows(x, "x", same)
+    _same_shape(dt, shape, "dt")
     dtp, ld_dt, _ = _rows(dt, "dt", same)
-    zp, ld_z, _ = _rows(z, "z", same)
-    bp, ld_b = _groups_of(B, x, "B")
-    cp, ld_c = _groups_of(C, x, "C")
+    zp = None
+    ld_z = 0
+    if z is not None:
+        _same_shape(z, shape, "z")
+        zp, ld_z, _ = _rows(z, "z", same)
+    bp, ld_b = _groups_of(B, x, "B", same)
+    cp, ld_c = _groups_of(C, x, "C", same)
     _same_shape(C, B.shape, "C")
-    groups, state = B.shape[-2:]
+    dim, (groups, state) = shape[-1], B.shape[-2:]
     f32 = torch.float32
     return ([xp, ld_x, dtp, ld_dt, _dense(A, (dim, state), f32, "A"), bp, ld_b, cp, ld_c,
              _dense(D, (dim,), f32, "D"), zp, ld_z, _dense(dt_bias, (dim,), f32, "dt_bias")],

@@ -573,19 +573,19 @@ ssm_scan_kernel(SsmArgs a, int n_cb, int cb_per_group) {
   }
 }
 
-// One token of each sequence, h in place.  S / 4 lanes per channel, four
-// values each, so that the states are read and written in whole rows; bound by
-// those bytes.  A block's sequence comes from the grid: found by division of a
-// 64-bit index, it cost half of the instructions.
+// One token of each sequence, h in place.  S / 8 lanes per channel, two groups
+// of four values each; bound by the states' bytes.  (Four values a lane: less
+// in flight and twice the work around them; several sequences to a thread:
+// fewer threads, slower.)
 constexpr int kStepThreads = 256;
 template <typename T, int S, bool VEC>
-__global__ void __launch_bounds__(kStepThreads, 2048 / kStepThreads) ssm_step_kernel(SsmArgs a) {
-  constexpr int kPer = S / 4;  // lanes per channel
+__global__ void __launch_bounds__(kStepThreads, 4) ssm_step_kernel(SsmArgs a, int per_group) {
+  constexpr int kPer = S / 8;  // lanes per channel; value s is in lane (s / 4) % kPer
   const int lane = threadIdx.x % kPer;
   const int c_own = blockIdx.x * (kStepThreads / kPer) + threadIdx.x / kPer;
   const bool live = c_own < a.dim;
   const int c = live ? c_own : a.dim - 1;  // (whole warps take part in the sums)
-  const int g = c / (a.dim / a.groups);
+  const int g = a.groups == 1 ? 0 : c / per_group;
   const int64_t n = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
   if (n >= a.N) return;  // (the whole block)
   const int64_t states = static_cast<int64_t>(a.N) * a.dim * S, gs = static_cast<int64_t>(a.groups) * S;
@@ -598,24 +598,39 @@ __global__ void __launch_bounds__(kStepThreads, 2048 / kStepThreads) ssm_step_ke
     }
   };
   const int64_t at = (n * a.dim + c) * S + 4 * lane;
-  float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (kda_guard(at, 4, states, a.err)) h = *reinterpret_cast<const float4*>(a.h0 + at);
+  float4 h[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    h[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (kda_guard(at + 4 * kPer * q, 4, states, a.err))
+      h[q] = *reinterpret_cast<const float4*>(a.h0 + at + 4 * kPer * q);
+  }
   const float x = element<T>(a.x, n, a.ld_x, c, true, a);
   float dt = element<T>(a.dt, n, a.ld_dt, c, true, a);
-  float A[4], B[4], C[4];
-  load(a.A, static_cast<int64_t>(c) * S + 4 * lane, static_cast<int64_t>(a.dim) * S, A);
-  load(static_cast<const T*>(a.B), n * a.ld_b + g * S + 4 * lane, (a.N - 1) * a.ld_b + gs, B);
-  load(static_cast<const T*>(a.C), n * a.ld_c + g * S + 4 * lane, (a.N - 1) * a.ld_c + gs, C);
+  float A[2][4], B[2][4], C[2][4];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int s = 4 * (lane + kPer * q);
+    load(a.A, static_cast<int64_t>(c) * S + s, static_cast<int64_t>(a.dim) * S, A[q]);
+    load(static_cast<const T*>(a.B), n * a.ld_b + g * S + s, (a.N - 1) * a.ld_b + gs, B[q]);
+    load(static_cast<const T*>(a.C), n * a.ld_c + g * S + s, (a.N - 1) * a.ld_c + gs, C[q]);
+  }
   const bool in = kda_guard(c, 1, a.dim, a.err);
   if (a.dt_bias && in) dt += a.dt_bias[c];
   if (a.softplus) dt = softplus(dt);
   const float u = dt * x, dl = dt * kLog2e;
-  h.x = fmaf(ex2(dl * A[0]), h.x, u * B[0]);
-  h.y = fmaf(ex2(dl * A[1]), h.y, u * B[1]);
-  h.z = fmaf(ex2(dl * A[2]), h.z, u * B[2]);
-  h.w = fmaf(ex2(dl * A[3]), h.w, u * B[3]);
-  if (live && kda_guard(at, 4, states, a.err)) *reinterpret_cast<float4*>(a.h_out + at) = h;
-  float y = fmaf(h.x, C[0], h.y * C[1]) + fmaf(h.z, C[2], h.w * C[3]);
+  float y = 0.f;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float4& v = h[q];
+    v.x = fmaf(ex2(dl * A[q][0]), v.x, u * B[q][0]);
+    v.y = fmaf(ex2(dl * A[q][1]), v.y, u * B[q][1]);
+    v.z = fmaf(ex2(dl * A[q][2]), v.z, u * B[q][2]);
+    v.w = fmaf(ex2(dl * A[q][3]), v.w, u * B[q][3]);
+    if (live && kda_guard(at + 4 * kPer * q, 4, states, a.err))
+      *reinterpret_cast<float4*>(a.h_out + at + 4 * kPer * q) = v;
+    y += fmaf(v.x, C[q][0], v.y * C[q][1]) + fmaf(v.z, C[q][2], v.w * C[q][3]);
+  }
 #pragma unroll
   for (int o = kPer / 2; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
   if (live && lane == 0) {
@@ -654,13 +669,13 @@ cudaError_t run_scan(const SsmArgs& a, bool cut, cudaStream_t s) {
 
 template <typename T, int S>
 cudaError_t run_step(const SsmArgs& a, cudaStream_t s) {
-  const int64_t blocks_x = (static_cast<int64_t>(a.dim) * (S / 4) + kStepThreads - 1) / kStepThreads;
+  const int64_t blocks_x = (static_cast<int64_t>(a.dim) * (S / 8) + kStepThreads - 1) / kStepThreads;
   const int64_t blocks_y = std::min<int64_t>(a.N, 65535), blocks_z = (a.N + blocks_y - 1) / blocks_y;
   if (blocks_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks_x), static_cast<unsigned>(blocks_y),
                   static_cast<unsigned>(blocks_z));
-  if (a.vec) ssm_step_kernel<T, S, true><<<grid, kStepThreads, 0, s>>>(a);
-  else ssm_step_kernel<T, S, false><<<grid, kStepThreads, 0, s>>>(a);
+  if (a.vec) ssm_step_kernel<T, S, true><<<grid, kStepThreads, 0, s>>>(a, a.dim / a.groups);
+  else ssm_step_kernel<T, S, false><<<grid, kStepThreads, 0, s>>>(a, a.dim / a.groups);
   return cudaGetLastError();
 }
 
