@@ -7,8 +7,11 @@ fallback: if the library is missing or no GPU is present, calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import shutil
 import subprocess
+import sysconfig
 import threading
 
 import numpy as np
@@ -22,11 +25,16 @@ _LIB = os.path.join(_BUILD, "libkda.so")
 # the bounds-checked build (-DKDA_BOUNDS_CHECK), objects and library apart
 _BUILD_CHECKED = os.path.join(_BUILD, "checked")
 _LIB_CHECKED = os.path.join(_BUILD_CHECKED, "libkda.so")
+# the module that takes torch tensors to the library's operators (csrc/kda_torch.cpp), for the
+# torch at hand
+_EXT = os.path.join(_BUILD, f"torch-{torch.__version__}", "kda_torch.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
 _libs = {}          # False: the normal library, True: the bounds-checked one
 _checked = False    # which one load() returns
+_extension = None   # the module of csrc/kda_torch.cpp
+_selected = None    # the same, once its calls go to the library that load() returns
 
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARGUMENT", 2: "KDA_ERR_UNSUPPORTED",
           3: "KDA_ERR_CUDA", 4: "KDA_ERR_OUT_OF_MEMORY", 5: "KDA_ERR_DEVICE_INPUT"}
@@ -46,8 +54,9 @@ def use_checked(checked: bool) -> None:
     """Route every call of this module to the bounds-checked library (True)
     or to the normal one (False, the default).  Both may be loaded at once;
     each keeps its own device state."""
-    global _checked
+    global _checked, _selected
     _checked = bool(checked)
+    _selected = None
 
 
 def _sources():
@@ -57,6 +66,43 @@ def _sources():
 def _headers():
     hs = [os.path.join(_CSRC, f) for f in os.listdir(_CSRC) if f.endswith((".h", ".cuh"))]
     return hs + [os.path.join(_INCLUDE, "kda.h")]
+
+
+def _build_extension(force: bool = False):
+    """(command, process) of the compilation of ``csrc/kda_torch.cpp``, or None when it is up to
+    date.  ``_EXT`` is in place once :func:`build` has waited for it."""
+    src = os.path.join(_CSRC, "kda_torch.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(_INCLUDE, "kda.h")))
+    if not force and os.path.exists(_EXT) and os.path.getmtime(_EXT) >= newest:
+        return None
+    os.makedirs(os.path.dirname(_EXT), exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    nvcc = shutil.which("nvcc")
+    cuda = os.path.dirname(os.path.dirname(nvcc)) if nvcc else "/usr/local/cuda"
+    lib = os.path.join(root, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", _INCLUDE, src, "-o", _EXT + f".tmp{os.getpid()}", "-L", lib, "-ltorch",
+           "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", "-ldl"]
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(procs, verbose):
+    """Wait for compilations; raise if one failed."""
+    failed = []
+    for cmd, p in filter(None, procs):
+        out, _ = p.communicate()
+        if verbose or p.returncode:
+            print(out.decode(errors="replace"))
+        if p.returncode:
+            failed.append(" ".join(cmd))
+        elif cmd[0] == "g++":
+            os.replace(_EXT + f".tmp{os.getpid()}", _EXT)
+    if failed:
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
 
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
@@ -69,30 +115,24 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     """
     bdir, lib_path = (_BUILD_CHECKED, _LIB_CHECKED) if checked else (_BUILD, _LIB)
     os.makedirs(bdir, exist_ok=True)
+    ext = _build_extension(force)
     srcs = _sources()
     newest = max(os.path.getmtime(p) for p in srcs + _headers())
     if not force and os.path.exists(lib_path) and os.path.getmtime(lib_path) >= newest:
+        _finish([ext], verbose)
         return lib_path
     common = ["nvcc", *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-I", _INCLUDE, "-I", _CSRC, "--expt-relaxed-constexpr"]
     if checked:
         common.append("-DKDA_BOUNDS_CHECK")
-    objs, procs = [], []
+    objs, procs = [], [ext]
     for src in srcs:
         obj = os.path.join(bdir, os.path.basename(src) + ".o")
         objs.append(obj)
         cmd = common + ["-c", src, "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                              stderr=subprocess.STDOUT)))
-    failed = []
-    for cmd, p in procs:
-        out, _ = p.communicate()
-        if verbose or p.returncode:
-            print(out.decode(errors="replace"))
-        if p.returncode:
-            failed.append(" ".join(cmd))
-    if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+    _finish(procs, verbose)
     tmp = lib_path + f".tmp{os.getpid()}"
     subprocess.check_call(["nvcc", *ARCH_FLAGS, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib_path)
@@ -528,115 +568,31 @@ def kda_decode_tokens_fused(q_raw, k_raw, v, gate, beta, S_inout, commit=None, o
 
 
 # ---- operators around the recurrent layer.  Tensors may be column slices of wider ones: rows
-# with a unit last stride, any row stride.  Outputs that are not given are allocated on the
-# stream of the call.
+# with a unit last stride, any row stride (over all leading dimensions).  Outputs that are not
+# given are allocated on the call's stream.
 
-def _rows(t, name, dtypes):
-    """(address, distance between rows, dtype code) of a [rows, columns] CUDA tensor, or of one
-    with more leading dimensions that are one row stride apart."""
-    if t is None:
-        return None, 0, 0
-    code = dtypes.get(t.dtype)
-    if code is None or not t.is_cuda:
-        raise KdaError(1, f"{name} must be a CUDA tensor of {' or '.join(map(str, dtypes))}, got "
-                          f"{t.dtype} on {t.device}")
-    shape, stride = t.shape, t.stride()
-    if len(stride) == 2 and shape[0] > 1 and stride[1] == 1:  # the usual case
-        return t.data_ptr(), stride[0], code
-    d = len(stride)
-    if d < 2:
-        raise KdaError(1, f"{name} must have at least 2 dimensions")
-    cols = shape[-1]
-    if stride[-1] != 1 and cols > 1:
-        raise KdaError(1, f"{name}: the last dimension must be contiguous")
-    rows = shape[-2]
-    ld = stride[-2] if rows > 1 else stride[-3] if d > 2 and shape[-3] > 1 else max(cols, 1)
-    for k in range(d - 3, -1, -1):
-        if shape[k] > 1 and stride[k] != ld * rows:
-            raise KdaError(1, f"{name}: the leading dimensions must be one row stride apart")
-        rows *= shape[k]
-    return t.data_ptr(), ld, code
+def _ops():
+    """The module of csrc/kda_torch.cpp, its calls going to the library that load() returns."""
+    global _extension, _selected
+    load()
+    with _lock:
+        if _extension is None:
+            if not os.path.exists(_EXT):
+                _finish([_build_extension()], False)
+            spec = importlib.util.spec_from_file_location("kda_torch", _EXT)
+            _extension = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_extension)
+        _extension.select(library_path(), KdaError)
+        _selected = _extension
+    return _selected
 
 
-def _same_shape(t, shape, name):
-    if t is not None and t.shape != shape:
-        raise KdaError(1, f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _out(given, name, shape, dtype, like, stream):
-    """The output `given`, its shape checked, or a new tensor that belongs to the call's stream."""
-    if given is not None:
-        _same_shape(given, shape, name)
-        return given
+def _call(stream, name, *args):
+    f = getattr(_selected or _ops(), name)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _handle(stream, like):
-    """The stream's handle; without one, that of the current stream (of the inputs' device)."""
-    if stream is None:  # the handle alone: a Stream object takes longer than a small launch
-        return torch._C._cuda_getCurrentRawStream(like.device.index)
-    return stream.cuda_stream
-
-
-def _vector(t, n, name):
-    """(address, dtype code) of a contiguous bf16 or f32 vector of n elements, or of None."""
-    if t is None:
-        return None, 1
-    code = _FLOATS.get(t.dtype)
-    if code is None or not t.is_cuda:
-        raise KdaError(1, f"{name} must be a bfloat16 or float32 CUDA tensor")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise KdaError(1, f"{name} must be a contiguous vector of {n} elements")
-    return t.data_ptr(), code
-
-
-def _only(dtype):
-    return {dtype: KDA_DTYPE[dtype]}
-
-
-_BF16, _F32, _E4M3 = _only(torch.bfloat16), _only(torch.float32), _only(torch.float8_e4m3fn)
-_FLOATS = _BF16 | _F32
-_SAME = {torch.bfloat16: _BF16, torch.float32: _F32}
-
-
-def _like(x, name="x"):
-    """The dtypes that tensors of x's dtype may have."""
-    same = _SAME.get(x.dtype)
-    if same is None:
-        raise KdaError(1, f"{name} must be bfloat16 or float32, got {x.dtype}")
-    return same
-
-
-def _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, quant):
-    same, shape = _like(x), x.shape
-    dim = shape[-1]
-    rows = x.numel() // max(dim, 1)
-    xp, ld_x, dt = _rows(x, "x", same)
-    wp, w_dt = _vector(weight, dim, "weight")
-    rp = hp = sp = None
-    ld_r = ld_h = ld_s = 0
-    if residual is not None:
-        _same_shape(residual, shape, "residual")
-        rp, ld_r, _ = _rows(residual, "residual", same)
-    if residual is not None or h is not None:
-        h = _out(h, "h", shape, x.dtype, x, stream)
-        hp, ld_h, _ = _rows(h, "h", same)
-    if quant:
-        if y is None:  # rows at multiples of 16 bytes, as kda_matmul_fp8 reads them
-            pad = -dim % 16
-            y = _out(None, "y", (*shape[:-1], dim + pad), torch.float8_e4m3fn, x, stream)
-            y = y[..., :dim] if pad else y
-        y_scale = _out(y_scale, "y_scale", (*shape[:-1], (dim + 127) // 128), torch.float32, x,
-                       stream)
-        sp, ld_s, _ = _rows(y_scale, "y_scale", _F32)
-    y = _out(y, "y", shape, x.dtype, x, stream)
-    yp, ld_y, y_dt = _rows(y, "y", _E4M3 if quant else same)
-    _check(load().kda_add_rms_norm(xp, ld_x, rp, ld_r, wp, hp, ld_h, yp, ld_y, sp, ld_s, rows, dim,
-                                   eps, dt, w_dt, y_dt, _handle(stream, x)))
-    return y, y_scale, h
+        return f(*args)
+    with torch.cuda.stream(stream):  # its outputs too belong to that stream
+        return f(*args)
 
 
 def kda_add_rms_norm(x, weight, residual=None, *, eps=1e-6, y=None, h=None, stream=None):
@@ -646,7 +602,7 @@ def kda_add_rms_norm(x, weight, residual=None, *, eps=1e-6, y=None, h=None, stre
     Returns (y, h): h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, both in x's
     dtype; h is None without a residual (unless given).  y and h may be x or the residual.
     """
-    y, _, h = _add_rms_norm(x, weight, residual, eps, h, y, None, stream, False)
+    y, _, h = _call(stream, "add_rms_norm", x, weight, residual, eps, y, None, h, False)
     return y, h
 
 
@@ -655,59 +611,17 @@ def kda_add_rms_norm_quant(x, weight, residual=None, *, eps=1e-6, y=None, y_scal
     """:func:`kda_add_rms_norm` with y in 8 bits: returns (y, y_scale, h), y float8_e4m3fn
     [..., dim] and y_scale f32 [..., ceil(dim / 128)] with y * y_scale (per 128 columns)
     standing for the normalised rows, as :func:`kda_matmul_fp8` reads them."""
-    return _add_rms_norm(x, weight, residual, eps, h, y, y_scale, stream, True)
+    return _call(stream, "add_rms_norm", x, weight, residual, eps, y, y_scale, h, True)
 
 
 def kda_matmul_fp8(a, a_scale, b, b_scale, out=None, *, out_dtype=torch.bfloat16, stream=None):
     """a [..., K] times the transpose of b [N, K], both float8_e4m3fn with rows on 16-byte
     boundaries; a_scale: f32 [..., ceil(K / 128)], b_scale: f32 [ceil(N / 128), ceil(K / 128)].
-    Returns out [..., N] in ``out_dtype`` (bf16 or f32), rounded once from 32-bit sums."""
-    K, (N, k_b) = a.shape[-1], b.shape
-    if k_b != K:
-        raise KdaError(1, f"a has {K} columns and b has {k_b}")
-    blocks = (K + 127) // 128
-    ap, ld_a, _ = _rows(a, "a", _E4M3)
-    _same_shape(a_scale, (*a.shape[:-1], blocks), "a_scale")
-    _same_shape(b_scale, ((N + 127) // 128, blocks), "b_scale")
-    asp, ld_as, _ = _rows(a_scale, "a_scale", _F32)
-    bp, ld_b, _ = _rows(b, "b", _E4M3)
-    bsp, ld_bs, _ = _rows(b_scale, "b_scale", _F32)
-    M = a.numel() // max(K, 1)
-    # a single row needs no distance to a next one
-    ld_a, ld_b = (ld + -ld % 16 if rows == 1 else ld for ld, rows in ((ld_a, M), (ld_b, N)))
-    out = _out(out, "out", (*a.shape[:-1], N), out_dtype, a, stream)
-    op, ld_o, o_dt = _rows(out, "out", _FLOATS)
-    _check(load().kda_matmul_fp8(ap, ld_a, asp, ld_as, bp, ld_b, bsp, ld_bs, op, ld_o, M, N, K,
-                                 o_dt, _handle(stream, a)))
-    return out
-
-
-def _dense(t, shape, dtype, name):
-    """The address of a contiguous CUDA tensor of that shape and dtype, or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _require(t, dtype, name)
-        _same_shape(t, shape, name)
-    return t.data_ptr()
-
-
-def _conv_weights(x, weight, bias):
-    dim = x.shape[-1]
-    if weight.dim() != 2 or weight.shape[0] != dim:
-        raise KdaError(1, f"weight must have the shape ({dim}, width), got {tuple(weight.shape)}")
-    _like(weight, "weight")
-    return (_dense(weight, weight.shape, weight.dtype, "weight"),
-            _dense(bias, (dim,), weight.dtype, "bias"), weight.shape[1], KDA_DTYPE[weight.dtype])
-
-
-def _sequences(x, cu_seqlens, n_seqs):
-    """(tokens, sequences, address of cu_seqlens) of packed [T, dim] or uniform [B, T_b, dim] x."""
-    tokens = x.numel() // max(x.shape[-1], 1)
-    if cu_seqlens is not None:
-        _require(cu_seqlens, torch.int32, "cu_seqlens")
-        return tokens, cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
-    return tokens, n_seqs if n_seqs is not None else (x.shape[0] if x.dim() > 2 else 1), None
+    Returns out [..., N], rounded once from 32-bit sums: ``out``, or a new tensor of
+    ``out_dtype`` (bf16 or f32)."""
+    if out is None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise KdaError(1, f"out must be bfloat16 or float32, got {out_dtype}")
+    return _call(stream, "matmul_fp8", a, a_scale, b, b_scale, out, out_dtype == torch.float32)
 
 
 def kda_short_conv_fwd(x, weight, bias=None, conv_state=None, cu_seqlens=None, *, n_seqs=None,
@@ -719,71 +633,14 @@ def kda_short_conv_fwd(x, weight, bias=None, conv_state=None, cu_seqlens=None, *
     dim] in x's dtype or None (zeros); cu_seqlens: int32 [N + 1] (CUDA) or None.  Returns
     (y, state): the state continues the sequences; ``state_out`` may be ``conv_state`` itself.
     """
-    T, N, cu = _sequences(x, cu_seqlens, n_seqs)
-    xp, ld_x, dt = _rows(x, "x", _FLOATS)
-    wp, bp, width, w_dt = _conv_weights(x, weight, bias)
-    shape = (N, width - 1, x.shape[-1])
-    y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
-    if want_state or state_out is not None:
-        state_out = _out(state_out, "state_out", shape, x.dtype, x, stream)
-    _check(load().kda_short_conv_fwd(xp, ld_x, wp, bp, _dense(conv_state, shape, x.dtype, "conv_state"),
-                                     _dense(state_out, shape, x.dtype, "state_out"), cu, yp, ld_y,
-                                     T, N, x.shape[-1], width, 1 if silu else 0, dt, w_dt,
-                                     _handle(stream, x)))
-    return y, state_out
+    return _call(stream, "short_conv_fwd", x, weight, bias, conv_state, cu_seqlens, n_seqs,
+                 bool(silu), bool(want_state), y, state_out)
 
 
 def kda_short_conv_step(x, weight, conv_state, bias=None, *, silu=True, y=None, stream=None):
     """One token of each sequence: x [N, dim]; ``conv_state`` [N, width - 1, dim] is updated in
     place.  Otherwise as :func:`kda_short_conv_fwd`.  Returns y [N, dim]."""
-    N, dim = x.shape
-    xp, ld_x, dt = _rows(x, "x", _FLOATS)
-    wp, bp, width, w_dt = _conv_weights(x, weight, bias)
-    y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
-    _check(load().kda_short_conv_step(xp, ld_x, wp, bp,
-                                      _dense(conv_state, (N, width - 1, dim), x.dtype, "conv_state"),
-                                      yp, ld_y, N, dim, width, 1 if silu else 0, dt, w_dt,
-                                      _handle(stream, x)))
-    return y
-
-
-def _groups_of(t, x, name, same):
-    """(address, distance between tokens) of B or C, [..., groups, state] with a dense token."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != x.dim() + 1 or shape[:-2] != x.shape[:-1]:
-        raise KdaError(1, f"{name} must have the shape {(*x.shape[:-1], 'groups', 'state')}, got "
-                          f"{tuple(shape)}")
-    if shape[-2] > 1 and stride[-2] != shape[-1]:
-        raise KdaError(1, f"{name}: the groups of a token must be dense")
-    if len(shape) == 3 and shape[0] > 1 and stride[2] == 1:  # the usual case
-        if t.dtype not in same or not t.is_cuda:
-            raise KdaError(1, f"{name} must be a CUDA tensor of {x.dtype}")
-        return t.data_ptr(), stride[0]
-    p, ld, _ = _rows(t.flatten(-2) if shape[-2] else t, name, same)
-    return p, ld
-
-
-def _ssm_args(x, dt, A, B, C, D, z, dt_bias):
-    """The arguments that the scan and its step share, and (dim, state, groups, dtype)."""
-    same, shape = _like(x), x.shape
-    xp, ld_x, code = _rows(x, "x", same)
-    _same_shape(dt, shape, "dt")
-    dtp, ld_dt, _ = _rows(dt, "dt", same)
-    zp = None
-    ld_z = 0
-    if z is not None:
-        _same_shape(z, shape, "z")
-        zp, ld_z, _ = _rows(z, "z", same)
-    bp, ld_b = _groups_of(B, x, "B", same)
-    cp, ld_c = _groups_of(C, x, "C", same)
-    _same_shape(C, B.shape, "C")
-    dim, (groups, state) = shape[-1], B.shape[-2:]
-    f32 = torch.float32
-    return ([xp, ld_x, dtp, ld_dt, _dense(A, (dim, state), f32, "A"), bp, ld_b, cp, ld_c,
-             _dense(D, (dim,), f32, "D"), zp, ld_z, _dense(dt_bias, (dim,), f32, "dt_bias")],
-            dim, state, groups, code)
+    return _call(stream, "short_conv_step", x, weight, conv_state, bias, bool(silu), y)
 
 
 def kda_ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlens=None, *,
@@ -796,28 +653,12 @@ def kda_ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_s
     or None; h0: f32 [N, dim, state] or None (zeros); cu_seqlens: int32 [N + 1] (CUDA) or None.
     Returns (y, h_final); ``h_final`` may be ``h0`` itself.
     """
-    T, N, cu = _sequences(x, cu_seqlens, n_seqs)
-    args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
-    y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
-    shape = (N, dim, state)
-    if want_state or h_final is not None:
-        h_final = _out(h_final, "h_final", shape, torch.float32, x, stream)
-    _check(load().kda_ssm_scan_fwd(*args, _dense(h0, shape, torch.float32, "h0"), cu, yp, ld_y,
-                                   _dense(h_final, shape, torch.float32, "h_final"), T, N, dim,
-                                   state, groups, 1 if softplus else 0, code, _handle(stream, x)))
-    return y, h_final
+    return _call(stream, "ssm_scan_fwd", x, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, n_seqs,
+                 bool(softplus), bool(want_state), y, h_final)
 
 
 def kda_ssm_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softplus=True, y=None,
                       stream=None):
     """One token of each sequence: x, dt, z [N, dim], B, C [N, groups, state]; ``h`` f32
     [N, dim, state] is updated in place.  Otherwise as :func:`kda_ssm_scan_fwd`.  Returns y."""
-    args, dim, state, groups, code = _ssm_args(x, dt, A, B, C, D, z, dt_bias)
-    N = x.shape[0]
-    y = _out(y, "y", x.shape, x.dtype, x, stream)
-    yp, ld_y, _ = _rows(y, "y", _SAME[x.dtype])
-    _check(load().kda_ssm_scan_step(*args, _dense(h, (N, dim, state), torch.float32, "h"), yp, ld_y,
-                                    N, dim, state, groups, 1 if softplus else 0, code,
-                                    _handle(stream, x)))
-    return y
+    return _call(stream, "ssm_scan_step", x, dt, A, B, C, h, D, z, dt_bias, bool(softplus), y)
