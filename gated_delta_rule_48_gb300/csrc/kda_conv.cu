@@ -10,7 +10,13 @@
 // Bound: HBM, x read once and y written once.  A thread owns a vector of
 // channels and walks down a strip of tokens with the last W - 1 rows in
 // registers, so a row is loaded once per strip; only the W - 1 rows above a
-// strip are read again (from L2).  The sums are in 32 bits.
+// strip are read again (from L2).  The sums are in 32 bits.  The next batch of
+// rows is loaded while one is computed, and kept as loaded until its turn;
+// eight rows a batch keep enough bytes in flight (four: 16 % slower).
+//
+// 16384 x 12288 bf16, width 4, SiLU: 133 us, 6.1 TB/s.  Channels that can only
+// be read two at a time (2050 of them) are bound by instructions: 20,011 rows
+// 39 us, 4.2 TB/s.  The step for 256 x 12288: 9.2 us, 5.5 TB/s.
 #include <cuda_runtime.h>
 
 #include "kda_ops.h"
