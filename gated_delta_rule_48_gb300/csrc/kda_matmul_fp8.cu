@@ -20,8 +20,9 @@
 // 16384 x 12288 x 4096: 0.66 to 0.70 ms, 2.35 to 2.5 PFLOP/s.  What bounds it is
 // the scaling: without the products it takes 0.63 ms, without the copies
 // 0.67 ms, without reading and adding the sums 0.56 ms.  32 x 12288 x 4096 (the
-// weights' bytes, 50 MB): 12.6 us, 4.0 TB/s, bound by the chain of waits per
-// hand-over (two k-blocks in about 0.35 us); 32 x 4096 x 4096: 7 us.
+// weights' bytes, 50 MB): 12.6 us.  From K = 8192 to 16384 another 100 MB take
+// 16.3 us, 6.2 TB/s: what is above the bytes is 4 us to launch, fill and write
+// out.  32 x 4096 x 4096: 6.7 us; 128 x 12288 x 4096: 15 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>
@@ -39,6 +40,7 @@ using namespace sm100;
 
 constexpr int kTileRows = 128;
 constexpr int kBlockK = 128;
+constexpr int kMaxSplits = 8;  // blocks of a cluster, which share a tile's k-blocks
 
 // D (+)= A B, 8-bit operands from shared memory; issued by one thread.
 __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -55,12 +57,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// A float at this block's shared address `at`, but of block `rank` of the cluster.
-__device__ __forceinline__ float load_of_block(uint32_t at, int rank) {
-  float v;
+// Four floats at this block's shared address `at`, but of block `rank` of the cluster.
+__device__ __forceinline__ float4 load_of_block(uint32_t at, int rank) {
+  float4 v;
   asm volatile(
-      "{\n .reg .b32 t;\n mapa.shared::cluster.u32 t, %1, %2;\n ld.shared::cluster.f32 %0, [t];\n}"
-      : "=f"(v)
+      "{\n .reg .b32 t;\n mapa.shared::cluster.u32 t, %4, %5;\n"
+      " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [t];\n}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
       : "r"(at), "r"(rank)
       : "memory");
   return v;
@@ -101,7 +104,22 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tme
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]) : "r"(taddr));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
 }
 
 // A warp's rows of the output through its own piece of shared memory, 128
@@ -124,7 +142,7 @@ struct Shape {
   // fills up their set of four (register shares go by sets), then the adding warps
   static constexpr int kThreads = 128 + 128 * kGroups;
   // 128 sums a thread: the first set gives registers to the others (launched
-  // with 168 each, 3 * 168 = 40 + 2 * 232)
+  // with 168 each, 3 * 168 = 56 + 2 * 224)
   static constexpr bool kShares = kCols == 128;
   static constexpr int kLaunchRegs = 168, kAddRegs = 224, kRestRegs = 56;
   static_assert(!kShares || 128 * (kRestRegs + kGroups * kAddRegs) <= kThreads * kLaunchRegs,
@@ -391,12 +409,11 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
           // One set of registers for all the loads: with two, to load ahead of
           // the additions, the kernel was 20 % slower.
           constexpr int kPieces = G::kCols / G::kLoad;
-          uint32_t dd[2][G::kLoad];
-          tmem_ld(at, dd[0]);
+          uint32_t d[G::kLoad];
+          tmem_ld(at, d);
 #pragma unroll
           for (int p = 0; p < G::kUnit * kPieces; ++p) {
             const int e = p / kPieces, i = p % kPieces;  // block of the unit, piece of its columns
-            uint32_t(&d)[G::kLoad] = dd[0];
             if (p > 0) tmem_ld(at + BN * e + G::kLoad * i, d);
             // (past the last block the scales and the products are zeros)
             const float scale =
@@ -502,14 +519,28 @@ matmul_kernel(const __grid_constant__ Maps maps, MatmulArgs a, int tiles_r, int 
       tile_at(tile0, r, c);
       const int first = BN * rank / splits, last = BN * (rank + 1) / splits;
       const int64_t extent = (a.M - 1) * a.ld_out + a.N;
-      for (int i = first * kTileRows + threadIdx.x; i < last * kTileRows; i += G::kThreads) {
+      // Four values of all blocks in flight at a time, added in the blocks' order:
+      // one value and one block after the other, 64 x 1024 x 4096 took 13 us.
+      for (int i = first * kTileRows + 4 * threadIdx.x; i < last * kTileRows; i += 4 * G::kThreads) {
         const int64_t m = static_cast<int64_t>(c) * BN + i / kTileRows;
         const int64_t n = static_cast<int64_t>(r) * kTileRows + i % kTileRows, e = m * a.ld_out + n;
         const uint32_t at = smem_u32(tiles) + 4 * i;
-        float sum = 0.f;
-        for (int q = 0; q < splits; ++q) sum += load_of_block(at, q);
-        if (m < a.M && n < a.N && kda_guard(e, 1, extent, a.err))
-          static_cast<OutT*>(a.out)[e] = from_f32<OutT>(sum);
+        float4 part[kMaxSplits];
+#pragma unroll
+        for (int q = 0; q < kMaxSplits; ++q)
+          part[q] = q < splits ? load_of_block(at, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kMaxSplits; ++q) {
+          sum[0] += part[q].x;
+          sum[1] += part[q].y;
+          sum[2] += part[q].z;
+          sum[3] += part[q].w;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (m < a.M && n + k < a.N && kda_guard(e + k, 1, extent, a.err))
+            static_cast<OutT*>(a.out)[e + k] = from_f32<OutT>(sum[k]);
       }
       __syncwarp();
       cluster_sync();  // no block's memory goes while another reads it
@@ -562,8 +593,74 @@ bool operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int6
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, boxes);
 }
 
+// Clusters of `splits` blocks that are resident at a time: fewer than the SMs
+// would give, as a cluster stays within a group of SMs.  Asked for once.
 template <int BN, bool SWAP, typename OutT>
-cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
+int resident_clusters(int splits) {
+  using G = Shape<BN, SWAP>;
+  struct Counts {
+    int of[kMaxSplits + 1];
+  };
+  static const Counts counts = [] {
+    Counts c;
+    memset(&c, 0, sizeof c);
+    constexpr auto kern = matmul_kernel<BN, SWAP, OutT>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(G::kSmem)) != cudaSuccess)
+      return c;
+    for (int n = 2; n <= kMaxSplits; n *= 2) {
+      cudaLaunchConfig_t cfg;
+      memset(&cfg, 0, sizeof cfg);
+      cfg.gridDim = dim3(static_cast<unsigned>(n));
+      cfg.blockDim = dim3(G::kThreads);
+      cfg.dynamicSmemBytes = G::kSmem;
+      cudaLaunchAttribute cluster;
+      cluster.id = cudaLaunchAttributeClusterDimension;
+      cluster.val.clusterDim.x = static_cast<unsigned>(n);
+      cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+      cfg.attrs = &cluster;
+      cfg.numAttrs = 1;
+      int found = 0;
+      if (cudaOccupancyMaxActiveClusters(&found, kern, &cfg) == cudaSuccess) c.of[n] = found;
+    }
+    return c;
+  }();
+  return counts.of[splits];
+}
+
+// How a product is cut into tiles, and into how many blocks its k-blocks.
+struct Cut {
+  int64_t tiles;
+  int splits;
+  double cost;  // estimated, in us
+};
+
+// Few tiles: a cluster of up to 8 blocks shares each one's k-blocks, as long as
+// all are resident and a block has two copies to overlap.  (16 tiles of 64 x
+// 128 with K = 4096: 8 blocks each, which are not all resident, 12.5 us.)
+//
+// The time goes by whole waves of tiles: a wave takes `block_us` per k-block
+// and about 1.5 us to fill and to write out, a launch 3 us, a cluster's sum 1 us.
+template <int BN, bool SWAP, typename OutT>
+Cut cut(const MatmulArgs& a, double block_us) {
+  using G = Shape<BN, SWAP>;
+  const int64_t rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;
+  Cut c;
+  c.tiles = ((rows + kTileRows - 1) / kTileRows) * ((cols + BN - 1) / BN);
+  c.splits = 1;
+  const int64_t kblocks = (a.K + kBlockK - 1) / kBlockK;
+  const int64_t units = (kblocks + G::kUnit - 1) / G::kUnit;
+  if (SWAP)
+    while (c.splits < kMaxSplits && units >= 4 * c.splits &&
+           c.tiles <= resident_clusters<BN, SWAP, OutT>(2 * c.splits))
+      c.splits *= 2;
+  const int64_t waves = c.splits > 1 ? 1 : (c.tiles + a.sm_count - 1) / a.sm_count;
+  c.cost = waves * ((kblocks + c.splits - 1) / c.splits * block_us + 1.5) + 3 + (c.splits > 1 ? 1 : 0);
+  return c;
+}
+
+template <int BN, bool SWAP, typename OutT>
+cudaError_t run(const MatmulArgs& a, const Cut& how, cudaStream_t s) {
   using G = Shape<BN, SWAP>;
   constexpr auto kern = matmul_kernel<BN, SWAP, OutT>;
   const int64_t rows = SWAP ? a.N : a.M, cols = SWAP ? a.M : a.N;
@@ -598,18 +695,11 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int tiles_r = static_cast<int>((rows + kTileRows - 1) / kTileRows);
   const int tiles_c = static_cast<int>((cols + BN - 1) / BN);
-  const int64_t n = static_cast<int64_t>(tiles_r) * tiles_c;
-  const int64_t slots = a.sm_count;
   const int band = 12;  // of 152 tiles in flight, 12 x 12.7
-  // Few tiles: a cluster of up to 8 blocks shares each one's k-blocks, as long
-  // as all are resident and a block has two copies to overlap.
-  int splits = 1;
-  const int units = ((a.K + kBlockK - 1) / kBlockK + G::kUnit - 1) / G::kUnit;
-  if (SWAP)
-    while (splits < 8 && 2 * splits * n <= slots && units >= 4 * splits) splits *= 2;
+  const int splits = how.splits;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? n * splits : std::min(n, slots)));
+  cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? how.tiles * splits : std::min<int64_t>(how.tiles, a.sm_count)));
   cfg.blockDim = dim3(G::kThreads);
   cfg.dynamicSmemBytes = G::kSmem;
   cfg.stream = s;
@@ -624,14 +714,23 @@ cudaError_t run(const MatmulArgs& a, cudaStream_t s) {
 
 template <typename OutT>
 cudaError_t choose(const MatmulArgs& a, cudaStream_t s) {
-  if (a.M <= 16) return run<16, true, OutT>(a, s);
-  if (a.M <= 32) return run<32, true, OutT>(a, s);
-  if (a.M <= 128) return run<64, true, OutT>(a, s);
-  const int64_t row_tiles = (a.M + kTileRows - 1) / kTileRows;
-  // the widest tile of which there are enough for every SM
-  if (row_tiles * ((a.N + 255) / 256) >= a.sm_count) return run<256, false, OutT>(a, s);
-  if (row_tiles * ((a.N + 127) / 128) >= a.sm_count) return run<128, false, OutT>(a, s);
-  return run<64, false, OutT>(a, s);
+  // Up to 32 rows one narrow tile holds them all, and the weights are read once:
+  // no wider one was faster from 512 x 8192 to 12288 x 4096.
+  if (a.M <= 16) return run<16, true, OutT>(a, cut<16, true, OutT>(a, 0.2), s);
+  if (a.M <= 32) return run<32, true, OutT>(a, cut<32, true, OutT>(a, 0.2), s);
+  // Above, the cheapest by whole waves, with the times per k-block that sweeps of
+  // 33 to 4096 rows gave.  (Taking the widest tile of which there is one for
+  // every SM, 128 x 12288 x 4096 took 25 us instead of 15, 384 x 4096 x 4096
+  // 18.5 instead of 12.5, 1024 x 4096 x 12288 56 instead of 48.)
+  const Cut s32 = cut<32, true, OutT>(a, 0.2), s64 = cut<64, true, OutT>(a, 0.31);
+  const Cut n64 = cut<64, false, OutT>(a, 0.2), n128 = cut<128, false, OutT>(a, 0.255);
+  const Cut n256 = cut<256, false, OutT>(a, 0.45);
+  const double least = std::min({s32.cost, s64.cost, n64.cost, n128.cost, n256.cost});
+  if (n256.cost <= least) return run<256, false, OutT>(a, n256, s);
+  if (n128.cost <= least) return run<128, false, OutT>(a, n128, s);
+  if (n64.cost <= least) return run<64, false, OutT>(a, n64, s);
+  if (s64.cost <= least) return run<64, true, OutT>(a, s64, s);
+  return run<32, true, OutT>(a, s32, s);
 }
 
 }  // namespace

@@ -56,6 +56,20 @@ def test_sizes(M, N, K, dtype):
     check(M, N, K, dtype)
 
 
+# Sizes on both sides of where the cheapest cut into tiles changes: one wave of wide tiles or two
+# of narrow ones, and k-blocks shared by 2, 4 or 8 blocks, all of which fit or do not.
+CUTS = [(48, 1000, 4000), (65, 1024, 4096), (128, 1000, 4100), (128, 2050, 1920), (96, 6145, 520),
+        (100, 12288, 640), (128, 12289, 384), (160, 1024, 4096), (250, 520, 8192), (384, 4096, 300),
+        (1024, 4096, 1500), (513, 12288, 256)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", CUTS)
+def test_cuts_into_tiles(M, N, K, dtype):
+    check(M, N, K, dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(8, 256, 512), (40, 384, 300), (300, 500, 700)])
 def test_strided_rows_and_outputs(M, N, K):
