@@ -135,12 +135,8 @@ struct Rows {
   void* p = nullptr;
   int64_t ld = 0;
 };
-Rows rows(const Tensor& t, at::ScalarType type, const char* name) {
-  if (!t.defined()) return Rows{};
-  of_type(t, type, name);
-  const auto shape = t.sizes();
-  const auto stride = t.strides();
-  const int64_t d = t.dim();
+Rows rows(void* p, at::IntArrayRef shape, at::IntArrayRef stride, const char* name) {
+  const int64_t d = shape.size();
   if (d < 2) refuse("%s must have at least 2 dimensions", name);
   if (stride[d - 1] != 1 && shape[d - 1] > 1) refuse("%s: the last dimension must be contiguous", name);
   int64_t n = shape[d - 2];
@@ -152,7 +148,12 @@ Rows rows(const Tensor& t, at::ScalarType type, const char* name) {
       refuse("%s: the leading dimensions must be one row stride apart", name);
     n *= shape[k];
   }
-  return Rows{t.data_ptr(), ld};
+  return Rows{p, ld};
+}
+Rows rows(const Tensor& t, at::ScalarType type, const char* name) {
+  if (!t.defined()) return Rows{};
+  of_type(t, type, name);
+  return rows(t.data_ptr(), t.sizes(), t.strides(), name);
 }
 // A contiguous tensor of that shape, or none.
 void* dense(const Tensor& t, at::IntArrayRef shape, at::ScalarType type, const char* name) {
@@ -233,9 +234,10 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows hr = rows(h, type, "h");
     const at::ScalarType y_type = quant ? at::kFloat8_e4m3fn : type;
     if (quant && a[4] == Py_None) {  // rows at multiples of 16 bytes, as matmul_fp8 reads them
-      const int64_t wide = (dim + 15) / 16 * 16;
-      y = at::empty(with_last(x, wide), x.options().dtype(y_type));
-      if (wide != dim) y = y.narrow(-1, 0, dim);
+      std::vector<int64_t> stride(x.dim(), 1);
+      stride[x.dim() - 2] = (dim + 15) / 16 * 16;
+      for (int64_t k = x.dim() - 3; k >= 0; --k) stride[k] = stride[k + 1] * x.size(k + 1);
+      y = at::empty_strided(x.sizes(), stride, x.options().dtype(y_type));
     } else {
       y = output(a[4], x.sizes(), y_type, x, "y");
     }
@@ -362,7 +364,12 @@ struct Ssm {
              shape_of(t.sizes()).c_str());
     if (t.size(-2) > 1 && t.stride(-2) != t.size(-1)) refuse("%s: the groups of a token must be dense", name);
     if (t.size(-2) == 0) refuse("%s has no groups", name);
-    return rows(t.select(-2, 0), type, name);
+    of_type(t, type, name);
+    // a token's first group stands for its row (a view by select took 2 us)
+    at::DimVector shape(t.sizes()), stride(t.strides());
+    shape.erase(shape.end() - 2);
+    stride.erase(stride.end() - 2);
+    return rows(t.data_ptr(), shape, stride, name);
   }
 
   Ssm(PyObject* x_o, PyObject* dt_o, PyObject* A_o, PyObject* B_o, PyObject* C_o, PyObject* D_o,
