@@ -17,13 +17,12 @@
 // tensor core's 128 lanes, and a tile reads no more of A than there is.  Where
 // there are few tiles a cluster of blocks shares each one's k-blocks.
 //
-// 16384 x 12288 x 4096: 0.66 to 0.74 ms (a short and a long run), 2.2 to 2.5
-// PFLOP/s.  What bounds it is
-// the scaling: without the products it takes 0.63 ms, without the copies
-// 0.67 ms, without reading and adding the sums 0.56 ms.  32 x 12288 x 4096 (the
-// weights' bytes, 50 MB): 12.6 us.  From K = 8192 to 16384 another 100 MB take
-// 16.3 us, 6.2 TB/s: what is above the bytes is 4 us to launch, fill and write
-// out.  32 x 4096 x 4096: 6.7 us; 128 x 12288 x 4096: 15 us.
+// 16384 x 12288 x 4096: 0.66 to 0.74 ms (in a short and in a long run), 2.2 to
+// 2.5 PFLOP/s.  What bounds it is the scaling: without the products it takes
+// 0.63 ms, without the copies 0.67 ms, without reading and adding the sums 0.56
+// ms.  32 x 12288 x 4096 (the weights' bytes, 50 MB): 12.6 us.  From K = 8192 to
+// 16384 another 100 MB take 16.3 us, 6.2 TB/s: what is above the bytes is 4 us to
+// launch, fill and write out.  32 x 4096 x 4096: 6.7 us; 128 x 12288 x 4096: 15 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>
