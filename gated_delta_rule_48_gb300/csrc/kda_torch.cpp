@@ -131,18 +131,19 @@ void of_type(const Tensor& t, at::ScalarType type, const char* name) {
 }
 
 // Rows with a unit last stride, one stride apart over all leading dimensions.
+// A single row stands its `width` from a next one (by default the last dimension).
 struct Rows {
   void* p = nullptr;
   int64_t ld = 0;
 };
-Rows rows(void* p, at::IntArrayRef shape, at::IntArrayRef stride, const char* name) {
+Rows rows(void* p, at::IntArrayRef shape, at::IntArrayRef stride, const char* name, int64_t width = 0) {
   const int64_t d = shape.size();
   if (d < 2) refuse("%s must have at least 2 dimensions", name);
   if (stride[d - 1] != 1 && shape[d - 1] > 1) refuse("%s: the last dimension must be contiguous", name);
   int64_t n = shape[d - 2];
   const int64_t ld = n > 1                       ? stride[d - 2]
                      : d > 2 && shape[d - 3] > 1 ? stride[d - 3]
-                                                 : std::max<int64_t>(shape[d - 1], 1);
+                                                 : std::max<int64_t>({width, shape[d - 1], 1});
   for (int64_t k = d - 3; k >= 0; --k) {
     if (shape[k] > 1 && stride[k] != ld * n)
       refuse("%s: the leading dimensions must be one row stride apart", name);
@@ -369,7 +370,7 @@ struct Ssm {
     at::DimVector shape(t.sizes()), stride(t.strides());
     shape.erase(shape.end() - 2);
     stride.erase(stride.end() - 2);
-    return rows(t.data_ptr(), shape, stride, name);
+    return rows(t.data_ptr(), shape, stride, name, t.size(-2) * t.size(-1));
   }
 
   Ssm(PyObject* x_o, PyObject* dt_o, PyObject* A_o, PyObject* B_o, PyObject* C_o, PyObject* D_o,

@@ -284,3 +284,29 @@ def test_nothing_to_do():
                                               None, h, P(9), 64, N, 64, 16, 1, 1, 0, None)
     assert step(None, 2) == 1 and b"h is NULL" in lib.kda_last_error_message()
     assert step(P(8), 0) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G", [2, 8])
+def test_one_token_of_several_groups(G, dtype):
+    """One sequence's one token, whose groups are all of B and C: as a step, as a packed prompt
+    and as a uniform batch; and no token at all."""
+    d = make(1, 1, 48, 16, G, dtype)
+    y_ref, my, h_ref, m = reference(d, [1])
+    check(d, [1], dtype)
+    check(d, [1], dtype, packed=False)
+    one = {k: d[k][None] for k in ("x", "dt", "z", "B", "C")}
+    y, h = kb.kda_ssm_scan_fwd(one["x"], one["dt"], d["A"], one["B"], one["C"], d["D"], one["z"],
+                               d["dt_bias"], d["h0"])
+    assert_near(y[0], y_ref, half_ulp(dtype) + 3e-6, "y", atol=1e-5 * my)
+    assert_near(h, h_ref, 0.0, "h", atol=1e-5 * m)
+    h = d["h0"].clone()
+    y = kb.kda_ssm_scan_step(d["x"], d["dt"], d["A"], d["B"], d["C"], h, d["D"], d["z"], d["dt_bias"])
+    assert_near(y, y_ref, half_ulp(dtype) + 3e-6, "y", atol=1e-5 * my)
+    assert_near(h, h_ref, 0.0, "h", atol=1e-5 * m)
+    none = {k: d[k][:0] for k in ("x", "dt", "z", "B", "C")}
+    y, h = kb.kda_ssm_scan_fwd(none["x"], none["dt"], d["A"], none["B"], none["C"], h0=d["h0"],
+                               cu_seqlens=cu_of([0]))
+    assert y.shape == (0, 48) and torch.equal(h, d["h0"])
+    assert kb.kda_get_device_error() == 0
