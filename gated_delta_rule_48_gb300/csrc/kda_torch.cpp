@@ -140,15 +140,17 @@ Rows rows(void* p, at::IntArrayRef shape, at::IntArrayRef stride, const char* na
   const int64_t d = shape.size();
   if (d < 2) refuse("%s must have at least 2 dimensions", name);
   if (stride[d - 1] != 1 && shape[d - 1] > 1) refuse("%s: the last dimension must be contiguous", name);
-  int64_t n = shape[d - 2];
-  const int64_t ld = n > 1                       ? stride[d - 2]
-                     : d > 2 && shape[d - 3] > 1 ? stride[d - 3]
-                                                 : std::max<int64_t>({width, shape[d - 1], 1});
-  for (int64_t k = d - 3; k >= 0; --k) {
-    if (shape[k] > 1 && stride[k] != ld * n)
-      refuse("%s: the leading dimensions must be one row stride apart", name);
+  const int64_t alone = std::max<int64_t>({width, shape[d - 1], 1});
+  int64_t ld = alone, n = 1;  // the rows of the dimensions looked at, and their distance
+  bool refused = false;
+  for (int64_t k = d - 2; k >= 0; --k) {
+    if (shape[k] == 0) return Rows{p, alone};  // no rows
+    if (shape[k] == 1) continue;               // its stride says nothing
+    if (n == 1) ld = stride[k];
+    else refused = refused || stride[k] != ld * n;
     n *= shape[k];
   }
+  if (refused) refuse("%s: the leading dimensions must be one row stride apart", name);
   return Rows{p, ld};
 }
 Rows rows(const Tensor& t, at::ScalarType type, const char* name) {

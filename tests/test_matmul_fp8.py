@@ -208,3 +208,16 @@ def test_nothing_is_written_past_the_last_row(M, N, dtype):
     kb.kda_matmul_fp8(a, sa, b, sb, behind[:M])
     assert (behind[M:] == 5).all()
     assert torch.equal(behind[:M], kb.kda_matmul_fp8(a, sa, b, sb, out_dtype=dtype))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lead", [(5, 1, 1), (1, 5, 1), (1, 1, 1), (3, 0)])
+def test_reads_what_the_norm_writes_with_dimensions_of_one(lead):
+    g = gen(9)
+    x = torch.randn(*lead, 2051, device=DEV, generator=g).bfloat16()
+    b, sb = operand(g, 200, 2051, 128, 0.01)
+    q, s, _ = kb.kda_add_rms_norm_quant(x, torch.ones(2051, device=DEV))
+    out = kb.kda_matmul_fp8(q, s, b, sb, out_dtype=torch.float32)
+    assert out.shape == (*lead, 200)
+    q2, s2, _ = kb.kda_add_rms_norm_quant(x.view(-1, 2051), torch.ones(2051, device=DEV))
+    assert torch.equal(out.view(-1, 200), kb.kda_matmul_fp8(q2, s2, b, sb, out_dtype=torch.float32))

@@ -184,3 +184,40 @@ def test_norm_binding_refuses():
     x = torch.zeros(4, 8)
     with pytest.raises(kb.KdaError, match="CUDA"):
         kb.kda_add_rms_norm(x, torch.zeros(8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(3, 0, 64), (0, 3, 64), (2, 0, 5, 77)])
+def test_norm_of_a_batch_without_rows(shape):
+    x, w = torch.empty(*shape, device=DEV), torch.ones(shape[-1], device=DEV)
+    y, h = kb.kda_add_rms_norm(x, w, x.clone())
+    assert y.shape == x.shape and h.shape == x.shape
+    q, s, _ = kb.kda_add_rms_norm_quant(x, w)
+    assert q.shape == x.shape and s.shape == (*shape[:-1], 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(5, 1, 1, 2051), (1, 5, 1, 2051), (1, 1, 1, 2051), (5, 1, 1, 1, 40)])
+def test_norm_of_rows_with_dimensions_of_one(shape):
+    """Dimensions of one between the rows and their columns, in rows that stand further apart
+    than they are long: what the 8-bit form allocates itself, and slices."""
+    g = gen(11)
+    x = randn(g, *shape, dtype=torch.bfloat16)
+    w = randn(g, shape[-1], dtype=torch.bfloat16)
+    rows = x.view(-1, shape[-1])
+    want, want_s, _ = kb.kda_add_rms_norm_quant(rows, w)
+    for given in (x, sliced(x)):
+        q, s, _ = kb.kda_add_rms_norm_quant(given, w)
+        assert q.shape == x.shape
+        assert torch.equal(q.float().view_as(rows), want.float()) and torch.equal(s.view_as(want_s), want_s)
+    y, _ = kb.kda_add_rms_norm(sliced(x), w)
+    assert torch.equal(y.view_as(rows), kb.kda_add_rms_norm(rows, w)[0])
+
+
+@pytest.mark.gpu
+def test_norm_refuses_rows_at_uneven_distances():
+    w = torch.ones(64, device=DEV)
+    wide = torch.zeros(4, 6, 64, device=DEV)
+    for x in (wide[:, :5], wide.transpose(0, 1), wide[:, None, ::2][:, :, :2]):
+        with pytest.raises(kb.KdaError, match="one row stride apart"):
+            kb.kda_add_rms_norm(x, w)

@@ -222,3 +222,10 @@ def test_output_beside_its_input():
     wide[:, :64] = x
     kb.kda_short_conv_fwd(wide[:, :64], w, b, s, cu_of([50, 3]), y=wide[:, 64:])
     assert torch.equal(wide[:, 64:], want) and torch.equal(wide[:, :64], x)
+
+
+@pytest.mark.gpu
+def test_a_uniform_batch_without_tokens_hands_the_state_through():
+    _, w, b, s = inputs([1] * 3, 40, 4, torch.bfloat16)
+    y, out = kb.kda_short_conv_fwd(torch.empty(3, 0, 40, dtype=torch.bfloat16, device=DEV), w, b, s)
+    assert y.shape == (3, 0, 40) and torch.equal(out, s)

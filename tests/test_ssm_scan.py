@@ -310,3 +310,13 @@ def test_one_token_of_several_groups(G, dtype):
                                cu_seqlens=cu_of([0]))
     assert y.shape == (0, 48) and torch.equal(h, d["h0"])
     assert kb.kda_get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G", [1, 4])
+def test_a_uniform_batch_without_tokens_hands_the_state_through(G):
+    d = make(3, 3, 40, 16, G)
+    none = {k: d[k].unflatten(0, (3, 1))[:, :0] for k in ("x", "dt", "z", "B", "C")}
+    y, h = kb.kda_ssm_scan_fwd(none["x"], none["dt"], d["A"], none["B"], none["C"], d["D"], none["z"],
+                               d["dt_bias"], d["h0"])
+    assert y.shape == (3, 0, 40) and torch.equal(h, d["h0"])
