@@ -569,7 +569,8 @@ def kda_decode_tokens_fused(q_raw, k_raw, v, gate, beta, S_inout, commit=None, o
 
 # ---- operators around the recurrent layer.  Tensors may be column slices of wider ones: rows
 # with a unit last stride, any row stride (over all leading dimensions).  Outputs that are not
-# given are allocated on the call's stream.
+# given are allocated on the call's stream.  All tensors of a call, and its stream, are on one
+# GPU, which need not be the current one.
 
 def _ops():
     """The module of csrc/kda_torch.cpp, its calls going to the library that load() returns."""
@@ -591,6 +592,9 @@ def _call(stream, name, *args):
     f = getattr(_selected or _ops(), name)
     if stream is None:
         return f(*args)
+    x = args[0]
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.device != stream.device:
+        raise KdaError(1, f"the stream is on {stream.device}, the tensors on {x.device}")
     with torch.cuda.stream(stream):  # its outputs too belong to that stream
         return f(*args)
 

@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/Exceptions.h>
@@ -124,8 +125,11 @@ kda_dtype code_of(at::ScalarType t, const char* name) {
   if (t == at::kFloat) return KDA_F32;
   refuse("%s must be bfloat16 or float32, got %s", name, type_name(t));
 }
-void of_type(const Tensor& t, at::ScalarType type, const char* name) {
+// Of that type, on x's GPU (the library runs on one GPU and cannot tell whose a pointer is).
+void of_type(const Tensor& t, at::ScalarType type, const char* name, const Tensor& x) {
   if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
+  if (t.get_device() != x.get_device())
+    refuse("%s is on cuda:%d, expected cuda:%d", name, (int)t.get_device(), (int)x.get_device());
   if (t.scalar_type() != type)
     refuse("%s must be %s, got %s", name, type_name(type), type_name(t.scalar_type()));
 }
@@ -153,15 +157,16 @@ Rows rows(void* p, at::IntArrayRef shape, at::IntArrayRef stride, const char* na
   if (refused) refuse("%s: the leading dimensions must be one row stride apart", name);
   return Rows{p, ld};
 }
-Rows rows(const Tensor& t, at::ScalarType type, const char* name) {
+Rows rows(const Tensor& t, at::ScalarType type, const char* name, const Tensor& x) {
   if (!t.defined()) return Rows{};
-  of_type(t, type, name);
+  of_type(t, type, name, x);
   return rows(t.data_ptr(), t.sizes(), t.strides(), name);
 }
 // A contiguous tensor of that shape, or none.
-void* dense(const Tensor& t, at::IntArrayRef shape, at::ScalarType type, const char* name) {
+void* dense(const Tensor& t, at::IntArrayRef shape, at::ScalarType type, const char* name,
+            const Tensor& x) {
   if (!t.defined()) return nullptr;
-  of_type(t, type, name);
+  of_type(t, type, name, x);
   if (!t.is_contiguous()) refuse("%s must be contiguous", name);
   same_shape(t, shape, name);
   return t.data_ptr();
@@ -176,7 +181,13 @@ Tensor output(PyObject* given, at::IntArrayRef shape, at::ScalarType type, const
   return t;
 }
 
-void* stream_of(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
+// For the time of a library call x's GPU is the current one; its current stream.
+struct Launch {
+  c10::cuda::CUDAGuard guard;
+  void* stream;
+  explicit Launch(const Tensor& x)
+      : guard(x.device()), stream(c10::cuda::getCurrentCUDAStream(x.get_device()).stream()) {}
+};
 
 int64_t row_count(const Tensor& t) {
   int64_t n = 1;
@@ -209,7 +220,7 @@ Sequences sequences(const Tensor& x, PyObject* cu_o, PyObject* n_o) {
   Sequences s{row_count(x), 0, nullptr};
   if (cu.defined()) {
     if (cu.dim() != 1 || cu.size(0) < 1) refuse("cu_seqlens must be a vector of n_seqs + 1 elements");
-    s.cu = static_cast<const int32_t*>(dense(cu, cu.sizes(), at::kInt, "cu_seqlens"));
+    s.cu = static_cast<const int32_t*>(dense(cu, cu.sizes(), at::kInt, "cu_seqlens", x));
     s.count = narrow(cu.size(0) - 1, "n_seqs");
   } else {
     s.count = narrow(n_o != Py_None ? integer(n_o) : x.dim() > 2 ? x.size(0) : 1, "n_seqs");
@@ -228,13 +239,13 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = x.scalar_type();
     const kda_dtype code = code_of(type, "x"), w_code = code_of(weight.scalar_type(), "weight");
     const int64_t dim = x.sizes().back(), groups = (dim + 127) / 128;
-    const Rows xr = rows(x, type, "x");
-    const void* wp = dense(weight, {dim}, weight.scalar_type(), "weight");
+    const Rows xr = rows(x, type, "x", x);
+    const void* wp = dense(weight, {dim}, weight.scalar_type(), "weight", x);
     if (residual.defined()) same_shape(residual, x.sizes(), "residual");
-    const Rows rr = rows(residual, type, "residual");
+    const Rows rr = rows(residual, type, "residual", x);
     Tensor h, y, scale;
     if (residual.defined() || a[6] != Py_None) h = output(a[6], x.sizes(), type, x, "h");
-    const Rows hr = rows(h, type, "h");
+    const Rows hr = rows(h, type, "h", x);
     const at::ScalarType y_type = quant ? at::kFloat8_e4m3fn : type;
     if (quant && a[4] == Py_None) {  // rows at multiples of 16 bytes, as matmul_fp8 reads them
       std::vector<int64_t> stride(x.dim(), 1);
@@ -245,11 +256,12 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       y = output(a[4], x.sizes(), y_type, x, "y");
     }
     if (quant) scale = output(a[5], with_last(x, groups), at::kFloat, x, "y_scale");
-    const Rows yr = rows(y, y_type, "y"), sr = rows(scale, at::kFloat, "y_scale");
+    const Rows yr = rows(y, y_type, "y", x), sr = rows(scale, at::kFloat, "y_scale", x);
+    const Launch on(x);
     check(g_lib->add_rms_norm(xr.p, xr.ld, rr.p, rr.ld, wp, hr.p, hr.ld, yr.p, yr.ld,
                               static_cast<float*>(sr.p), sr.ld, row_count(x), narrow(dim, "dim"),
                               static_cast<float>(real(a[3])), code, w_code, quant ? KDA_E4M3 : code,
-                              stream_of(x)));
+                              on.stream));
     PyObject* r = PyTuple_New(3);
     if (!r) return nullptr;
     auto item = [](const Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); };
@@ -272,17 +284,18 @@ PyObject* matmul_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
       refuse("a has %lld columns and b has the shape %s", (long long)K, shape_of(b.sizes()).c_str());
     same_shape(a_scale, with_last(a, blocks), "a_scale");
     same_shape(b_scale, {(N + 127) / 128, blocks}, "b_scale");
-    Rows ar = rows(a, at::kFloat8_e4m3fn, "a"), br = rows(b, at::kFloat8_e4m3fn, "b");
-    const Rows as = rows(a_scale, at::kFloat, "a_scale"), bs = rows(b_scale, at::kFloat, "b_scale");
+    Rows ar = rows(a, at::kFloat8_e4m3fn, "a", a), br = rows(b, at::kFloat8_e4m3fn, "b", a);
+    const Rows as = rows(a_scale, at::kFloat, "a_scale", a), bs = rows(b_scale, at::kFloat, "b_scale", a);
     // a single row needs no distance to a next one
     if (M == 1) ar.ld = (ar.ld + 15) / 16 * 16;
     if (N == 1) br.ld = (br.ld + 15) / 16 * 16;
     const Tensor out = output(v[4], with_last(a, N), v[5] == Py_True ? at::kFloat : at::kBFloat16, a, "out");
     const kda_dtype code = code_of(out.scalar_type(), "out");
-    const Rows o = rows(out, out.scalar_type(), "out");
+    const Rows o = rows(out, out.scalar_type(), "out", a);
+    const Launch on(a);
     check(g_lib->matmul_fp8(ar.p, ar.ld, static_cast<float*>(as.p), as.ld, br.p, br.ld,
                             static_cast<float*>(bs.p), bs.ld, o.p, o.ld, narrow(M, "M"), narrow(N, "N"),
-                            narrow(K, "K"), code, stream_of(a)));
+                            narrow(K, "K"), code, on.stream));
     return THPVariable_Wrap(out);
   });
 }
@@ -308,9 +321,9 @@ struct Conv {
       refuse("weight must have the shape (%lld, width), got %s", (long long)dim,
              shape_of(weight.sizes()).c_str());
     width = narrow(weight.size(1), "width");
-    xr = rows(x, type, "x");
-    wp = dense(weight, weight.sizes(), weight.scalar_type(), "weight");
-    bp = dense(tensor(b_o, "bias", true), {dim}, weight.scalar_type(), "bias");
+    xr = rows(x, type, "x", x);
+    wp = dense(weight, weight.sizes(), weight.scalar_type(), "weight", x);
+    bp = dense(tensor(b_o, "bias", true), {dim}, weight.scalar_type(), "bias", x);
   }
 };
 
@@ -320,15 +333,16 @@ PyObject* short_conv_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Conv c(a[0], a[1], a[2]);
     const Sequences s = sequences(c.x, a[4], a[5]);
     const int64_t shape[3] = {s.count, c.width - 1, c.dim};
-    const void* in = dense(tensor(a[3], "conv_state", true), shape, c.type, "conv_state");
+    const void* in = dense(tensor(a[3], "conv_state", true), shape, c.type, "conv_state", c.x);
     const Tensor y = output(a[8], c.x.sizes(), c.type, c.x, "y");
-    const Rows yr = rows(y, c.type, "y");
+    const Rows yr = rows(y, c.type, "y", c.x);
     Tensor state;
     if (a[7] == Py_True || a[9] != Py_None) state = output(a[9], shape, c.type, c.x, "state_out");
-    check(g_lib->short_conv_fwd(c.xr.p, c.xr.ld, c.wp, c.bp, in,
-                                dense(state, shape, c.type, "state_out"), s.cu, yr.p, yr.ld, s.tokens,
+    void* to = dense(state, shape, c.type, "state_out", c.x);
+    const Launch on(c.x);
+    check(g_lib->short_conv_fwd(c.xr.p, c.xr.ld, c.wp, c.bp, in, to, s.cu, yr.p, yr.ld, s.tokens,
                                 s.count, narrow(c.dim, "dim"), c.width, a[6] == Py_True, c.code,
-                                c.w_code, stream_of(c.x)));
+                                c.w_code, on.stream));
     return Py_BuildValue("(NN)", THPVariable_Wrap(y),
                          state.defined() ? THPVariable_Wrap(state) : Py_NewRef(Py_None));
   });
@@ -340,12 +354,13 @@ PyObject* short_conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Conv c(a[0], a[1], a[3]);
     if (c.x.dim() != 2) refuse("x must have 2 dimensions, got %s", shape_of(c.x.sizes()).c_str());
     const int64_t shape[3] = {c.x.size(0), c.width - 1, c.dim};
-    void* state = dense(tensor(a[2], "conv_state"), shape, c.type, "conv_state");
+    void* state = dense(tensor(a[2], "conv_state"), shape, c.type, "conv_state", c.x);
     const Tensor y = output(a[5], c.x.sizes(), c.type, c.x, "y");
-    const Rows yr = rows(y, c.type, "y");
+    const Rows yr = rows(y, c.type, "y", c.x);
+    const Launch on(c.x);
     check(g_lib->short_conv_step(c.xr.p, c.xr.ld, c.wp, c.bp, state, yr.p, yr.ld,
                                  narrow(c.x.size(0), "n_seqs"), narrow(c.dim, "dim"), c.width,
-                                 a[4] == Py_True, c.code, c.w_code, stream_of(c.x)));
+                                 a[4] == Py_True, c.code, c.w_code, on.stream));
     return THPVariable_Wrap(y);
   });
 }
@@ -367,7 +382,7 @@ struct Ssm {
              shape_of(t.sizes()).c_str());
     if (t.size(-2) > 1 && t.stride(-2) != t.size(-1)) refuse("%s: the groups of a token must be dense", name);
     if (t.size(-2) == 0) refuse("%s has no groups", name);
-    of_type(t, type, name);
+    of_type(t, type, name, x);
     // a token's first group stands for its row (a view by select took 2 us)
     at::DimVector shape(t.sizes()), stride(t.strides());
     shape.erase(shape.end() - 2);
@@ -383,19 +398,19 @@ struct Ssm {
     type = x.scalar_type();
     code = code_of(type, "x");
     dim = x.sizes().back();
-    xr = rows(x, type, "x");
+    xr = rows(x, type, "x", x);
     same_shape(dt, x.sizes(), "dt");
-    dtr = rows(dt, type, "dt");
+    dtr = rows(dt, type, "dt", x);
     if (z.defined()) same_shape(z, x.sizes(), "z");
-    zr = rows(z, type, "z");
+    zr = rows(z, type, "z", x);
     br = groups_of(B, "B");
     same_shape(C, B.sizes(), "C");
     cr = groups_of(C, "C");
     groups = B.size(-2);
     state = B.size(-1);
-    A = static_cast<float*>(dense(tensor(A_o, "A"), {dim, state}, at::kFloat, "A"));
-    D = static_cast<float*>(dense(tensor(D_o, "D", true), {dim}, at::kFloat, "D"));
-    bias = static_cast<float*>(dense(tensor(bias_o, "dt_bias", true), {dim}, at::kFloat, "dt_bias"));
+    A = static_cast<float*>(dense(tensor(A_o, "A"), {dim, state}, at::kFloat, "A", x));
+    D = static_cast<float*>(dense(tensor(D_o, "D", true), {dim}, at::kFloat, "D", x));
+    bias = static_cast<float*>(dense(tensor(bias_o, "dt_bias", true), {dim}, at::kFloat, "dt_bias", x));
   }
 };
 
@@ -405,16 +420,16 @@ PyObject* ssm_scan_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ssm m(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
     const Sequences s = sequences(m.x, a[9], a[10]);
     const int64_t shape[3] = {s.count, m.dim, m.state};
-    const float* h0 = static_cast<float*>(dense(tensor(a[8], "h0", true), shape, at::kFloat, "h0"));
+    const float* h0 = static_cast<float*>(dense(tensor(a[8], "h0", true), shape, at::kFloat, "h0", m.x));
     const Tensor y = output(a[13], m.x.sizes(), m.type, m.x, "y");
-    const Rows yr = rows(y, m.type, "y");
+    const Rows yr = rows(y, m.type, "y", m.x);
     Tensor h;
     if (a[12] == Py_True || a[14] != Py_None) h = output(a[14], shape, at::kFloat, m.x, "h_final");
+    float* to = static_cast<float*>(dense(h, shape, at::kFloat, "h_final", m.x));
+    const Launch on(m.x);
     check(g_lib->ssm_scan_fwd(m.xr.p, m.xr.ld, m.dtr.p, m.dtr.ld, m.A, m.br.p, m.br.ld, m.cr.p, m.cr.ld,
-                              m.D, m.zr.p, m.zr.ld, m.bias, h0, s.cu, yr.p, yr.ld,
-                              static_cast<float*>(dense(h, shape, at::kFloat, "h_final")), s.tokens,
-                              s.count, narrow(m.dim, "dim"), narrow(m.state, "state"),
-                              narrow(m.groups, "groups"), a[11] == Py_True, m.code, stream_of(m.x)));
+                              m.D, m.zr.p, m.zr.ld, m.bias, h0, s.cu, yr.p, yr.ld, to, s.tokens, s.count, narrow(m.dim, "dim"), narrow(m.state, "state"),
+                              narrow(m.groups, "groups"), a[11] == Py_True, m.code, on.stream));
     return Py_BuildValue("(NN)", THPVariable_Wrap(y),
                          h.defined() ? THPVariable_Wrap(h) : Py_NewRef(Py_None));
   });
@@ -426,14 +441,15 @@ PyObject* ssm_scan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ssm m(a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[8]);
     if (m.x.dim() != 2) refuse("x must have 2 dimensions, got %s", shape_of(m.x.sizes()).c_str());
     const int64_t shape[3] = {m.x.size(0), m.dim, m.state};
-    float* h = static_cast<float*>(dense(tensor(a[5], "h"), shape, at::kFloat, "h"));
+    float* h = static_cast<float*>(dense(tensor(a[5], "h"), shape, at::kFloat, "h", m.x));
     const Tensor y = output(a[10], m.x.sizes(), m.type, m.x, "y");
-    const Rows yr = rows(y, m.type, "y");
+    const Rows yr = rows(y, m.type, "y", m.x);
+    const Launch on(m.x);
     check(g_lib->ssm_scan_step(m.xr.p, m.xr.ld, m.dtr.p, m.dtr.ld, m.A, m.br.p, m.br.ld, m.cr.p, m.cr.ld,
                                m.D, m.zr.p, m.zr.ld, m.bias, h, yr.p, yr.ld,
                                narrow(m.x.size(0), "n_seqs"), narrow(m.dim, "dim"),
                                narrow(m.state, "state"), narrow(m.groups, "groups"), a[9] == Py_True,
-                               m.code, stream_of(m.x)));
+                               m.code, on.stream));
     return THPVariable_Wrap(y);
   });
 }
