@@ -221,3 +221,26 @@ def test_reads_what_the_norm_writes_with_dimensions_of_one(lead):
     assert out.shape == (*lead, 200)
     q2, s2, _ = kb.kda_add_rms_norm_quant(x.view(-1, 2051), torch.ones(2051, device=DEV))
     assert torch.equal(out.view(-1, 200), kb.kda_matmul_fp8(q2, s2, b, sb, out_dtype=torch.float32))
+
+
+def test_loaded_sums_are_used_together_with_what_the_wait_passes_on():
+    """A load from tensor memory returns before its registers are written.  Their first use stands
+    behind the wait because it also takes a scale that went through the wait; a statement that
+    took nothing but the registers (a pairing, a move to another kind) could be moved before it,
+    and no result would tell until a compiler does so.  So the source is looked at."""
+    import os
+    import re
+    path = os.path.join(os.path.dirname(kb.__file__), "csrc", "kda_matmul_fp8.cu")
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    loads = re.findall(r'tcgen05\.ld\.sync.*?:\s*"r"\(taddr\)', text, re.S)
+    assert loads and all('"=f"(r[0])' in x and '"=r"' not in x for x in loads)
+    uses = re.findall(r"[^;{}\n]*\bd\[[^;]*;", text)
+    assert uses
+    for use in uses:
+        use = " ".join(use.split())
+        assert (re.fullmatch(r"float d\[G::kLoad\];", use)
+                or re.fullmatch(r"(lo|hi) = fmaf\(d\[[^]]*\], s[01], \1\);", use)
+                or re.fullmatch(r"add_scaled_pair\(lo, hi, d\[j\], d\[j \+ 1\], s0, s1\);", use)), use
+    assert re.search(r"const float scale =\s*wait_ld\(", text)
+    assert all(re.search(rf"const float {s} = SWAP \? __shfl_sync\(0xffffffffu, scale, .*: scale;", text)
+               for s in ("s0", "s1"))
