@@ -310,8 +310,14 @@ __device__ __forceinline__ float rcp(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// v sigmoid(v).  The approximate exponential and reciprocal are within a few
-// units of the last place of the 32-bit result.
+// v sigmoid(v).  Relative error: (1.25 |v| + 8) 2^-24, of which 1.25 |v| is the
+// rounding of the exponent v log2 e and the rest the approximate exponential
+// (2^-22.5) and reciprocal (2^-23) and two roundings.  Below v = -87.3 the
+// reciprocal is smaller than 2^-126 and flushed: the result is -0, less than
+// 88 * 2^-126 = 1.1e-36 off.  (The quotient in 32 bits, v / (1 + e^-v), is -0 from
+// v = -88.8 on.  Scaled by powers of two so that the result fades out instead,
+// the convolution was 2 to 3.5 % slower and the scan of 4 x 4096 tokens, 4096
+// channels 10 %: 427 -> 471 us.)
 __device__ __forceinline__ float silu(float v) { return v * rcp(1.0f + ex2(v * -kLog2e)); }
 
 }  // namespace kda

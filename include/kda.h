@@ -497,7 +497,8 @@ kda_status kda_matmul_fp8(const void *a, int64_t ld_a, const float *a_scale,
  *
  *     y[t, d] = act(bias[d] + sum_j weight[d, j] x[t - width + 1 + j, d])
  *
- * act is SiLU (`activation` != 0) or nothing.  The width - 1 rows before a
+ * act is SiLU (`activation` != 0; a result smaller than 1.1e-36 may be 0) or
+ * nothing.  The width - 1 rows before a
  * sequence's first token are those of its state, or zeros; the last
  * width - 1 rows of state and tokens together are its state afterwards.  Sums
  * are in 32 bits, y is rounded once, the state is copied.
@@ -542,7 +543,7 @@ kda_status kda_short_conv_step(const void *x, int64_t ld_x, const void *weight,
  *     y   = sum(h C) + D[d] x;   with a gate z, y = y * z sigmoid(z)
  * B and C of a token are shared by the dim / groups channels of a group
  * (channel d is in group d / (dim / groups)).  Everything is in 32 bits; y is
- * rounded once.
+ * rounded once.  A gate z sigmoid(z) smaller than 1.1e-36 may be 0.
  *
  * Tensors (T = total_tokens, N = n_seqs; the step: one token per sequence, T = N):
  *   x, dt, z   bf16 or f32 (`dtype`) [T, dim]    read; z may be NULL (no gate)

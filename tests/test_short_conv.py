@@ -229,3 +229,24 @@ def test_a_uniform_batch_without_tokens_hands_the_state_through():
     _, w, b, s = inputs([1] * 3, 40, 4, torch.bfloat16)
     y, out = kb.kda_short_conv_fwd(torch.empty(3, 0, 40, dtype=torch.bfloat16, device=DEV), w, b, s)
     assert y.shape == (3, 0, 40) and torch.equal(out, s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [1, 2, 4])
+def test_silu_far_out(dim):
+    """Large pre-activations of both signs.  In half ulps: the exponent's rounding and its
+    constant's move the exponential by 1.25 |v|; the exponential's own error (2^-22.5 = 2.8), the
+    reciprocal's (2^-23 = 2) and the sum's and product's roundings are under 8.  Where the sigmoid
+    is below 2^-126 (v < -87.3) the result may be 0."""
+    v = torch.cat([torch.linspace(-110, 110, 20001), torch.tensor([-1e-30, 1e-30, -1e-38, 1e30, 3e38, -3e38]),
+                   torch.zeros(1)]).to(DEV)
+    v = v[:v.numel() // dim * dim]
+    x = v.view(-1, dim).contiguous()
+    w = torch.tensor([0.0, 1.0], device=DEV).repeat(dim, 1)
+    ref = v.double() * torch.sigmoid(v.double())
+    atol = 1.25 * v.double().abs().clamp(max=120) * 2.0 ** -24 * ref.abs()
+    atol = torch.where(v < -87.3, torch.maximum(atol, ref.abs()), atol)
+    for y in (kb.kda_short_conv_fwd(x, w)[0],
+              kb.kda_short_conv_step(x, w, torch.zeros(x.shape[0], 1, dim, device=DEV))):
+        assert_near(y.flatten(), ref, 8 * 2.0 ** -24, "y", atol=atol)
+        assert ((y.flatten() - ref).abs()[v < -87.3] <= 88 * 2.0 ** -126).all()

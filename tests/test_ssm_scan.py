@@ -320,3 +320,21 @@ def test_a_uniform_batch_without_tokens_hands_the_state_through(G):
     y, h = kb.kda_ssm_scan_fwd(none["x"], none["dt"], d["A"], none["B"], none["C"], d["D"], none["z"],
                                d["dt_bias"], d["h0"])
     assert y.shape == (3, 0, 40) and torch.equal(h, d["h0"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [33, 64])
+def test_gate_far_out(dim):
+    """y is the gate's SiLU alone (no readout, D x = 1); its tolerance as in the convolution's test
+    of the same."""
+    z = torch.linspace(-110, 110, 300 * dim, device=DEV).view(300, dim)
+    d = make(300, 1, dim, 16, dtype=torch.float32)
+    one, none = torch.ones(300, dim, device=DEV), torch.zeros_like(d["C"])
+    ref = z.double() * torch.sigmoid(z.double())
+    atol = 1.25 * z.double().abs() * 2.0 ** -24 * ref.abs()
+    atol = torch.where(z < -87.3, torch.maximum(atol, ref.abs()), atol)
+    y, _ = kb.kda_ssm_scan_fwd(one, d["dt"], d["A"], d["B"], none, one[0], z, d["dt_bias"])
+    assert_near(y, ref, 8 * 2.0 ** -24, "y", atol=atol)
+    h = torch.zeros(300, dim, 16, device=DEV)
+    y = kb.kda_ssm_scan_step(one, d["dt"], d["A"], d["B"], none, h, one[0], z, d["dt_bias"])
+    assert_near(y, ref, 8 * 2.0 ** -24, "y", atol=atol)
