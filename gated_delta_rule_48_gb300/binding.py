@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sysconfig
 import threading
+import warnings
 
 import numpy as np
 import torch
@@ -87,22 +88,49 @@ def _build_extension(force: bool = False):
            "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
            "-I", _INCLUDE, src, "-o", _EXT + f".tmp{os.getpid()}", "-L", lib, "-ltorch",
            "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", "-ldl"]
-    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    try:
+        return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:  # no such compiler
+        return cmd, e
+
+
+def _finish_extension(ext, verbose: bool = False) -> str:
+    """Wait for what :func:`_build_extension` started.  Returns why it failed, or "" with
+    ``_EXT`` in place; after a failure there is no (older) ``_EXT``."""
+    if ext is None:
+        return ""
+    cmd, p = ext
+    if isinstance(p, OSError):
+        why = str(p)
+    else:
+        why = p.communicate()[0].decode(errors="replace")
+        if verbose:
+            print(why)
+        if p.returncode == 0:
+            os.replace(_EXT + f".tmp{os.getpid()}", _EXT)
+            return ""
+    if os.path.exists(_EXT):
+        os.unlink(_EXT)
+    return f"compilation failed:\n{' '.join(cmd)}\n{why}"
 
 
 def _finish(procs, verbose):
-    """Wait for compilations; raise if one failed."""
+    """Wait for the library's compilations; raise if one failed."""
     failed = []
-    for cmd, p in filter(None, procs):
+    for cmd, p in procs:
         out, _ = p.communicate()
         if verbose or p.returncode:
             print(out.decode(errors="replace"))
         if p.returncode:
             failed.append(" ".join(cmd))
-        elif cmd[0] == "g++":
-            os.replace(_EXT + f".tmp{os.getpid()}", _EXT)
     if failed:
-        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
+        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+
+
+def _warn(failure: str):
+    if failure:
+        warnings.warn(f"the operators' Python calls are not available: {failure}", RuntimeWarning,
+                      stacklevel=3)
 
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
@@ -112,6 +140,11 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
 
     Translation units compile in parallel; nvcc cross-compiles, so no GPU is
     needed.  Rebuilds only when a source or header is newer than the library.
+
+    The module that takes torch tensors to the operators is compiled beside it.
+    The library does not need it (nor torch's and Python's headers): where it
+    cannot be compiled that is a warning here, and an error of the operators'
+    Python calls.
     """
     bdir, lib_path = (_BUILD_CHECKED, _LIB_CHECKED) if checked else (_BUILD, _LIB)
     os.makedirs(bdir, exist_ok=True)
@@ -119,20 +152,22 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     srcs = _sources()
     newest = max(os.path.getmtime(p) for p in srcs + _headers())
     if not force and os.path.exists(lib_path) and os.path.getmtime(lib_path) >= newest:
-        _finish([ext], verbose)
+        _warn(_finish_extension(ext, verbose))
         return lib_path
     common = ["nvcc", *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-I", _INCLUDE, "-I", _CSRC, "--expt-relaxed-constexpr"]
     if checked:
         common.append("-DKDA_BOUNDS_CHECK")
-    objs, procs = [], [ext]
+    objs, procs = [], []
     for src in srcs:
         obj = os.path.join(bdir, os.path.basename(src) + ".o")
         objs.append(obj)
         cmd = common + ["-c", src, "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                              stderr=subprocess.STDOUT)))
+    failure = _finish_extension(ext, verbose)
     _finish(procs, verbose)
+    _warn(failure)
     tmp = lib_path + f".tmp{os.getpid()}"
     subprocess.check_call(["nvcc", *ARCH_FLAGS, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib_path)
@@ -579,7 +614,9 @@ def _ops():
     with _lock:
         if _extension is None:
             if not os.path.exists(_EXT):
-                _finish([_build_extension()], False)
+                failure = _finish_extension(_build_extension())
+                if failure:
+                    raise RuntimeError(f"kda_torch: {failure}")
             spec = importlib.util.spec_from_file_location("kda_torch", _EXT)
             _extension = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(_extension)
