@@ -103,7 +103,8 @@ struct State {
       for (int q = 0; q < kPairs / 2; ++q) {
         const int64_t e = (c + k) * S + at(lane4, q);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < live && kda_guard(e, 4, dim * S, err)) v = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
+        // (A may be null where there are no tokens)
+        if (A && k < live && kda_guard(e, 4, dim * S, err)) v = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
         a[k][2 * q] = pack2(v.x * kLog2e, v.y * kLog2e);
         a[k][2 * q + 1] = pack2(v.z * kLog2e, v.w * kLog2e);
       }

@@ -338,3 +338,19 @@ def test_gate_far_out(dim):
     h = torch.zeros(300, dim, 16, device=DEV)
     y = kb.kda_ssm_scan_step(one, d["dt"], d["A"], d["B"], none, h, one[0], z, d["dt_bias"])
     assert_near(y, ref, 8 * 2.0 ** -24, "y", atol=atol)
+
+
+@pytest.mark.gpu
+def test_no_tokens_need_no_inputs():
+    """T = 0 through the C entry with every input NULL, as the other inputs may be: the states are
+    handed through, or zeros."""
+    N, dim, S = 3, 40, 16
+    h0 = torch.randn(N, dim, S, device=DEV)
+    for given, want in ((h0, h0), (None, torch.zeros_like(h0))):
+        h = torch.full_like(h0, 7.0)
+        torch.cuda.synchronize()
+        st = kb.load().kda_ssm_scan_fwd(None, dim, None, dim, None, None, S, None, S, None, None, dim, None,
+                                        None if given is None else ctypes.c_void_p(given.data_ptr()), None,
+                                        None, dim, ctypes.c_void_p(h.data_ptr()), 0, N, dim, S, 1, 1, 0, None)
+        assert st == 0 and kb.kda_get_device_error() == 0
+        assert torch.equal(h, want)
