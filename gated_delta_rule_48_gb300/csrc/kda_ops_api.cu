@@ -393,6 +393,9 @@ extern "C" kda_status kda_matmul_fp8(const void* a, int64_t ld_a, const float* a
   KDA_TRY(check_rows("b", b, ld_b, K, 1));
   KDA_TRY(check_rows("b_scale", b_scale, ld_b_scale, kb, 4));
   KDA_TRY(check_rows("out", out, ld_out, N, os));
+  // (a single row has no next one, whatever its distance)
+  if (M == 1) ld_a = (ld_a + 15) / 16 * 16;
+  if (N == 1) ld_b = (ld_b + 15) / 16 * 16;
   const struct { const void* p; int64_t ld; const char* n; } wide[] = {{a, ld_a, "a"}, {b, ld_b, "b"}};
   for (auto& w : wide)  // the tensor copies' rule
     if (!aligned(w.p, 16) || w.ld % 16 != 0)

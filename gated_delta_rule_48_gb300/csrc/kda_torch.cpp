@@ -284,11 +284,8 @@ PyObject* matmul_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
       refuse("a has %lld columns and b has the shape %s", (long long)K, shape_of(b.sizes()).c_str());
     same_shape(a_scale, with_last(a, blocks), "a_scale");
     same_shape(b_scale, {(N + 127) / 128, blocks}, "b_scale");
-    Rows ar = rows(a, at::kFloat8_e4m3fn, "a", a), br = rows(b, at::kFloat8_e4m3fn, "b", a);
+    const Rows ar = rows(a, at::kFloat8_e4m3fn, "a", a), br = rows(b, at::kFloat8_e4m3fn, "b", a);
     const Rows as = rows(a_scale, at::kFloat, "a_scale", a), bs = rows(b_scale, at::kFloat, "b_scale", a);
-    // a single row needs no distance to a next one
-    if (M == 1) ar.ld = (ar.ld + 15) / 16 * 16;
-    if (N == 1) br.ld = (br.ld + 15) / 16 * 16;
     const Tensor out = output(v[4], with_last(a, N), v[5] == Py_True ? at::kFloat : at::kBFloat16, a, "out");
     const kda_dtype code = code_of(out.scalar_type(), "out");
     const Rows o = rows(out, out.scalar_type(), "out", a);

@@ -244,3 +244,18 @@ def test_loaded_sums_are_used_together_with_what_the_wait_passes_on():
     assert re.search(r"const float scale =\s*wait_ld\(", text)
     assert all(re.search(rf"const float {s} = SWAP \? __shfl_sync\(0xffffffffu, scale, .*: scale;", text)
                for s in ("s0", "s1"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(1, 300), (5, 1), (1, 1)])
+def test_a_single_row_through_the_c_entry(M, N):
+    """Its only row starts on a 16-byte boundary, whatever the distance to a next one."""
+    K = 203
+    a, sa, b, sb, want = check(M, N, K, torch.float32)
+    out = torch.empty(M, N, device=DEV)
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())
+    torch.cuda.synchronize()
+    st = kb.load().kda_matmul_fp8(ptr(a), K if M == 1 else a.stride(0), ptr(sa), 2, ptr(b),
+                                  K if N == 1 else b.stride(0), ptr(sb), 2, ptr(out), N, M, N, K, 1, None)
+    assert st == 0 and kb.kda_get_device_error() == 0
+    assert torch.equal(out, want)
