@@ -205,7 +205,8 @@ const Tensor& matrix(const Tensor& t, const char* name) {
   return t;
 }
 int32_t narrow(int64_t v, const char* name) {
-  if (v > INT32_MAX) refuse("%s=%lld is too large", name, (long long)v);
+  if (v < 0 || v > INT32_MAX)
+    refuse("%s=%lld is %s", name, (long long)v, v < 0 ? "negative" : "too large");
   return static_cast<int32_t>(v);
 }
 
@@ -318,6 +319,7 @@ struct Conv {
       refuse("weight must have the shape (%lld, width), got %s", (long long)dim,
              shape_of(weight.sizes()).c_str());
     width = narrow(weight.size(1), "width");
+    if (width == 0) refuse("weight has a width of 0");
     xr = rows(x, type, "x", x);
     wp = dense(weight, weight.sizes(), weight.scalar_type(), "weight", x);
     bp = dense(tensor(b_o, "bias", true), {dim}, weight.scalar_type(), "bias", x);

@@ -1,6 +1,6 @@
-"""The operators' Python calls refuse tensors of several GPUs, and a stream of another one, on the
-host and before anything is allocated or launched.  The tensors here have a device, a shape and
-strides and no memory, so that no GPU is needed."""
+"""The operators' Python calls refuse tensors of several GPUs, a stream of another one, and sizes
+that no tensor has, on the host and before anything is allocated or launched.  The tensors here
+have a device, a shape and strides and no memory, so that no GPU is needed."""
 import types
 
 import pytest
@@ -58,3 +58,18 @@ def test_a_stream_of_another_gpu_is_refused(name):
     other = types.SimpleNamespace(device=torch.device("cuda:1"))
     with pytest.raises(kb.KdaError, match="the stream is on cuda:1, the tensors on cuda:0"):
         getattr(kb, name)(**arguments(name), stream=other)
+
+
+@pytest.mark.parametrize("name", ["kda_short_conv_fwd", "kda_ssm_scan_fwd"])
+def test_a_negative_number_of_sequences_is_refused(name):
+    made = arguments(name)
+    made["cu_seqlens"] = made["conv_state" if "conv" in name else "h0"] = None
+    made["state_out" if "conv" in name else "h_final"] = None
+    with pytest.raises(kb.KdaError, match="n_seqs=-1 is negative"):
+        getattr(kb, name)(**made, n_seqs=-1)
+
+
+@pytest.mark.parametrize("name", ["kda_short_conv_fwd", "kda_short_conv_step"])
+def test_a_convolution_of_width_zero_is_refused(name):
+    with pytest.raises(kb.KdaError, match="width of 0"):
+        getattr(kb, name)(**(arguments(name) | dict(weight=bare((32, 0)))))
