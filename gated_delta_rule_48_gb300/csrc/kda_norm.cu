@@ -9,7 +9,8 @@
 // The norm is taken of the 32-bit sum, before h is rounded for storage.
 //
 // Bound: HBM.  Every element is read once and written once: a row stays in
-// registers between its sum of squares and its scaling.  A warp takes 256
+// registers between its sum of squares and its scaling (above 16,384 columns, 64
+// values a thread, partly in local memory).  A warp takes 256
 // columns at a time, 8 to a lane, so a group of 128 columns lies in half a
 // warp (16-byte loads of consecutive columns) or, where rows do not start on
 // 16-byte boundaries, in four of each lane's eight elements (one element per
@@ -19,7 +20,14 @@
 // 16384 x 4096 bf16 rows with a residual to e4m3: 83 us, 5.7 TB/s (94 us with a
 // block for each row, whose loads then wait for nothing but its own end);
 // 1777 x 2051 32-bit rows (no two of them aligned alike): 11 us, 4.3 TB/s; one
-// row of 4096: 1.9 us.
+// row of 4096: 1.9 us.  Above 8192 columns no next row is fetched ahead: 4096 x
+// 12288 and 4096 x 32768 bf16 rows with a residual to e4m3 take 92 and 330 us, 3.9
+// and 2.9 TB/s.
+//
+// A value is multiplied by 448 / max rather than divided by the scale: one
+// division a group.  Of bf16 rows 8 values in a million then come out one step of
+// e4m3 beside the quotient's, those that lie within 1e-7 of the middle between
+// two steps; either way the rows are equally far from the unrounded ones.
 #include <cuda_runtime.h>
 
 #include <algorithm>
