@@ -167,10 +167,10 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
                                              stderr=subprocess.STDOUT)))
     failure = _finish_extension(ext, verbose)
     _finish(procs, verbose)
-    _warn(failure)
     tmp = lib_path + f".tmp{os.getpid()}"
     subprocess.check_call(["nvcc", *ARCH_FLAGS, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib_path)
+    _warn(failure)  # (with the library in place, should warnings be errors)
     return lib_path
 
 

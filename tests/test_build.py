@@ -2,6 +2,7 @@
 torch or Python), and only that module's calls fail then."""
 import os
 import subprocess
+import warnings
 
 import pytest
 import torch
@@ -59,3 +60,12 @@ def test_a_library_that_does_not_compile_is_an_error(elsewhere, monkeypatch):
     with pytest.raises(RuntimeError, match="nvcc failed"):
         kb.build()
     assert not os.path.exists(kb._LIB)
+
+
+def test_the_library_is_there_where_warnings_are_errors(elsewhere, monkeypatch):
+    no_compiler(monkeypatch)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning, match="operators' Python calls are not available"):
+            kb.build()
+    assert os.path.exists(kb._LIB)
