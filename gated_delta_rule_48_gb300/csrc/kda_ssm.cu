@@ -12,22 +12,23 @@
 // Everything is in 32 bits; exp(dt' A) is 2^(dt' (A log2 e)) by the hardware's
 // approximate exponential.
 //
-// Floor: per token, channel and state value one exponential and four multiply-adds
-// (against 8 bytes per token and channel).  What holds it above is that few warps
-// hide each other's latencies: with 164 registers a thread a scheduler has two
-// or three, and issues in 53 to 62 % of its cycles, no pipe above 66 %.  Where
-// whole sequences make 256 blocks for 152 SMs, 104 of these have two and 48 one.
-// Four lanes
-// share two neighbouring channels, a quarter of their states each, and take a
-// tile of tokens at a time.  What a token needs once (softplus, gate, loads,
-// the store) is done by the lane whose number is the token's, and (dt', dt' x)
-// handed round through shared memory, so nothing is computed four times; B and
-// C are converted once per block, and a lane's read of them serves both
-// channels (with one channel per lane the reads bound the kernel, and it was
-// 15 % slower).  The recurrence runs on pairs of 32-bit values in one
-// instruction (12 % faster than single ones), and a token's decays are
-// computed three tokens ahead of its turn.  Three tiles are under way: one in
-// the recurrence, one staged beside it, one in flight to registers.
+// Floor: per token, channel and state value one exponential and four multiply-
+// adds (against 8 bytes per token and channel).  What holds it above is that
+// few warps hide each other's latencies: with 164 registers a thread a
+// scheduler has two or three, and issues in 43 to 62 % of its cycles, no pipe
+// above 66 %.  Where whole sequences make 256 blocks for 152 SMs, 104 of these
+// have two and 48 one.
+//
+// Four lanes share two neighbouring channels, a quarter of their states each,
+// and take a tile of tokens at a time.  What a token needs once (softplus,
+// gate, loads, the store) is done by the lane whose number is the token's, and
+// (dt', dt' x) handed round through shared memory, so nothing is computed four
+// times; B and C are converted once per block, and a lane's read of them serves
+// both channels (with one channel per lane the reads bound the kernel, and it
+// was 15 % slower).  The recurrence runs on pairs of 32-bit values in one
+// instruction (12 % faster than single ones), and a token's decays are computed
+// three tokens ahead of its turn.  Three tiles are under way: one in the
+// recurrence, one staged beside it, one in flight to registers.
 //
 // 16,384 tokens x 4096 channels x 16 states, bf16 with gate: 0.42 ms (1.3 TB/s
 // of inputs and outputs); the tokens' own work is a third of the instructions.
@@ -38,8 +39,8 @@
 // first launch computes h_local and sum(dt') of such pieces, and in the second
 // each block chains the pieces before its own to its entry state, one after the
 // other: in one sequence of 65,536 tokens that is 14 pieces at 2048 channels, but
-// up to 454 at 64 (second launch 97 us, the first, which computes nearly the
-// same, 21 us).  Where no sequence is cut there is one launch.
+// up to 454 at 64 (second launch 97 us, the first, the same without the readout,
+// 21 us).  Where no sequence is cut there is one launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -563,7 +563,8 @@ kda_status kda_short_conv_step(const void *x, int64_t ld_x, const void *weight,
  * state is 16, 32, 64 or 128, else KDA_ERR_UNSUPPORTED.  T = 0 or N = 0 are valid.
  *
  * Prompts with few sequences and channels are cut into chunks of tokens that
- * run side by side; results are the same up to rounding.  That takes a
+ * run side by side; results are the same up to rounding (states that grow,
+ * dt' A > 0, by less than 2^128 over a chunk).  That takes a
  * workspace, allocated and freed stream-ordered on `stream`, of
  * (state + 1) * dim * 4 bytes per chunk, and a copy of h0 where h_final is h0.
  * The step allocates nothing.
