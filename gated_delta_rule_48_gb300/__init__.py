@@ -11,9 +11,14 @@ from .binding import (  # noqa: F401
     build,
     kda_add_rms_norm,
     kda_add_rms_norm_quant,
+    kda_attention_fwd,
     kda_chunk_fwd,
     kda_decode_step,
     kda_get_device_error,
+    kda_kv4_attention,
+    kda_kv4_cache,
+    kda_kv4_read,
+    kda_kv4_write,
     kda_matmul_fp8,
     kda_short_conv_fwd,
     kda_short_conv_step,
@@ -23,7 +28,8 @@ from .binding import (  # noqa: F401
     load,
 )
 
-__all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_chunk_fwd",
-           "kda_decode_step", "kda_get_device_error", "kda_matmul_fp8", "kda_short_conv_fwd",
+__all__ = ["KdaError", "build", "kda_add_rms_norm", "kda_add_rms_norm_quant", "kda_attention_fwd",
+           "kda_chunk_fwd", "kda_decode_step", "kda_get_device_error", "kda_kv4_attention",
+           "kda_kv4_cache", "kda_kv4_read", "kda_kv4_write", "kda_matmul_fp8", "kda_short_conv_fwd",
            "kda_short_conv_step", "kda_ssm_scan_fwd",
            "kda_ssm_scan_step", "library_path", "load"]

@@ -180,6 +180,12 @@ class KdaTensor(ctypes.Structure):
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
 
 
+class KdaKv4Cache(ctypes.Structure):
+    """``kda_kv4_cache`` of include/kda.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + [
+        (n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "d")]
+
+
 KDA_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.int32: 2, torch.float8_e4m3fn: 3}
 
 
@@ -281,6 +287,16 @@ def load():
             lib.kda_matmul_fp8.restype = i
             lib.kda_matmul_fp8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32,
                                            i32, i, vp]
+            cp = ctypes.POINTER(KdaKv4Cache)
+            lib.kda_attention_fwd.restype = i
+            lib.kda_attention_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, i64,
+                                              i32, i32, i32, i32, f32, i32, vp]
+            for name in ("kda_kv4_write", "kda_kv4_read"):
+                getattr(lib, name).restype = i
+                getattr(lib, name).argtypes = [vp, i64, vp, i64, cp, vp, i64, i32, vp, vp, i64, i32, vp]
+            lib.kda_kv4_attention.restype = i
+            lib.kda_kv4_attention.argtypes = [vp, i64, cp, vp, i64, i32, vp, vp, i64, vp, i32, i32, i32,
+                                              f32, vp]
             lib.kda_profile_enable.restype = None
             lib.kda_profile_enable.argtypes = [ctypes.c_int]
             lib.kda_profile_read.restype = ctypes.c_int
@@ -703,3 +719,61 @@ def kda_ssm_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, softpl
     """One token of each sequence: x, dt, z [N, dim], B, C [N, groups, state]; ``h`` f32
     [N, dim, state] is updated in place.  Otherwise as :func:`kda_ssm_scan_fwd`.  Returns y."""
     return _call(stream, "ssm_scan_step", x, dt, A, B, C, h, D, z, dt_bias, bool(softplus), y)
+
+
+# ---- full attention and its cache in 4 bits
+
+def kda_attention_fwd(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, n_seqs=None, causal=True,
+                      scale=None, want_lse=False, out=None, lse=None, stream=None):
+    """Attention over prompts (see include/kda.h).
+
+    q: bf16 [Tq, heads, d] (or [B, Tq_b, heads, d], a uniform batch); k, v: bf16 [Tk, kv_heads, d]
+    (or [B, Tk_b, kv_heads, d]); a token's heads are dense, tokens may be any multiple of 16 bytes
+    apart; cu_seqlens_q: int32 [N + 1] (CUDA) or None; cu_seqlens_k: the same for keys, None where
+    they are the queries'.  With fewer queries than keys the queries are their sequence's last ones.
+    scale: 1 / sqrt(d) if None.  Returns (out, lse): out as q, lse f32 [Tq, heads] (the logarithms
+    of the sums) or None unless wanted or given.
+    """
+    return _call(stream, "attention_fwd", q, k, v, cu_seqlens_q, cu_seqlens_k, n_seqs, bool(causal),
+                 scale, bool(want_lse), out, lse)
+
+
+def kda_kv4_cache(n_pages, page_size, kv_heads, d, device="cuda"):
+    """The arrays of a paged cache in 4 bits (layout: include/kda.h): (k_codes, k_scales, v_codes,
+    v_scales), uint8 [n_pages, kv_heads, page_size, d / 2] and bf16 [.., d / 32], of zeros."""
+    new = lambda n, dtype: torch.zeros(n_pages, kv_heads, page_size, n, dtype=dtype, device=device)
+    codes, scales = (d // 2, torch.uint8), (d // 32, torch.bfloat16)
+    return new(*codes), new(*scales), new(*codes), new(*scales)
+
+
+def kda_kv4_write(k, v, cache, block_table, start=None, cu_seqlens=None, *, n_seqs=None, stream=None):
+    """Quantise tokens into a paged cache (see include/kda.h), which is updated in place.
+
+    k, v: bf16 [T, kv_heads, d] or [B, T_b, kv_heads, d]; cache: as :func:`kda_kv4_cache` makes it;
+    block_table: int32 [N, max_pages], the pages of each sequence; start: int32 [N], the position of
+    each sequence's first token (None: 0; negative: that sequence is left out); cu_seqlens: int32
+    [N + 1] or None (N = block_table's rows, or ``n_seqs``, of equal length).
+    """
+    _call(stream, "kv4_write", k, v, cache, block_table, start, cu_seqlens, n_seqs)
+
+
+def kda_kv4_read(cache, block_table, total_tokens, start=None, cu_seqlens=None, *, n_seqs=None, k=None,
+                 v=None, stream=None):
+    """Read positions of a paged cache back: the reverse of :func:`kda_kv4_write`.  Returns (k, v),
+    bf16 [total_tokens, kv_heads, d]; rows of sequences that are left out stay as they are."""
+    if stream is not None and isinstance(block_table, torch.Tensor) and block_table.is_cuda \
+            and block_table.device != stream.device:
+        raise KdaError(1, f"the stream is on {stream.device}, the tensors on {block_table.device}")
+    return _call(stream, "kv4_read", cache, block_table, total_tokens, start, cu_seqlens, n_seqs, k, v)
+
+
+def kda_kv4_attention(q, cache, block_table, seq_lens, *, scale=None, want_lse=False, out=None, lse=None,
+                      stream=None):
+    """Attention of each sequence's last tokens over a paged cache in 4 bits (see include/kda.h).
+
+    q: bf16 [N, heads, d], or [N, n_tokens, heads, d] for several tokens of each sequence; seq_lens:
+    int32 [N], the positions in the cache, the queries' own among them; cache and block_table as for
+    :func:`kda_kv4_write`.  scale: 1 / sqrt(d) if None.  Returns (out, lse) as
+    :func:`kda_attention_fwd`.
+    """
+    return _call(stream, "kv4_attention", q, cache, block_table, seq_lens, scale, bool(want_lse), out, lse)

@@ -669,6 +669,8 @@ extern "C" kda_status kda_get_device_error(void* stream) {
     msg += "the sequences have more checkpoints than max_checkpoints (the excess was dropped); ";
   if (word & kDevErrBounds)
     msg += "a kernel index fell outside its buffer (bounds-checked build; the access was skipped); ";
+  if (word & kDevErrPage)
+    msg += "a position has no page in block_table (outside the cache, or behind the table's last column); ";
   return fail(KDA_ERR_DEVICE_INPUT, "%s", msg.c_str());
 }
 

@@ -27,6 +27,7 @@ enum DeviceError : int {
   kDevErrCommit = 8,         // a decode commit count outside [0, tokens per call]
   kDevErrCheckpoints = 16,   // more prefill checkpoints than the caller's buffer holds
   kDevErrBounds = 32,        // bounds-checked build: an index fell outside its buffer
+  kDevErrPage = 64,          // a position of a paged cache without a valid page
 };
 
 // ---- bounds-checked build.  Compiled with -DKDA_BOUNDS_CHECK, every plain

@@ -1,0 +1,202 @@
+// The cache in 4 bits: keys and values quantised as they are written into its
+// pages, and spans of it read back.
+//
+//   s = bf16(max(max |x|, 2^-64) / 7) over 32 channels,  n = x / s rounded half
+//   to even, stored as n + 8;  read back: bf16(n s)
+//
+// Bound: bytes (2 read and 0.5625 written per value, or the reverse).  Four
+// lanes take a token and head: lane j reads channels 8 j .. 8 j + 7 of every
+// group, 16 bytes at a time, and ends up with 16 bytes of codes that lie side by
+// side; a group's maximum is that of its four lanes.
+//
+// The order of a row's codes is the one in which kda_kv4_attention's lanes need
+// them.  Keys: 32-bit word j G + g holds channels 32 g + 8 j + 0..7 (G = d / 32
+// groups, nibble i the channel + i).  Values: 16-bit word r G + g holds channels
+// 32 g + 4 r + 0..3.
+#include <algorithm>
+
+#include "kda_attention.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// max(., 2^-64) / 7, rounded once more to bf16.  A NaN stays one, an infinity too.
+__device__ __forceinline__ uint32_t scale_bits(float top) {
+  return from_f32<Bf16>(__fdiv_rn(max_nan(top, kAmaxMin), 7.0f)).bits;
+}
+// n + 8; a quotient that is NaN (a group with an infinity or NaN) counts as 0
+__device__ __forceinline__ uint32_t code_of(float x, float scale) {
+  const float n = rintf(__fdiv_rn(x, scale));
+  return static_cast<uint32_t>(static_cast<int32_t>(n == n ? n : 0.0f) + 8);
+}
+
+// Words of codes of 8 channels each, one of every group: as they lie in a row of
+// keys (KEYS), or in a row of values (2 x 4 channels, the groups' halves side by
+// side).  Turns one into the other; its own inverse where G = 2.
+template <int G>
+__device__ __forceinline__ void to_values(const uint32_t (&w)[G], uint32_t (&out)[G]) {
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    out[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+    out[G / 2 + i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+  }
+}
+template <int G>
+__device__ __forceinline__ void from_values(const uint32_t (&w)[G], uint32_t (&out)[G]) {
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    out[2 * i] = __byte_perm(w[i], w[G / 2 + i], 0x5410);
+    out[2 * i + 1] = __byte_perm(w[i], w[G / 2 + i], 0x7632);
+  }
+}
+
+template <int G>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[G]) {
+  if constexpr (G == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int G>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[G]) {
+  if constexpr (G == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  }
+}
+
+// A row's part of one lane: values to codes, scales by the first lane.
+template <int G, bool KEYS>
+__device__ __forceinline__ void quantise(const Kv4Pages& p, const Bf16* x, bool valid, int64_t row,
+                                         int j, int* err) {
+  uint4 raw[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+    raw[g] = valid ? *reinterpret_cast<const uint4*>(x + 32 * g + 8 * j) : make_uint4(0, 0, 0, 0);
+  uint32_t words[G], scales[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+    float v[8], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(v[i]));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    scales[g] = scale_bits(top);
+    const float scale = __uint_as_float(scales[g] << 16);
+    words[g] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) words[g] |= code_of(v[i], scale) << (4 * i);
+  }
+  const int64_t rows = kv4_rows(p);
+  if (!valid || !kda_guard(row, 1, rows, err)) return;
+  uint8_t* codes = (KEYS ? p.k_codes : p.v_codes) + row * (16 * G) + 4 * G * j;
+  if constexpr (KEYS) {
+    store_words<G>(codes, words);
+  } else {
+    uint32_t turned[G];
+    to_values<G>(words, turned);
+    store_words<G>(codes, turned);
+  }
+  if (j == 0) {
+    uint32_t* to = reinterpret_cast<uint32_t*>((KEYS ? p.k_scales : p.v_scales) + row * G);
+    if constexpr (G == 4)
+      *reinterpret_cast<uint2*>(to) = make_uint2(scales[0] | scales[1] << 16, scales[2] | scales[3] << 16);
+    else
+      *to = scales[0] | scales[1] << 16;
+  }
+}
+
+template <int G, bool KEYS>
+__device__ __forceinline__ void restore(const Kv4Pages& p, Bf16* x, int64_t row, int j, int* err) {
+  if (!kda_guard(row, 1, kv4_rows(p), err)) return;
+  uint32_t words[G];
+  const uint8_t* codes = (KEYS ? p.k_codes : p.v_codes) + row * (16 * G) + 4 * G * j;
+  if constexpr (KEYS) {
+    load_words<G>(codes, words);
+  } else {
+    uint32_t turned[G];
+    load_words<G>(codes, turned);
+    from_values<G>(turned, words);
+  }
+  const uint16_t* scales = (KEYS ? p.k_scales : p.v_scales) + row * G;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float scale = bf16_to_f32(scales[g]);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = static_cast<float>(static_cast<int>(words[g] >> (4 * i) & 15u) - 8) * scale;
+    store8(x + 32 * g + 8 * j, v);
+  }
+}
+
+template <int G, bool WRITE>
+__global__ void __launch_bounds__(kThreads) span_kernel(Kv4SpanArgs a) {
+  if (a.cu && blockIdx.x == 0) check_cu_seqlens(a.cu, a.N, a.T, threadIdx.x, kThreads, a.err);
+  const int j = threadIdx.x & 3;
+  const int64_t items = a.T * a.pages.heads;
+  // (whole warps go on together: a group's maximum goes over its lanes)
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 4);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * (kThreads / 4); base < items; base += step) {
+    const int64_t item = base + (threadIdx.x >> 2);
+    const int64_t t = item / a.pages.heads;
+    const int32_t head = static_cast<int32_t>(item - t * a.pages.heads);
+    bool valid = item < items;
+    int64_t row = 0;
+    if (valid) {
+      int32_t n;
+      int64_t first, end;
+      if (a.cu) n = sequence_of(a.cu, a.N, t, a.err);
+      else n = static_cast<int32_t>(t / (a.T / a.N));
+      sequence_span(a.cu, a.N, a.T, n, first, end, a.err);
+      int32_t start = 0;
+      if (a.start && kda_guard(n, 1, a.N, a.err)) start = a.start[n];
+      valid = start >= 0 && t >= first && t < end;
+      if (valid) {
+        const int64_t slot = kv4_slot(a.pages, a.N, n, start + (t - first), a.err);
+        valid = slot >= 0;
+        if (valid) row = kv4_row(a.pages, slot, head);
+      }
+    }
+    const int64_t at_k = t * a.ld_k + static_cast<int64_t>(head) * a.pages.d;
+    const int64_t at_v = t * a.ld_v + static_cast<int64_t>(head) * a.pages.d;
+    const int64_t width = static_cast<int64_t>(a.pages.heads) * a.pages.d;
+    valid = valid && kda_guard(at_k, a.pages.d, (a.T - 1) * a.ld_k + width, a.err) &&
+            kda_guard(at_v, a.pages.d, (a.T - 1) * a.ld_v + width, a.err);
+    if constexpr (WRITE) {
+      quantise<G, true>(a.pages, a.k + at_k, valid, row, j, a.err);
+      quantise<G, false>(a.pages, a.v + at_v, valid, row, j, a.err);
+    } else if (valid) {
+      restore<G, true>(a.pages, a.k + at_k, row, j, a.err);
+      restore<G, false>(a.pages, a.v + at_v, row, j, a.err);
+    }
+  }
+}
+
+template <bool WRITE>
+cudaError_t launch(const Kv4SpanArgs& a, const char* name, cudaStream_t s) {
+  const int64_t blocks = (a.T * a.pages.heads * 4 + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(blocks, 1), 1 << 20)));
+  prof_begin(s, name);
+  if (a.pages.d == 128) span_kernel<4, WRITE><<<grid, kThreads, 0, s>>>(a);
+  else span_kernel<2, WRITE><<<grid, kThreads, 0, s>>>(a);
+  prof_end(s, name);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(const Kv4SpanArgs& a, cudaStream_t s) { return launch<true>(a, "kda_kv4_write", s); }
+cudaError_t launch_kv4_read(const Kv4SpanArgs& a, cudaStream_t s) { return launch<false>(a, "kda_kv4_read", s); }
+
+}  // namespace kda

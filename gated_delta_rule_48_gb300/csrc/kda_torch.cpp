@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <map>
@@ -32,6 +33,10 @@ struct Library {
   decltype(&kda_short_conv_step) short_conv_step;
   decltype(&kda_ssm_scan_fwd) ssm_scan_fwd;
   decltype(&kda_ssm_scan_step) ssm_scan_step;
+  decltype(&kda_attention_fwd) attention_fwd;
+  decltype(&kda_kv4_write) kv4_write;
+  decltype(&kda_kv4_read) kv4_read;
+  decltype(&kda_kv4_attention) kv4_attention;
   decltype(&kda_last_error_message) last_error_message;
 };
 std::map<std::string, Library> g_libraries;
@@ -453,6 +458,212 @@ PyObject* ssm_scan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- full attention
+// Tokens of heads: [..., heads, d], a token's values dense.
+struct Heads {
+  void* p = nullptr;
+  int64_t ld = 0, tokens = 1, heads = 0, d = 0;
+};
+Heads heads_of(const Tensor& t, const char* name, const Tensor& x) {
+  const int64_t n = t.dim();
+  if (n < 3) refuse("%s must have at least 3 dimensions, got %s", name, shape_of(t.sizes()).c_str());
+  of_type(t, at::kBFloat16, name, x);
+  Heads h;
+  h.heads = t.size(n - 2);
+  h.d = t.size(n - 1);
+  if ((h.d > 1 && t.stride(n - 1) != 1) || (h.heads > 1 && t.stride(n - 2) != h.d))
+    refuse("%s: the heads of a token must be dense", name);
+  for (int64_t k = 0; k + 2 < n; ++k) h.tokens *= t.size(k);
+  // a token's first head stands for its row
+  at::DimVector shape(t.sizes()), stride(t.strides());
+  shape.erase(shape.end() - 2);
+  stride.erase(stride.end() - 2);
+  const Rows r = rows(t.data_ptr(), shape, stride, name, h.heads * h.d);
+  h.p = r.p;
+  h.ld = r.ld;
+  return h;
+}
+const Tensor& on_gpu(const Tensor& t, const char* name) {
+  if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
+  return t;
+}
+
+float scale_of(PyObject* o, int64_t d) {
+  return o == Py_None ? 1.0f / std::sqrt(static_cast<float>(d)) : static_cast<float>(real(o));
+}
+
+// The output given or, if wanted, a new one for the sums' logarithms.
+Tensor lse_of(PyObject* given, bool want, const Tensor& q) {
+  if (!want && given == Py_None) return Tensor();
+  return output(given, q.sizes().slice(0, q.dim() - 1), at::kFloat, q, "lse");
+}
+PyObject* pair(const Tensor& a, const Tensor& b) {
+  return Py_BuildValue("(NN)", THPVariable_Wrap(a), b.defined() ? THPVariable_Wrap(b) : Py_NewRef(Py_None));
+}
+
+// q, k, v, cu_seqlens_q, cu_seqlens_k, n_seqs, causal, scale, want_lse, out, lse
+PyObject* attention_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 11, [&]() -> PyObject* {
+    const Tensor& q = on_gpu(tensor(a[0], "q"), "q");
+    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const Heads qh = heads_of(q, "q", q), kh = heads_of(k, "k", q), vh = heads_of(v, "v", q);
+    if (k.dim() != q.dim() || kh.d != qh.d)
+      refuse("k must have q's dimensions and head size, got %s", shape_of(k.sizes()).c_str());
+    same_shape(v, k.sizes(), "v");
+    const Tensor& cq = tensor(a[3], "cu_seqlens_q", true);
+    const Tensor& ck = tensor(a[4], "cu_seqlens_k", true);
+    if (ck.defined() && !cq.defined()) refuse("cu_seqlens_k is given but cu_seqlens_q is not");
+    int32_t seqs;
+    const int32_t *cqp = nullptr, *ckp = nullptr;
+    if (cq.defined()) {
+      if (cq.dim() != 1 || cq.size(0) < 1) refuse("cu_seqlens_q must be a vector of n_seqs + 1 elements");
+      seqs = narrow(cq.size(0) - 1, "n_seqs");
+      cqp = static_cast<const int32_t*>(dense(cq, cq.sizes(), at::kInt, "cu_seqlens_q", q));
+      ckp = static_cast<const int32_t*>(dense(ck, cq.sizes(), at::kInt, "cu_seqlens_k", q));
+    } else {
+      seqs = narrow(a[5] != Py_None ? integer(a[5]) : q.dim() > 3 ? q.size(0) : 1, "n_seqs");
+    }
+    const Tensor out = output(a[9], q.sizes(), at::kBFloat16, q, "out");
+    const Heads oh = heads_of(out, "out", q);
+    const Tensor lse = lse_of(a[10], a[8] == Py_True, q);
+    float* lp = static_cast<float*>(dense(lse, q.sizes().slice(0, q.dim() - 1), at::kFloat, "lse", q));
+    const Launch on(q);
+    check(g_lib->attention_fwd(qh.p, qh.ld, kh.p, kh.ld, vh.p, vh.ld, cqp, ckp, oh.p, oh.ld, lp, qh.tokens,
+                               kh.tokens, seqs, narrow(qh.heads, "heads"), narrow(kh.heads, "kv_heads"),
+                               narrow(qh.d, "d"), scale_of(a[7], qh.d), a[6] == Py_True, on.stream));
+    return pair(out, lse);
+  });
+}
+
+// (k_codes, k_scales, v_codes, v_scales) and the block table
+struct Pages {
+  kda_kv4_cache cache;
+  const int32_t* table;
+  int64_t ld, seqs;
+  int32_t width;
+
+  Pages(PyObject* o, PyObject* table_o, const Tensor& x) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4)
+      refuse("cache must be the tuple (k_codes, k_scales, v_codes, v_scales)");
+    static const char* const names[4] = {"k_codes", "k_scales", "v_codes", "v_scales"};
+    void* p[4];
+    const Tensor& codes = tensor(PyTuple_GET_ITEM(o, 0), "k_codes");
+    if (codes.dim() != 4)
+      refuse("k_codes must have the shape (pages, heads, page_size, d / 2), got %s",
+             shape_of(codes.sizes()).c_str());
+    at::DimVector shape(codes.sizes());
+    const int64_t d = 2 * shape[3];
+    for (int i = 0; i < 4; ++i) {
+      shape[3] = i % 2 ? d / 32 : d / 2;
+      p[i] = dense(tensor(PyTuple_GET_ITEM(o, i), names[i]), shape, i % 2 ? at::kBFloat16 : at::kByte,
+                   names[i], x);
+    }
+    cache = kda_kv4_cache{p[0], p[1], p[2], p[3], narrow(shape[0], "n_pages"), narrow(shape[2], "page_size"),
+                          narrow(shape[1], "kv_heads"), narrow(d, "d")};
+    const Tensor& t = tensor(table_o, "block_table");
+    if (t.dim() != 2) refuse("block_table must have 2 dimensions, got %s", shape_of(t.sizes()).c_str());
+    const Rows r = rows(t, at::kInt, "block_table", x);
+    table = static_cast<const int32_t*>(r.p);
+    ld = r.ld;
+    seqs = t.size(0);
+    width = narrow(t.size(1), "max_pages");
+  }
+};
+
+// The spans of both: start, cu_seqlens, n_seqs of tokens [T, heads, d] or [B, T_b, heads, d].
+struct Span {
+  const int32_t *start, *cu = nullptr;
+  int32_t count;
+
+  Span(PyObject* start_o, PyObject* cu_o, PyObject* n_o, const Pages& pages, const Tensor& x) {
+    const Tensor& c = tensor(cu_o, "cu_seqlens", true);
+    if (c.defined()) {
+      if (c.dim() != 1 || c.size(0) < 1) refuse("cu_seqlens must be a vector of n_seqs + 1 elements");
+      cu = static_cast<const int32_t*>(dense(c, c.sizes(), at::kInt, "cu_seqlens", x));
+      count = narrow(c.size(0) - 1, "n_seqs");
+    } else {
+      count = narrow(n_o != Py_None ? integer(n_o) : pages.seqs, "n_seqs");
+    }
+    if (pages.seqs != count)
+      refuse("block_table has %lld rows for %d sequences", (long long)pages.seqs, count);
+    const Tensor& s = tensor(start_o, "start", true);
+    start = static_cast<const int32_t*>(dense(s, {count}, at::kInt, "start", x));
+  }
+};
+
+void of_cache(const Heads& h, const Pages& p, const char* name) {
+  if (h.heads != p.cache.n_kv_heads || h.d != p.cache.d)
+    refuse("%s has %lld heads of %lld, the cache %d of %d", name, (long long)h.heads, (long long)h.d,
+           p.cache.n_kv_heads, p.cache.d);
+}
+
+// k, v, cache, block_table, start, cu_seqlens, n_seqs
+PyObject* kv4_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 7, [&]() -> PyObject* {
+    const Tensor& k = on_gpu(tensor(a[0], "k"), "k");
+    const Tensor& v = tensor(a[1], "v");
+    const Heads kh = heads_of(k, "k", k), vh = heads_of(v, "v", k);
+    same_shape(v, k.sizes(), "v");
+    const Pages p(a[2], a[3], k);
+    of_cache(kh, p, "k");
+    const Span s(a[4], a[5], a[6], p, k);
+    const Launch on(k);
+    check(g_lib->kv4_write(kh.p, kh.ld, vh.p, vh.ld, &p.cache, p.table, p.ld, p.width, s.start, s.cu,
+                           kh.tokens, s.count, on.stream));
+    Py_RETURN_NONE;
+  });
+}
+
+// cache, block_table, total_tokens, start, cu_seqlens, n_seqs, k, v
+PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 8, [&]() -> PyObject* {
+    const Tensor& table = on_gpu(tensor(a[1], "block_table"), "block_table");
+    const Pages p(a[0], a[1], table);
+    const Span s(a[3], a[4], a[5], p, table);
+    const int64_t tokens = integer(a[2]);
+    if (tokens < 0) refuse("total_tokens=%lld is negative", (long long)tokens);
+    const int64_t shape[3] = {tokens, p.cache.n_kv_heads, p.cache.d};
+    Tensor made[2];
+    Heads h[2];
+    for (int i = 0; i < 2; ++i) {
+      const char* name = i ? "v" : "k";
+      const Tensor& t = tensor(a[6 + i], name, true);
+      made[i] = t.defined() ? t : at::empty(shape, table.options().dtype(at::kBFloat16));
+      h[i] = heads_of(made[i], name, table);
+      of_cache(h[i], p, name);
+      if (h[i].tokens != tokens)
+        refuse("%s has %lld tokens, expected %lld", name, (long long)h[i].tokens, (long long)tokens);
+    }
+    const Launch on(table);
+    check(g_lib->kv4_read(h[0].p, h[0].ld, h[1].p, h[1].ld, &p.cache, p.table, p.ld, p.width, s.start, s.cu,
+                          tokens, s.count, on.stream));
+    return pair(made[0], made[1]);
+  });
+}
+
+// q, cache, block_table, seq_lens, scale, want_lse, out, lse
+PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 8, [&]() -> PyObject* {
+    const Tensor& q = on_gpu(tensor(a[0], "q"), "q");
+    const Heads qh = heads_of(q, "q", q);
+    if (q.dim() > 4) refuse("q must have 3 or 4 dimensions, got %s", shape_of(q.sizes()).c_str());
+    const Pages p(a[1], a[2], q);
+    if (qh.d != p.cache.d) refuse("q has heads of %lld, the cache of %d", (long long)qh.d, p.cache.d);
+    const int32_t seqs = narrow(q.size(0), "n_seqs");
+    if (p.seqs != seqs) refuse("block_table has %lld rows for %d sequences", (long long)p.seqs, seqs);
+    const int32_t* lens = static_cast<const int32_t*>(dense(tensor(a[3], "seq_lens"), {seqs}, at::kInt, "seq_lens", q));
+    const Tensor out = output(a[6], q.sizes(), at::kBFloat16, q, "out");
+    const Heads oh = heads_of(out, "out", q);
+    const Tensor lse = lse_of(a[7], a[5] == Py_True, q);
+    float* lp = static_cast<float*>(dense(lse, q.sizes().slice(0, q.dim() - 1), at::kFloat, "lse", q));
+    const Launch on(q);
+    check(g_lib->kv4_attention(qh.p, qh.ld, &p.cache, p.table, p.ld, p.width, lens, oh.p, oh.ld, lp, seqs,
+                               q.dim() == 4 ? narrow(q.size(1), "n_tokens") : 1, narrow(qh.heads, "heads"),
+                               scale_of(a[4], qh.d), on.stream));
+    return pair(out, lse);
+  });
+}
+
 // path, KdaError: the calls go to the library at that path from now on.
 PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -477,6 +688,8 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!find(l.add_rms_norm, "kda_add_rms_norm") || !find(l.matmul_fp8, "kda_matmul_fp8") ||
         !find(l.short_conv_fwd, "kda_short_conv_fwd") || !find(l.short_conv_step, "kda_short_conv_step") ||
         !find(l.ssm_scan_fwd, "kda_ssm_scan_fwd") || !find(l.ssm_scan_step, "kda_ssm_scan_step") ||
+        !find(l.attention_fwd, "kda_attention_fwd") || !find(l.kv4_write, "kda_kv4_write") ||
+        !find(l.kv4_read, "kda_kv4_read") || !find(l.kv4_attention, "kda_kv4_attention") ||
         !find(l.last_error_message, "kda_last_error_message")) {
       PyErr_Format(PyExc_OSError, "%s lacks an entry point", path);
       return nullptr;
@@ -492,7 +705,9 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {KDA_METHOD(select),         KDA_METHOD(add_rms_norm),
                            KDA_METHOD(matmul_fp8),     KDA_METHOD(short_conv_fwd),
                            KDA_METHOD(short_conv_step), KDA_METHOD(ssm_scan_fwd),
-                           KDA_METHOD(ssm_scan_step),  {nullptr, nullptr, 0, nullptr}};
+                           KDA_METHOD(ssm_scan_step),  KDA_METHOD(attention_fwd),
+                           KDA_METHOD(kv4_write),      KDA_METHOD(kv4_read),
+                           KDA_METHOD(kv4_attention),  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "kda_torch", nullptr, -1, g_methods};
 
 }  // namespace

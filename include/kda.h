@@ -59,7 +59,7 @@ typedef enum {
     KDA_ERR_UNSUPPORTED = 2,      /* valid but not implemented (e.g. dk = 96)     */
     KDA_ERR_CUDA = 3,             /* a CUDA runtime call or launch failed         */
     KDA_ERR_OUT_OF_MEMORY = 4,    /* the stream-ordered workspace allocation failed */
-    KDA_ERR_DEVICE_INPUT = 5      /* the GPU rejected an input (bad cu_seqlens)   */
+    KDA_ERR_DEVICE_INPUT = 5      /* the GPU rejected an input (bad cu_seqlens, page) */
 } kda_status;
 
 /*
@@ -588,6 +588,139 @@ kda_status kda_ssm_scan_step(const void *x, int64_t ld_x, const void *dt,
                              int32_t state, int32_t groups,
                              int32_t dt_softplus, kda_dtype dtype,
                              void *stream);
+
+/*
+ * Full attention and its cache.
+ *
+ * A model of recurrent layers has a full-attention layer after every few of
+ * them (the lecture and the orkas.ai close read: three recurrent layers to
+ * one global layer without positions).  The calls below are that layer's
+ * attention over prompts, a paged cache that holds its keys and values in
+ * 4 bits, and the attention of new tokens over that cache.  They follow the
+ * conventions of the operators above (rows at any distance, a pointer of any
+ * alignment of its element unless stated).  A token's heads are dense; `ld_*`
+ * is the distance between tokens.
+ *
+ * kda_attention_fwd -- attention over prompts.
+ *
+ *     out[i] = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j)
+ *
+ * over the keys j of query i's sequence, with `causal` those at or before it,
+ * where the queries are the last ones of their sequence (query i of Lq reaches
+ * keys 0 .. i + Lk - Lq).  Query head h reads key and value head
+ * h / (n_heads / n_kv_heads).  A query that reaches no key gets zeros, and an
+ * lse of -infinity.  Keys and values a query does not reach have no influence,
+ * whatever they hold.  Scores, maxima and sums are in 32 bits; p is rounded to
+ * bf16 for the product with v (off by at most 2^-8 of each term), out is
+ * rounded once.
+ *
+ * Tensors:
+ *   q    bf16 [total_q, n_heads, d]      read   } every token's first value on
+ *   k    bf16 [total_k, n_kv_heads, d]   read   } a 16-byte boundary
+ *   v    bf16 [total_k, n_kv_heads, d]   read   }
+ *   out  bf16 [total_q, n_heads, d]      written }
+ *   lse  f32  [total_q, n_heads], dense  written; NULL = not produced:
+ *                                        log sum_j p_ij
+ *   cu_seqlens_q, cu_seqlens_k  i32 [N + 1] as in kda_chunk_fwd (checked on the
+ *        GPU: a malformed array is reported by kda_get_device_error, and out
+ *        and lse are then unspecified).  cu_seqlens_k NULL = cu_seqlens_q; both
+ *        NULL = n_seqs sequences of total_q / n_seqs queries and
+ *        total_k / n_seqs keys.
+ * d is 64 or 128, else KDA_ERR_UNSUPPORTED.  n_heads is a multiple of
+ * n_kv_heads.  scale is positive and finite.  total_q = 0 is a no-op.
+ * Allocates nothing.
+ */
+kda_status kda_attention_fwd(const void *q, int64_t ld_q, const void *k,
+                             int64_t ld_k, const void *v, int64_t ld_v,
+                             const int32_t *cu_seqlens_q,
+                             const int32_t *cu_seqlens_k, void *out,
+                             int64_t ld_out, float *lse, int64_t total_q,
+                             int64_t total_k, int32_t n_seqs, int32_t n_heads,
+                             int32_t n_kv_heads, int32_t d, float scale,
+                             int32_t causal, void *stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  A page holds page_size
+ * positions of one sequence; column i of row n of the block table names the
+ * page of positions i * page_size .. (i + 1) * page_size - 1 of sequence n.
+ *
+ * 32 channels of a token and head share a scale:
+ *     s = bf16(max(max |x|, 2^-64) / 7),   n = x / s rounded half to even
+ * and are stored as codes n + 8 (n in [-7, 7]); they stand for n * s.  A group
+ * that holds a NaN or an infinity stands for NaN in all its channels.
+ *
+ *   k_codes, v_codes    u8   [n_pages, n_kv_heads, page_size, d / 2]
+ *   k_scales, v_scales  bf16 [n_pages, n_kv_heads, page_size, d / 32]
+ * dense and 16-byte aligned.  With G = d / 32 groups, nibble i (from the low
+ * end) of 32-bit word j G + g of a row of k_codes is the code of channel
+ * 32 g + 8 j + i, and nibble i of 16-bit word r G + g of a row of v_codes that
+ * of channel 32 g + 4 r + i.
+ * page_size is a power of two from 16 to 65536, d is 64 or 128.
+ */
+typedef struct {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int32_t n_pages, page_size, n_kv_heads, d;
+} kda_kv4_cache;
+
+/*
+ * kda_kv4_write -- quantise tokens into the cache; kda_kv4_read -- read
+ * positions back, rounded to bf16.
+ *
+ * Token i of sequence n is position start[n] + i.
+ *   k, v         bf16 [T, n_kv_heads, d], every token's first value on a 16-byte
+ *                boundary; read by the write, written by the read
+ *   block_table  i32 [N, max_pages], rows ld_table apart   read
+ *   start        i32 [N]   read; NULL = zeros.  A sequence whose start is
+ *                negative is left out: its tokens are not written (the read
+ *                leaves its rows as they are).
+ *   cu_seqlens   i32 [N + 1] as in kda_chunk_fwd (checked on the GPU; of a
+ *                malformed array or start it is unspecified which valid
+ *                positions are read or written), or NULL
+ * A position whose page is not in [0, n_pages) or whose column is not below
+ * max_pages is reported by kda_get_device_error; it is not written, or its row
+ * is left as it is.  Two tokens of one write must not have the same page and
+ * place: what such a place then holds is unspecified.
+ * T = 0 or N = 0 are valid.  Allocates nothing.
+ */
+kda_status kda_kv4_write(const void *k, int64_t ld_k, const void *v,
+                         int64_t ld_v, const kda_kv4_cache *cache,
+                         const int32_t *block_table, int64_t ld_table,
+                         int32_t max_pages, const int32_t *start,
+                         const int32_t *cu_seqlens, int64_t total_tokens,
+                         int32_t n_seqs, void *stream);
+kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
+                        const kda_kv4_cache *cache, const int32_t *block_table,
+                        int64_t ld_table, int32_t max_pages,
+                        const int32_t *start, const int32_t *cu_seqlens,
+                        int64_t total_tokens, int32_t n_seqs, void *stream);
+
+/*
+ * kda_kv4_attention -- attention of the last n_tokens positions of each
+ * sequence over the cache (n_tokens = 1: a decoding step; more: a draft).
+ *
+ * As kda_attention_fwd, causal, with the keys and values n * s of the cache's
+ * first seq_lens[n] positions, the queries' own among them (written before):
+ * query i of a sequence reaches positions 0 .. seq_lens[n] - n_tokens + i, and
+ * none (zeros, an lse of -infinity) where that is negative.  Scores are sums
+ * over whole numbers n in 32 bits, scaled per group; p * s of a value's group
+ * is rounded to bf16 for the product with its n; out is rounded once.
+ *
+ *   q         bf16 [N, n_tokens, n_heads, d], tokens ld_q apart      read
+ *   seq_lens  i32 [N]                                                read
+ *   out       bf16 [N, n_tokens, n_heads, d], tokens ld_out apart    written
+ *   lse       f32 [N, n_tokens, n_heads], dense   written; NULL = not produced
+ * q and out start on a 16-byte boundary at every token.  A position without a
+ * valid page (as in kda_kv4_write) is reported by kda_get_device_error, and its
+ * sequence's rows are then unspecified.  n_heads is a multiple of the cache's
+ * n_kv_heads.  scale is positive and finite.  N = 0 or n_tokens = 0 are no-ops.
+ */
+kda_status kda_kv4_attention(const void *q, int64_t ld_q,
+                             const kda_kv4_cache *cache,
+                             const int32_t *block_table, int64_t ld_table,
+                             int32_t max_pages, const int32_t *seq_lens,
+                             void *out, int64_t ld_out, float *lse,
+                             int32_t n_seqs, int32_t n_tokens, int32_t n_heads,
+                             float scale, void *stream);
 
 /*
  * kda_get_device_error -- synchronise `stream`, then return and clear the
