@@ -74,7 +74,8 @@ struct Kv4AttentionArgs {
   int sm_count;
   int* err;
 };
-cudaError_t launch_kv4_attention(const Kv4AttentionArgs& a, cudaStream_t s);
+// Allocates its workspace: a status of its own if that fails, else `e`.
+kda_status launch_kv4_attention(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e);
 
 // ---- device helpers
 // The slot (page * page_size + place) of a position >= 0 of sequence n, or -1

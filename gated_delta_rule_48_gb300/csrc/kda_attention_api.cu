@@ -268,5 +268,7 @@ extern "C" kda_status kda_kv4_attention(const void* q, int64_t ld_q, const kda_k
   a.scale = scale;
   KDA_TRY(device_sm_count(&a.sm_count));
   KDA_TRY(device_error_word(&a.err));
-  return launched(launch_kv4_attention(a, static_cast<cudaStream_t>(stream)), "cache attention launch");
+  cudaError_t e = cudaSuccess;
+  KDA_TRY(launch_kv4_attention(a, static_cast<cudaStream_t>(stream), e));
+  return launched(e, "cache attention launch");
 }

@@ -1,92 +1,576 @@
 // A few query tokens of each sequence over the cache in 4 bits.
 //
-// One warp takes a query and head: a key per lane, 32 at a time, with the
-// running maximum and sum, and the values with a few channels per lane.
+//   x = c sum_g s_tg sum_{c in g} q_c n_tc,   p = 2^(x - m),   o_c = sum_t p_t s'_tg n'_tc / sum_t p_t
+//
+// with c = scale log2 e, a key's scales s and codes n, a value's s' and n', per
+// group g of 32 channels.
+//
+// Bound: the cache's bytes (1.125 per channel of a token and head), and close to
+// them the instructions that take codes apart.  A step is a token or a few, so
+// that there are 1 to 16 query rows (tokens x heads of a group) for each key: too
+// few for tensor memory's 128 lanes, and codes would have to go through shared
+// memory as bf16 first.  So the products are warp-wide ones (m16n8k16) with the
+// cache as the 16-row operand, straight from the registers it was unpacked into:
+// S^T = K Q^T (16 tokens x 8 query rows), O^T += V^T P^T (16 channels x 8 query
+// rows).
+//   - A code is a bf16 value by an AND and an OR: bits 3..6 of 0x4180 hold n + 8
+//     as 16 + (n + 8) = 24 + n.  For keys the 24 goes away with the accumulator's
+//     first value, -24 sum_{c in g} q_c; for values it is subtracted (exactly).
+//   - Scales never touch the codes: a group's part of a score is scaled in 32
+//     bits, and a value's scale is multiplied into p, which is rounded to bf16
+//     then (as in kda_attention_fwd; the rounding of p itself is left out).
+//   - The order of codes in a row is that in which a lane needs them: 16 bytes of
+//     a key, 8 of a value, each with channels of all groups.
+//
+// Work: the slices of 16 positions of all (sequence, key head, 16 query rows)
+// form one line that is cut into equal parts, one per block, whatever the
+// sequences' lengths.  A block goes through its part unit by unit, its warps a
+// slice each in turn, with copies a few slices ahead; units that lie in one block
+// are written out, the parts of others combined by a second launch.
 #include <cmath>
 
+#include <algorithm>
+
 #include "kda_attention.h"
+#include "kda_sm100.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kWarps = 4;
+using sm100::smem_u32;
 
-template <int G>
-__global__ void __launch_bounds__(32 * kWarps) kv4_attention_kernel(Kv4AttentionArgs a) {
-  constexpr int D = 32 * G;
-  __shared__ float s_q[kWarps][D];
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSlice = 16;        // positions of a slice
+constexpr int kDepth = 4;         // slices of a warp in flight
+constexpr float kLowest = -1e30f; // a maximum of nothing
+constexpr float kSlack = 8.0f;    // log2 of how far p may pass 1
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Where a block's part of a unit lies that is not whole.
+struct Meta {
+  int32_t last;       // the last block that has a part (-1: nothing to combine)
+  int32_t slot;       // of the first block's part
+  int32_t seq, head, col0;
+  int32_t pad[3];
+};
+
+template <int G, int NT>
+struct Shape {
+  static constexpr int D = 32 * G, kCols = 8 * NT;
+  static constexpr int kRow = 16 * G;                           // bytes of a row of codes
+  static constexpr int kPitchV = kRow + 16;                     // so that a warp's reads meet no bank twice
+  static constexpr int kScaleBytes = kSlice * 2 * G;            // of keys, of values
+  static constexpr int kStage = kSlice * (kRow + kPitchV) + 2 * kScaleBytes;
+  static constexpr int kRing = kWarps * kDepth * kStage;
+  static constexpr int kParts = kWarps * kCols * (D + 4) * 4;   // the warps' results, over the ring
+  static constexpr int kSmem = kRing > kParts ? kRing : kParts;
+  static constexpr int kRecord = kCols * (D + 2);               // floats of a part: o, then m and l
+};
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8 x 8 values of 16 bits, turned.
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// Nibbles i of both halves as bf16: 24 + n.
+template <int I>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+  const uint32_t at = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return (at & 0x00780078u) | 0x41804180u;
+}
+// The same less 24.
+template <int I>
+__device__ __forceinline__ uint32_t whole_numbers(uint32_t w) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(nibbles<I>(w)), "r"(0xc1c0c1c0u));
+  return r;
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ float half_of(uint32_t pair, int i) {
+  return __uint_as_float(i ? pair & 0xffff0000u : pair << 16);
+}
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
+  using S = Shape<G, NT>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int64_t s_start[3];  // sequence, slices before it, all slices
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, j = lane & 3;
   const Kv4Pages& p = a.pages;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t rows = static_cast<int64_t>(a.N) * a.tokens;
-  if (item >= rows * a.heads) return;
-  const int64_t t = item / a.heads;
-  const int32_t head = static_cast<int32_t>(item - t * a.heads), n = static_cast<int32_t>(t / a.tokens);
-  const int32_t kv = head / (a.heads / p.heads);
-  const int64_t reach = max(0, a.seq_lens[n] - a.tokens + 1 + static_cast<int32_t>(t % a.tokens));
-  for (int c = lane; c < D; c += 32)
-    s_q[warp][c] = to_f32(a.q[t * a.ld_q + head * D + c]) * (a.scale * kLog2e);
-  __syncwarp();
-  float top = -INFINITY, sum = 0.0f, o[G] = {};
-  for (int64_t j0 = 0; j0 < reach; j0 += 32) {
-    const int64_t j = j0 + lane;
-    float x = -INFINITY;
-    int64_t row = -1;
-    if (j < reach) {
-      const int64_t slot = kv4_slot(p, a.N, n, j, a.err);
-      if (slot >= 0) row = kv4_row(p, slot, kv);
+  const int group = a.heads / p.heads, cols = a.tokens * group;
+  const int blocks_c = (cols + S::kCols - 1) / S::kCols;
+  const int64_t per_seq = static_cast<int64_t>(p.heads) * blocks_c;  // units of a sequence
+  const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
+  auto len_of = [&](int64_t n) -> int64_t {
+    return kda_guard(n, 1, a.N, a.err) ? max(a.seq_lens[n], 0) : 0;
+  };
+  auto slices_of = [&](int64_t n) { return (len_of(n) + kSlice - 1) / kSlice; };
+
+  // ---- sequences of no positions: zeros
+  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+    if (len_of(n) > 0) continue;
+    for (int e = threadIdx.x; e < a.tokens * a.heads * (S::D / 8); e += kThreads) {
+      const int64_t at = (n * a.tokens + e / (a.heads * (S::D / 8))) * a.ld_out + e % (a.heads * (S::D / 8)) * 8;
+      if (kda_guard(at, 8, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
+        *reinterpret_cast<uint4*>(a.out + at) = make_uint4(0, 0, 0, 0);
     }
-    if (row >= 0) {
-      x = 0.0f;
-      for (int w = 0; w < 4 * G; ++w) {
-        const int g = w % G, part = w / G;
-        const uint32_t codes = reinterpret_cast<const uint32_t*>(p.k_codes + row * (16 * G))[w];
-        float y = 0.0f;
-        for (int i = 0; i < 8; ++i)
-          y = fmaf(static_cast<float>(static_cast<int>(codes >> (4 * i) & 15u) - 8),
-                   s_q[warp][32 * g + 8 * part + i], y);
-        x = fmaf(y, bf16_to_f32(p.k_scales[row * G + g]), x);
-      }
-    }
-    float next = max_nan(top, x);
-#pragma unroll
-    for (int w = 16; w; w /= 2) next = max_nan(next, __shfl_xor_sync(0xffffffffu, next, w));
-    const float base = next == -INFINITY ? 0.0f : next, keep = ex2(top - base), e = ex2(x - base);
-    top = next;
-    sum = sum * keep + e;
-#pragma unroll
-    for (int i = 0; i < G; ++i) o[i] *= keep;
-    for (int i = 0; i < 32; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, e, i);
-      const int64_t r = __shfl_sync(0xffffffffu, row, i);
-      if (r < 0) continue;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {  // channel 32 g + lane
-        const uint16_t h = reinterpret_cast<const uint16_t*>(p.v_codes + r * (16 * G))[(lane / 4) * G + g];
-        const float v = static_cast<float>(static_cast<int>(h >> (4 * (lane % 4)) & 15) - 8);
-        o[g] = fmaf(pi, v * bf16_to_f32(p.v_scales[r * G + g]), o[g]);
-      }
-    }
+    if (a.lse)
+      for (int e = threadIdx.x; e < a.tokens * a.heads; e += kThreads)
+        if (kda_guard(n * a.tokens * a.heads + e, 1, n_rows * a.heads, a.err))
+          a.lse[n * a.tokens * a.heads + e] = -INFINITY;
   }
+
+  // ---- this block's part of the line
+  const int64_t chunk = (a.N + kThreads - 1) / kThreads;
+  const int64_t c0 = min(chunk * threadIdx.x, static_cast<int64_t>(a.N)), c1 = min(c0 + chunk, static_cast<int64_t>(a.N));
+  int64_t own = 0;
+  for (int64_t n = c0; n < c1; ++n) own += slices_of(n);
+  int64_t scan = own;
 #pragma unroll
-  for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  const float r = reach > 0 ? 1.0f / sum : 0.0f;
-  Bf16* out = a.out + t * a.ld_out + head * D;
+  for (int w = 1; w < 32; w *= 2) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, scan, w);
+    if (lane >= w) scan += up;
+  }
+  if (lane == 31) s_sum[warp] = scan;
+  __syncthreads();
+  int64_t before = scan - own, total = 0;
 #pragma unroll
-  for (int g = 0; g < G; ++g) out[32 * g + lane] = from_f32<Bf16>(o[g] * r);
-  if (a.lse && lane == 0) a.lse[item] = reach > 0 ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t all = total * per_seq;
+  // no more blocks than have two slices for each warp
+  const int64_t used = max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), all / (2 * kWarps)));
+  const int64_t b = blockIdx.x;
+  const int64_t part0 = b < used ? all * b / used : all, part1 = b < used ? all * (b + 1) / used : all;
+  if (threadIdx.x == 0) {
+    Meta none;
+    none.last = -1;
+    metas[b] = none;
+  }
+  if (part0 >= part1) return;
+  if (part0 >= before * per_seq && part0 < (before + own) * per_seq) {
+    int64_t n = c0, at = before, count = slices_of(n);
+    while ((at + count) * per_seq <= part0) {
+      at += count;
+      count = slices_of(++n);
+    }
+    s_start[0] = n;
+    s_start[1] = at;
+  }
+  __syncthreads();
+  int64_t seq = s_start[0], seq_first = s_start[1] * per_seq;  // the sequence's first slice of the line
+
+  unsigned char* const ring = smem + warp * (kDepth * S::kStage);
+  const float c = a.scale * kLog2e;
+  for (int64_t at = part0; at < part1;) {
+    int64_t slices = slices_of(seq);
+    while (at >= seq_first + slices * per_seq) {
+      seq_first += slices * per_seq;
+      slices = slices_of(++seq);
+    }
+    const int64_t unit = (at - seq_first) / slices;  // of the sequence
+    const int64_t unit_first = seq_first + unit * slices;
+    const int32_t head = static_cast<int32_t>(unit / blocks_c), col0 = static_cast<int32_t>(unit % blocks_c) * S::kCols;
+    const int64_t first = at - unit_first, last = min(part1 - unit_first, slices);  // slices [first, last)
+    const int64_t len = len_of(seq);
+    const int64_t visible = len - a.tokens + 1;  // positions the first query reaches
+
+    // ---- queries: fragments of Q^T, and -24 times the groups' sums
+    uint32_t q[G][2][NT][2];
+    float offset[G][NT][2];
+    int32_t reach[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int col = col0 + 8 * t + r;
+      const int64_t row = seq * a.tokens + col / group;
+      const int64_t from = row * a.ld_q + static_cast<int64_t>(head * group + col % group) * S::D;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (col < cols && kda_guard(from + 32 * g + 8 * j, 8, (n_rows - 1) * a.ld_q + a.heads * S::D, a.err))
+          w = *reinterpret_cast<const uint4*>(a.q + from + 32 * g + 8 * j);
+        // channels 8 j + (0, 4), (1, 5), (2, 6), (3, 7), as the keys' nibbles come
+        q[g][0][t][0] = __byte_perm(w.x, w.z, 0x5410);
+        q[g][0][t][1] = __byte_perm(w.x, w.z, 0x7632);
+        q[g][1][t][0] = __byte_perm(w.y, w.w, 0x5410);
+        q[g][1][t][1] = __byte_perm(w.y, w.w, 0x7632);
+        float sum = ((half_of(w.x, 0) + half_of(w.x, 1)) + (half_of(w.y, 0) + half_of(w.y, 1))) +
+                    ((half_of(w.z, 0) + half_of(w.z, 1)) + (half_of(w.w, 0) + half_of(w.w, 1)));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= -24.0f;
+        offset[g][t][0] = __shfl_sync(0xffffffffu, sum, 8 * j);
+        offset[g][t][1] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)  // of this lane's columns 2 j + e
+        reach[t][e] = static_cast<int32_t>(visible + (col0 + 8 * t + 2 * j + e) / group);
+    }
+    float o[2 * G][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int g = 0; g < 2 * G; ++g) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.0f;
+      m[t][0] = m[t][1] = kLowest;
+      l[t][0] = l[t][1] = 0.0f;
+    }
+
+    // ---- this warp's slices: first + warp, + 4, ...
+    const int64_t mine = max(int64_t{0}, (last - first - warp + kWarps - 1) / kWarps);
+    auto page_of = [&](int64_t i) -> int32_t {  // of slice number i of the warp
+      if (i >= mine) return 0;
+      const int64_t col = ((first + warp + i * kWarps) * kSlice) >> p.page_shift, e = seq * p.ld_table + col;
+      int32_t page = -1;
+      if (col < p.width && kda_guard(e, 1, (a.N - 1) * p.ld_table + p.width, a.err)) page = p.table[e];
+      return page;
+    };
+    auto fetch = [&](int64_t i, int32_t page) {
+      if (i < mine) {
+        if (page < 0 || page >= p.n_pages) {
+          if (lane == 0) atomicOr(a.err, kDevErrPage);
+          page = 0;
+        }
+        const int64_t pos = (first + warp + i * kWarps) * kSlice;
+        const int64_t row = kv4_row(p, (static_cast<int64_t>(page) << p.page_shift) + (pos & ((1 << p.page_shift) - 1)), head);
+        const uint32_t to = smem_u32(ring + (i % kDepth) * S::kStage);
+        if (p.n_pages > 0 && kda_guard(row, kSlice, kv4_rows(p), a.err)) {
+          constexpr int kChunks = S::kRow / 16;  // of a row
+#pragma unroll
+          for (int e = 0; e < kSlice * kChunks; e += 32) {
+            const int k = e + lane;
+            copy16(to + 16 * k, p.k_codes + row * S::kRow + 16 * k);
+            copy16(to + kSlice * S::kRow + k / kChunks * S::kPitchV + k % kChunks * 16, p.v_codes + row * S::kRow + 16 * k);
+          }
+          constexpr int kS = S::kScaleBytes / 16;
+          if (lane < 2 * kS) {
+            const unsigned char* from = reinterpret_cast<const unsigned char*>(lane < kS ? p.k_scales : p.v_scales) +
+                                        row * (2 * G) + 16 * (lane % kS);
+            copy16(to + kSlice * (S::kRow + S::kPitchV) + 16 * lane, from);
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i, page_of(i));
+    int32_t next_page = page_of(kDepth - 1);
+    for (int64_t i = 0; i < mine; ++i) {
+      fetch(i + kDepth - 1, next_page);
+      next_page = page_of(i + kDepth);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+      __syncwarp();
+      const unsigned char* stage = ring + (i % kDepth) * S::kStage;
+      const int64_t pos = (first + warp + i * kWarps) * kSlice;
+
+      // ---- scores of positions r and r + 8
+      float x[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
+      {
+        uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
+        const unsigned char* from = stage + r * S::kRow + 4 * G * j;
+        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * r;
+        if constexpr (G == 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(from), v = *reinterpret_cast<const uint4*>(from + 8 * S::kRow);
+          k0[0] = u.x; k0[1] = u.y; k0[2] = u.z; k0[3] = u.w;
+          k1[0] = v.x; k1[1] = v.y; k1[2] = v.z; k1[3] = v.w;
+          const uint2 f = *reinterpret_cast<const uint2*>(scales), h = *reinterpret_cast<const uint2*>(scales + 16 * G);
+          s0[0] = f.x; s0[1] = f.y; s1[0] = h.x; s1[1] = h.y;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(from), v = *reinterpret_cast<const uint2*>(from + 8 * S::kRow);
+          k0[0] = u.x; k0[1] = u.y; k1[0] = v.x; k1[1] = v.y;
+          s0[0] = *reinterpret_cast<const uint32_t*>(scales);
+          s1[0] = *reinterpret_cast<const uint32_t*>(scales + 16 * G);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint32_t f0[4] = {nibbles<0>(k0[g]), nibbles<0>(k1[g]), nibbles<1>(k0[g]), nibbles<1>(k1[g])};
+          const uint32_t f1[4] = {nibbles<2>(k0[g]), nibbles<2>(k1[g]), nibbles<3>(k0[g]), nibbles<3>(k1[g])};
+          const float lo = half_of(s0[g / 2], g % 2), hi = half_of(s1[g / 2], g % 2);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float d[4] = {offset[g][t][0], offset[g][t][1], offset[g][t][0], offset[g][t][1]};
+            mma(d, f0, q[g][0][t][0], q[g][0][t][1]);
+            mma(d, f1, q[g][1][t][0], q[g][1][t][1]);
+            x[t][0] = fmaf(d[0], lo, x[t][0]);
+            x[t][1] = fmaf(d[1], lo, x[t][1]);
+            x[t][2] = fmaf(d[2], hi, x[t][2]);
+            x[t][3] = fmaf(d[3], hi, x[t][3]);
+          }
+        }
+      }
+      // ---- softmax
+      const bool masked = pos + kSlice > visible;
+      bool up = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[t][e] *= c;
+          if (masked && pos + r + (e >> 1) * 8 >= reach[t][e & 1]) x[t][e] = -INFINITY;
+          up = up || x[t][e] > m[t][e & 1] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(m[t][e], fmaxf(x[t][e], x[t][e + 2]));
+#pragma unroll
+            for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float keep = ex2(m[t][e] - top);
+            m[t][e] = top;
+            l[t][e] *= keep;
+#pragma unroll
+            for (int g = 0; g < 2 * G; ++g) {
+              o[g][t][e] *= keep;
+              o[g][t][e + 2] *= keep;
+            }
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[t][e] = ex2(x[t][e] - m[t][e & 1]);
+          l[t][e & 1] += x[t][e];
+        }
+      // ---- values
+      {
+        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + S::kScaleBytes + 2 * G * r;
+        const unsigned char* from = stage + kSlice * S::kRow + 2 * j * S::kPitchV + 2 * G * r;
+        uint32_t s0[G / 2], s1[G / 2], w[4][G / 2];
+        if constexpr (G == 4) {
+          const uint2 f = *reinterpret_cast<const uint2*>(scales), h = *reinterpret_cast<const uint2*>(scales + 16 * G);
+          s0[0] = f.x; s0[1] = f.y; s1[0] = h.x; s1[1] = h.y;
+        } else {
+          s0[0] = *reinterpret_cast<const uint32_t*>(scales);
+          s1[0] = *reinterpret_cast<const uint32_t*>(scales + 16 * G);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // positions 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+          const unsigned char* at_k = from + (k / 2 * 8 + k % 2) * S::kPitchV;
+          if constexpr (G == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(at_k);
+            w[k][0] = u.x; w[k][1] = u.y;
+          } else {
+            w[k][0] = *reinterpret_cast<const uint32_t*>(at_k);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float lo = half_of(s0[g / 2], g % 2), hi = half_of(s1[g / 2], g % 2);
+          uint32_t b0[NT], b1[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float f[4] = {x[t][0] * lo, x[t][1] * lo, x[t][2] * hi, x[t][3] * hi};
+            if (masked) {  // (what is not reached may have any scale)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (pos + r + (e >> 1) * 8 >= reach[t][e & 1]) f[e] = 0.0f;
+            }
+            b0[t] = turned(pack2_bf16(f[0], f[1]));
+            b1[t] = turned(pack2_bf16(f[2], f[3]));
+          }
+          // channels 4 r + i of the group, positions in pairs
+          const uint32_t sel = g % 2 ? 0x7632 : 0x5410;
+          const uint32_t y0 = __byte_perm(w[0][g / 2], w[1][g / 2], sel), y1 = __byte_perm(w[2][g / 2], w[3][g / 2], sel);
+          const uint32_t f0[4] = {whole_numbers<0>(y0), whole_numbers<1>(y0), whole_numbers<0>(y1), whole_numbers<1>(y1)};
+          const uint32_t f1[4] = {whole_numbers<2>(y0), whole_numbers<3>(y0), whole_numbers<2>(y1), whole_numbers<3>(y1)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma(o[2 * g][t], f0, b0[t], b1[t]);
+            mma(o[2 * g + 1][t], f1, b0[t], b1[t]);
+          }
+        }
+      }
+      __syncwarp();  // the stage is free
+    }
+
+    // ---- the warps' results together
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* const parts = reinterpret_cast<float*>(smem);  // [warp][column][D + 4]: o, m, l
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w < 32; w *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
+        float* to = parts + (warp * S::kCols + 8 * t + 2 * j + e) * (S::D + 4);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {  // channels 32 g + 4 r + 0..3
+          *reinterpret_cast<float4*>(to + 32 * g + 4 * r) =
+              make_float4(o[2 * g][t][e], o[2 * g][t][e + 2], o[2 * g + 1][t][e], o[2 * g + 1][t][e + 2]);
+        }
+        if (r == 0) {
+          to[S::D] = m[t][e];
+          to[S::D + 1] = l[t][e];
+        }
+      }
+    __syncthreads();
+    const bool complete = first == 0 && last == slices;
+    const int slot = at == part0 ? 0 : 1;
+    float* const record = records + (b * 2 + slot) * S::kRecord;
+    for (int e = threadIdx.x; e < S::kCols * (S::D / 4); e += kThreads) {
+      const int col = e / (S::D / 4), ch = e % (S::D / 4) * 4;
+      float top = kLowest, sum = 0.0f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[(w * S::kCols + col) * (S::D + 4) + S::D]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* from = parts + (w * S::kCols + col) * (S::D + 4);
+        const float keep = ex2(from[S::D] - top);
+        const float4 x = *reinterpret_cast<const float4*>(from + ch);
+        sum = fmaf(from[S::D + 1], keep, sum);
+        v.x = fmaf(x.x, keep, v.x);
+        v.y = fmaf(x.y, keep, v.y);
+        v.z = fmaf(x.z, keep, v.z);
+        v.w = fmaf(x.w, keep, v.w);
+      }
+      if (complete) {
+        const int g_col = col0 + col;
+        if (g_col < cols) {
+          const bool any = visible + g_col / group > 0;
+          const float scale = any ? 1.0f / sum : 0.0f;
+          const int64_t row = seq * a.tokens + g_col / group;
+          const int32_t h = head * group + g_col % group;
+          const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
+          if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
+            *reinterpret_cast<uint2*>(a.out + to) =
+                any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale))
+                    : make_uint2(0, 0);
+          if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
+            a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+        }
+      } else {
+        *reinterpret_cast<float4*>(record + col * S::D + ch) = v;
+        if (ch == 0) {
+          record[S::kCols * S::D + 2 * col] = top;
+          record[S::kCols * S::D + 2 * col + 1] = sum;
+        }
+      }
+    }
+    if (!complete && first == 0 && threadIdx.x == 0) {  // this block has the unit's first part
+      Meta mt;
+      mt.last = static_cast<int32_t>(((unit_first + slices) * used - 1) / all);
+      mt.slot = slot;
+      mt.seq = static_cast<int32_t>(seq);
+      mt.head = head;
+      mt.col0 = col0;
+      metas[b] = mt;
+    }
+    __syncthreads();  // the ring is filled again
+    at = unit_first + last;
+  }
+}
+
+// The parts of a unit that several blocks worked on: block (b, column).
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads) combine_kernel(Kv4AttentionArgs a, const float* records, const Meta* metas) {
+  using S = Shape<G, NT>;
+  __shared__ float4 s_v[kThreads];
+  __shared__ float s_m[kThreads], s_l[kThreads];
+  constexpr int kLanes = S::D / 4, kSets = kThreads / kLanes;  // channels in fours; sets of parts
+  const Meta mt = metas[blockIdx.x];
+  if (mt.last < 0) return;
+  const int group = a.heads / a.pages.heads, cols = a.tokens * group;
+  const int col = blockIdx.y, g_col = mt.col0 + col;
+  if (g_col >= cols) return;
+  const int ch = threadIdx.x % kLanes * 4, set = threadIdx.x / kLanes;
+  const int64_t b0 = blockIdx.x;
+  float top = kLowest, sum = 0.0f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m2, float l2, const float4& x) {
+    const float next = fmaxf(top, m2), k0 = ex2(top - next), k1 = ex2(m2 - next);
+    top = next;
+    sum = fmaf(l2, k1, sum * k0);
+    v.x = fmaf(x.x, k1, v.x * k0);
+    v.y = fmaf(x.y, k1, v.y * k0);
+    v.z = fmaf(x.z, k1, v.z * k0);
+    v.w = fmaf(x.w, k1, v.w * k0);
+  };
+#pragma unroll 4
+  for (int64_t b = b0 + set; b <= mt.last; b += kSets) {
+    const float* record = records + (b * 2 + (b == b0 ? mt.slot : 0)) * S::kRecord;
+    add(record[S::kCols * S::D + 2 * col], record[S::kCols * S::D + 2 * col + 1],
+        *reinterpret_cast<const float4*>(record + col * S::D + ch));
+  }
+  s_v[threadIdx.x] = v;
+  s_m[threadIdx.x] = top;
+  s_l[threadIdx.x] = sum;
+  __syncthreads();
+  if (set != 0) return;
+  for (int i = 1; i < kSets; ++i) add(s_m[i * kLanes + threadIdx.x], s_l[i * kLanes + threadIdx.x], s_v[i * kLanes + threadIdx.x]);
+  const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
+  const int64_t row = static_cast<int64_t>(mt.seq) * a.tokens + g_col / group;
+  const int32_t h = mt.head * group + g_col % group;
+  const int64_t len = kda_guard(mt.seq, 1, a.N, a.err) ? a.seq_lens[mt.seq] : 0;
+  const bool any = len - a.tokens + 1 + g_col / group > 0;
+  const float scale = 1.0f / sum;
+  const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
+  if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
+    *reinterpret_cast<uint2*>(a.out + to) =
+        any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale)) : make_uint2(0, 0);
+  if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
+    a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+}
+
+template <int G, int NT>
+kda_status run(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
+  using S = Shape<G, NT>;
+  constexpr auto kern = kv4_attention_kernel<G, NT>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return KDA_OK;
+  static const int resident = [] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, S::kSmem) == cudaSuccess ? n : 0;
+  }();
+  const int blocks = a.sm_count * std::max(resident, 1);
+  void* ws = nullptr;
+  const size_t records = sizeof(float) * 2 * blocks * S::kRecord;
+  const kda_status st = workspace_alloc(records + sizeof(Meta) * blocks, s, &ws);
+  if (st != KDA_OK) return st;
+  float* rec = static_cast<float*>(ws);
+  Meta* metas = reinterpret_cast<Meta*>(static_cast<unsigned char*>(ws) + records);
+  kern<<<blocks, kThreads, S::kSmem, s>>>(a, rec, metas);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    combine_kernel<G, NT><<<dim3(blocks, S::kCols), kThreads, 0, s>>>(a, rec, metas);
+    e = cudaGetLastError();
+  }
+  const cudaError_t ef = cudaFreeAsync(ws, s);
+  if (e == cudaSuccess) e = ef;
+  return KDA_OK;
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_attention(const Kv4AttentionArgs& a, cudaStream_t s) {
-  const int64_t blocks = (static_cast<int64_t>(a.N) * a.tokens * a.heads + kWarps - 1) / kWarps;
+kda_status launch_kv4_attention(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
+  const int cols = a.tokens * (a.heads / a.pages.heads);
   prof_begin(s, "kda_kv4_attention");
-  if (a.pages.d == 128) kv4_attention_kernel<4><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, s>>>(a);
-  else kv4_attention_kernel<2><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, s>>>(a);
+  const kda_status st = a.pages.d == 128 ? (cols <= 8 ? run<4, 1>(a, s, e) : run<4, 2>(a, s, e))
+                                         : (cols <= 8 ? run<2, 1>(a, s, e) : run<2, 2>(a, s, e));
   prof_end(s, "kda_kv4_attention");
-  return cudaGetLastError();
+  return st;
 }
 
 }  // namespace kda
