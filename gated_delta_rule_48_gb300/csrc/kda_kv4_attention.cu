@@ -13,9 +13,17 @@
 // cache as the 16-row operand, straight from the registers it was unpacked into:
 // S^T = K Q^T (16 tokens x 8 query rows), O^T += V^T P^T (16 channels x 8 query
 // rows).
-//   - A code is a bf16 value by an AND and an OR: bits 3..6 of 0x4180 hold n + 8
-//     as 16 + (n + 8) = 24 + n.  For keys the 24 goes away with the accumulator's
-//     first value, -24 sum_{c in g} q_c; for values it is subtracted (exactly).
+//   - A key's code n + 8 in the low bits of a 16-bit half is the f16 number
+//     (n + 8) 2^-24 as it stands (a subnormal one), in bits 4..7 16 times that: two
+//     codes to an AND, and four bits' shift less.  The queries' bf16 values are f16
+//     ones after a power of two for each row (what is 2^30 times smaller than a row's
+//     largest value may round).  The 8 goes away with the accumulator's first
+//     value, one product of the groups' scales with -8 2^-24 sum_{c in g} q_c in four
+//     bf16 parts.
+//   - A value's code is, as it stands, the bf16 number (n + 8) 2^-133 or 16 times
+//     that; one multiply-add makes it n 2^-6 exactly.  p, which it is multiplied by,
+//     needs the range of bf16.  (Leaving the 8 in and taking it off by a product with
+//     a constant was slower, 342 instead of 325 us, and not exact where p n is small.)
 //   - Scales never touch the codes: a group's part of a score is scaled in 32
 //     bits, and a value's scale is multiplied into p, which is rounded to bf16
 //     then (as in kda_attention_fwd; the rounding of p itself is left out).
@@ -30,6 +38,7 @@
 #include <cmath>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_attention.h"
 #include "kda_sm100.cuh"
@@ -69,12 +78,21 @@ struct Shape {
   static constexpr int kRecord = kCols * (D + 2);               // floats of a part: o, then m and l
 };
 
+// d += A B (or d = A B), bf16 operands.
+template <bool ADD = true>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (ADD)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // 8 x 8 values of 16 bits, turned.
 __device__ __forceinline__ uint32_t turned(uint32_t v) {
@@ -82,18 +100,50 @@ __device__ __forceinline__ uint32_t turned(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// Nibbles i of both halves as bf16: 24 + n.
-template <int I>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  const uint32_t at = I == 0 ? w << 3 : w >> (4 * I - 3);
-  return (at & 0x00780078u) | 0x41804180u;
+// d = A B (or d += A B), f16 operands.
+template <bool ADD>
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  if constexpr (ADD)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
-// The same less 24.
-template <int I>
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Codes n + 8 of both halves (bits 0..3, or 4..7 with HIGH) as n 2^-6 in bf16, exactly:
+// bits 0..7 of a bf16 number without the others are a whole number of 2^-133, also
+// where bit 7 makes it a normal one.
+template <bool HIGH>
 __device__ __forceinline__ uint32_t whole_numbers(uint32_t w) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(nibbles<I>(w)), "r"(0xc1c0c1c0u));
+  // (times 2^127 or 2^123, less 8 2^-6)
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(r)
+      : "r"(w & (HIGH ? 0x00f000f0u : 0x000f000fu)), "r"(HIGH ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
   return r;
+}
+template <int N>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -116,8 +166,11 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   const int blocks_c = (cols + S::kCols - 1) / S::kCols;
   const int64_t per_seq = static_cast<int64_t>(p.heads) * blocks_c;  // units of a sequence
   const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
+  // No more positions than the table has pages for (what is beyond is an error), and
+  // none whose number could pass 32 bits a few slices ahead.
+  const int64_t capacity = min(static_cast<int64_t>(p.width) << p.page_shift, int64_t{0x7ffff000});
   auto len_of = [&](int64_t n) -> int64_t {
-    return kda_guard(n, 1, a.N, a.err) ? max(a.seq_lens[n], 0) : 0;
+    return kda_guard(n, 1, a.N, a.err) ? min(static_cast<int64_t>(max(a.seq_lens[n], 0)), capacity) : 0;
   };
   auto slices_of = [&](int64_t n) { return (len_of(n) + kSlice - 1) / kSlice; };
 
@@ -139,7 +192,10 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   const int64_t chunk = (a.N + kThreads - 1) / kThreads;
   const int64_t c0 = min(chunk * threadIdx.x, static_cast<int64_t>(a.N)), c1 = min(c0 + chunk, static_cast<int64_t>(a.N));
   int64_t own = 0;
-  for (int64_t n = c0; n < c1; ++n) own += slices_of(n);
+  for (int64_t n = c0; n < c1; ++n) {
+    own += slices_of(n);
+    if (blockIdx.x == 0 && kda_guard(n, 1, a.N, a.err) && a.seq_lens[n] > capacity) atomicOr(a.err, kDevErrPage);
+  }
   int64_t scan = own;
 #pragma unroll
   for (int w = 1; w < 32; w *= 2) {
@@ -190,125 +246,147 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     const int32_t head = static_cast<int32_t>(unit / blocks_c), col0 = static_cast<int32_t>(unit % blocks_c) * S::kCols;
     const int64_t first = at - unit_first, last = min(part1 - unit_first, slices);  // slices [first, last)
     const int64_t len = len_of(seq);
-    const int64_t visible = len - a.tokens + 1;  // positions the first query reaches
+    const int32_t visible = static_cast<int32_t>(len) - a.tokens + 1;  // positions the first query reaches
 
-    // ---- queries: fragments of Q^T, and -24 times the groups' sums
-    uint32_t q[G][2][NT][2];
-    float offset[G][NT][2];
+    // ---- queries: fragments of Q^T in f16, and -8 times the groups' sums
+    uint32_t q[G][2][NT][2];   // [group][k 16]: channels 8 j + (0, 4), (1, 5), then (2, 6), (3, 7)
+    uint32_t offset[NT][2];    // their parts in bf16: of groups (0, 1), (2, 3), lane j the part j
+    float cc[NT][2];
     int32_t reach[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int col = col0 + 8 * t + r;
       const int64_t row = seq * a.tokens + col / group;
       const int64_t from = row * a.ld_q + static_cast<int64_t>(head * group + col % group) * S::D;
+      uint4 w[G];
+      uint32_t top = 0;  // of the magnitudes' bits
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        uint4 w = make_uint4(0, 0, 0, 0);
+        w[g] = make_uint4(0, 0, 0, 0);
         if (col < cols && kda_guard(from + 32 * g + 8 * j, 8, (n_rows - 1) * a.ld_q + a.heads * S::D, a.err))
-          w = *reinterpret_cast<const uint4*>(a.q + from + 32 * g + 8 * j);
-        // channels 8 j + (0, 4), (1, 5), (2, 6), (3, 7), as the keys' nibbles come
-        q[g][0][t][0] = __byte_perm(w.x, w.z, 0x5410);
-        q[g][0][t][1] = __byte_perm(w.x, w.z, 0x7632);
-        q[g][1][t][0] = __byte_perm(w.y, w.w, 0x5410);
-        q[g][1][t][1] = __byte_perm(w.y, w.w, 0x7632);
-        float sum = ((half_of(w.x, 0) + half_of(w.x, 1)) + (half_of(w.y, 0) + half_of(w.y, 1))) +
-                    ((half_of(w.z, 0) + half_of(w.z, 1)) + (half_of(w.w, 0) + half_of(w.w, 1)));
+          w[g] = *reinterpret_cast<const uint4*>(a.q + from + 32 * g + 8 * j);
+        const uint32_t u = __vmaxu2(__vmaxu2(w[g].x & 0x7fff7fffu, w[g].y & 0x7fff7fffu),
+                                    __vmaxu2(w[g].z & 0x7fff7fffu, w[g].w & 0x7fff7fffu));
+        top = max(top, max(u >> 16, u & 0xffffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^k brings the largest magnitude into [2^14, 2^15); an infinity or NaN makes the row NaN
+      const int k = min(141 - static_cast<int>(top >> 7), 126);
+      const float up = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+      // 2^-k and the 2^24 of codes read as f16
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23) * 0x1p24f;
+      cc[t][0] = c * __shfl_sync(0xffffffffu, down, 8 * j);
+      cc[t][1] = c * __shfl_sync(0xffffffffu, down, 8 * j + 4);
+      offset[t][0] = offset[t][1] = 0;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t x[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // channels 8 j + i, 8 j + i + 4: nibbles i and i + 4
+          const float v0 = half_of(x[i / 2], i % 2) * up, v1 = half_of(x[2 + i / 2], i % 2) * up;
+          // (codes in bits 4..7 of a half are read 16 times as large)
+          q[g][i / 2][t][i % 2] = pack2_f16(v0 * (i % 2 ? 0.0625f : 1.0f), v1 * (i % 2 ? 0.0625f : 1.0f));
+          sum += v0 + v1;
+        }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sum *= -24.0f;
-        offset[g][t][0] = __shfl_sync(0xffffffffu, sum, 8 * j);
-        offset[g][t][1] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
+        sum *= -8.0f * 0x1p-24f;
+        uint32_t part = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t bits = from_f32<Bf16>(sum).bits;
+          if (i == j) part = bits;
+          sum -= __uint_as_float(bits << 16);
+        }
+        offset[t][g / 2] |= part << (16 * (g % 2));
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)  // of this lane's columns 2 j + e
-        reach[t][e] = static_cast<int32_t>(visible + (col0 + 8 * t + 2 * j + e) / group);
+      for (int e = 0; e < 2; ++e)  // of this lane's columns 2 j + e, from its first position r on
+        reach[t][e] = visible + (col0 + 8 * t + 2 * j + e) / group - r;
     }
-    float o[2 * G][NT][4], m[NT][2], l[NT][2];
+    float o[2 * G][NT][4], m[NT][2], l[NT][2], limit[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int g = 0; g < 2 * G; ++g) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.0f;
-      m[t][0] = m[t][1] = kLowest;
-      l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = limit[t][e] = kLowest;
+        l[t][e] = 0.0f;
+      }
     }
 
     // ---- this warp's slices: first + warp, + 4, ...
-    const int64_t mine = max(int64_t{0}, (last - first - warp + kWarps - 1) / kWarps);
-    auto page_of = [&](int64_t i) -> int32_t {  // of slice number i of the warp
-      if (i >= mine) return 0;
-      const int64_t col = ((first + warp + i * kWarps) * kSlice) >> p.page_shift, e = seq * p.ld_table + col;
+    const int32_t mine = static_cast<int32_t>(max(int64_t{0}, (last - first - warp + kWarps - 1) / kWarps));
+    const int32_t pos0 = static_cast<int32_t>((first + warp) * kSlice);  // of the first one
+    const int32_t* const pages = p.table + seq * p.ld_table;
+    const int32_t place = (1 << p.page_shift) - 1;  // a position's bits in its page
+    const int32_t head_rows = head << p.page_shift, page_rows = p.heads << p.page_shift;
+    const uint8_t* const from_k = p.k_codes + 16 * lane;
+    const uint8_t* const from_v = p.v_codes + 16 * lane;
+    constexpr int kS = S::kScaleBytes / 16;
+    const uint8_t* const from_s = reinterpret_cast<const uint8_t*>(lane < kS ? p.k_scales : p.v_scales) + 16 * (lane % kS);
+    constexpr int kChunks = S::kRow / 16;  // of a row
+    const uint32_t to_k = smem_u32(ring) + 16 * lane;
+    const uint32_t to_v = smem_u32(ring) + kSlice * S::kRow + lane / kChunks * S::kPitchV + lane % kChunks * 16;
+    const uint32_t to_s = smem_u32(ring) + kSlice * (S::kRow + S::kPitchV) + 16 * lane;
+    const int32_t stop = pos0 + mine * (kWarps * kSlice);
+    auto page_of = [&](int32_t pos) -> int32_t {  // of a position of the warp's slices
       int32_t page = -1;
-      if (col < p.width && kda_guard(e, 1, (a.N - 1) * p.ld_table + p.width, a.err)) page = p.table[e];
+      if (pos < stop && (pos >> p.page_shift) < p.width &&
+          kda_guard(seq * p.ld_table + (pos >> p.page_shift), 1, (a.N - 1) * p.ld_table + p.width, a.err))
+        page = pages[pos >> p.page_shift];
       return page;
     };
-    auto fetch = [&](int64_t i, int32_t page) {
-      if (i < mine) {
-        if (page < 0 || page >= p.n_pages) {
-          if (lane == 0) atomicOr(a.err, kDevErrPage);
-          page = 0;
-        }
-        const int64_t pos = (first + warp + i * kWarps) * kSlice;
-        const int64_t row = kv4_row(p, (static_cast<int64_t>(page) << p.page_shift) + (pos & ((1 << p.page_shift) - 1)), head);
-        const uint32_t to = smem_u32(ring + (i % kDepth) * S::kStage);
-        if (p.n_pages > 0 && kda_guard(row, kSlice, kv4_rows(p), a.err)) {
-          constexpr int kChunks = S::kRow / 16;  // of a row
+    auto fetch = [&](int32_t pos, int32_t page, uint32_t at_stage) {
+      if (pos < stop) {
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages)) {
+          const int64_t row = static_cast<int64_t>(page) * page_rows + (head_rows + (pos & place));
+          if (kda_guard(row, kSlice, kv4_rows(p), a.err)) {
+            const uint8_t* k = from_k + row * S::kRow;
+            const uint8_t* v = from_v + row * S::kRow;
 #pragma unroll
-          for (int e = 0; e < kSlice * kChunks; e += 32) {
-            const int k = e + lane;
-            copy16(to + 16 * k, p.k_codes + row * S::kRow + 16 * k);
-            copy16(to + kSlice * S::kRow + k / kChunks * S::kPitchV + k % kChunks * 16, p.v_codes + row * S::kRow + 16 * k);
+            for (int e = 0; e < kSlice * kChunks; e += 32) {
+              copy16(to_k + at_stage + 16 * e, k + 16 * e);
+              copy16(to_v + at_stage + e / kChunks * S::kPitchV, v + 16 * e);
+            }
+            if (lane < 2 * kS) copy16(to_s + at_stage, from_s + row * (2 * G));
           }
-          constexpr int kS = S::kScaleBytes / 16;
-          if (lane < 2 * kS) {
-            const unsigned char* from = reinterpret_cast<const unsigned char*>(lane < kS ? p.k_scales : p.v_scales) +
-                                        row * (2 * G) + 16 * (lane % kS);
-            copy16(to + kSlice * (S::kRow + S::kPitchV) + 16 * lane, from);
-          }
+        } else if (lane == 0) {
+          atomicOr(a.err, kDevErrPage);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(i, page_of(i));
-    int32_t next_page = page_of(kDepth - 1);
-    for (int64_t i = 0; i < mine; ++i) {
-      fetch(i + kDepth - 1, next_page);
-      next_page = page_of(i + kDepth);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-      __syncwarp();
-      const unsigned char* stage = ring + (i % kDepth) * S::kStage;
-      const int64_t pos = (first + warp + i * kWarps) * kSlice;
 
+    // One slice; MASKED: some column does not reach all of its positions.
+    auto process = [&](const unsigned char* stage, int32_t pos, auto masked_c) {
+      constexpr bool MASKED = decltype(masked_c)::value;
       // ---- scores of positions r and r + 8
       float x[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.0f;
       {
         uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
-        const unsigned char* from = stage + r * S::kRow + 4 * G * j;
-        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * r;
-        if constexpr (G == 4) {
-          const uint4 u = *reinterpret_cast<const uint4*>(from), v = *reinterpret_cast<const uint4*>(from + 8 * S::kRow);
-          k0[0] = u.x; k0[1] = u.y; k0[2] = u.z; k0[3] = u.w;
-          k1[0] = v.x; k1[1] = v.y; k1[2] = v.z; k1[3] = v.w;
-          const uint2 f = *reinterpret_cast<const uint2*>(scales), h = *reinterpret_cast<const uint2*>(scales + 16 * G);
-          s0[0] = f.x; s0[1] = f.y; s1[0] = h.x; s1[1] = h.y;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(from), v = *reinterpret_cast<const uint2*>(from + 8 * S::kRow);
-          k0[0] = u.x; k0[1] = u.y; k1[0] = v.x; k1[1] = v.y;
-          s0[0] = *reinterpret_cast<const uint32_t*>(scales);
-          s1[0] = *reinterpret_cast<const uint32_t*>(scales + 16 * G);
-        }
+        load_words<G>(stage + r * S::kRow + 4 * G * j, k0);
+        load_words<G>(stage + (r + 8) * S::kRow + 4 * G * j, k1);
+        load_words<G / 2>(stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * r, s0);
+        load_words<G / 2>(stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * (r + 8), s1);
+        // what the 8 in n + 8 adds: the groups' scales times the offsets' four parts
+        const uint32_t scales[4] = {s0[0], s1[0], G == 4 ? s0[G / 2 - 1] : 0u, G == 4 ? s1[G / 2 - 1] : 0u};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma<false>(x[t], scales, offset[t][0], offset[t][1]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint32_t f0[4] = {nibbles<0>(k0[g]), nibbles<0>(k1[g]), nibbles<1>(k0[g]), nibbles<1>(k1[g])};
-          const uint32_t f1[4] = {nibbles<2>(k0[g]), nibbles<2>(k1[g]), nibbles<3>(k0[g]), nibbles<3>(k1[g])};
+          const uint32_t h0 = k0[g] >> 8, h1 = k1[g] >> 8;
+          const uint32_t f0[4] = {k0[g] & 0x000f000fu, k1[g] & 0x000f000fu, k0[g] & 0x00f000f0u, k1[g] & 0x00f000f0u};
+          const uint32_t f1[4] = {h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u};
           const float lo = half_of(s0[g / 2], g % 2), hi = half_of(s1[g / 2], g % 2);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float d[4] = {offset[g][t][0], offset[g][t][1], offset[g][t][0], offset[g][t][1]};
-            mma(d, f0, q[g][0][t][0], q[g][0][t][1]);
-            mma(d, f1, q[g][1][t][0], q[g][1][t][1]);
+            float d[4];
+            mma_f16<false>(d, f0, q[g][0][t]);
+            mma_f16<true>(d, f1, q[g][1][t]);
             x[t][0] = fmaf(d[0], lo, x[t][0]);
             x[t][1] = fmaf(d[1], lo, x[t][1]);
             x[t][2] = fmaf(d[2], hi, x[t][2]);
@@ -317,26 +395,30 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         }
       }
       // ---- softmax
-      const bool masked = pos + kSlice > visible;
+      bool hidden[NT][4];
       bool up = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[t][e] *= c;
-          if (masked && pos + r + (e >> 1) * 8 >= reach[t][e & 1]) x[t][e] = -INFINITY;
-          up = up || x[t][e] > m[t][e & 1] + kSlack;
+          if constexpr (MASKED) {
+            hidden[t][e] = pos + (e >> 1) * 8 >= reach[t][e & 1];
+            if (hidden[t][e]) x[t][e] = -INFINITY;
+          }
+          up = up || x[t][e] > limit[t][e & 1];
         }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(m[t][e], fmaxf(x[t][e], x[t][e + 2]));
+            float top = fmaxf(x[t][e], x[t][e + 2]) * cc[t][e];
 #pragma unroll
             for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            top = fmaxf(m[t][e], top);
             const float keep = ex2(m[t][e] - top);
             m[t][e] = top;
+            limit[t][e] = (top + kSlack) / cc[t][e];
             l[t][e] *= keep;
 #pragma unroll
             for (int g = 0; g < 2 * G; ++g) {
@@ -349,31 +431,18 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[t][e] = ex2(x[t][e] - m[t][e & 1]);
+          x[t][e] = ex2(fmaf(x[t][e], cc[t][e & 1], -m[t][e & 1]));
           l[t][e & 1] += x[t][e];
         }
       // ---- values
       {
-        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + S::kScaleBytes + 2 * G * r;
-        const unsigned char* from = stage + kSlice * S::kRow + 2 * j * S::kPitchV + 2 * G * r;
         uint32_t s0[G / 2], s1[G / 2], w[4][G / 2];
-        if constexpr (G == 4) {
-          const uint2 f = *reinterpret_cast<const uint2*>(scales), h = *reinterpret_cast<const uint2*>(scales + 16 * G);
-          s0[0] = f.x; s0[1] = f.y; s1[0] = h.x; s1[1] = h.y;
-        } else {
-          s0[0] = *reinterpret_cast<const uint32_t*>(scales);
-          s1[0] = *reinterpret_cast<const uint32_t*>(scales + 16 * G);
-        }
+        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + S::kScaleBytes;
+        load_words<G / 2>(scales + 2 * G * r, s0);
+        load_words<G / 2>(scales + 2 * G * (r + 8), s1);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // positions 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-          const unsigned char* at_k = from + (k / 2 * 8 + k % 2) * S::kPitchV;
-          if constexpr (G == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(at_k);
-            w[k][0] = u.x; w[k][1] = u.y;
-          } else {
-            w[k][0] = *reinterpret_cast<const uint32_t*>(at_k);
-          }
-        }
+        for (int k = 0; k < 4; ++k)  // positions 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+          load_words<G / 2>(stage + kSlice * S::kRow + (2 * j + k / 2 * 8 + k % 2) * S::kPitchV + 2 * G * r, w[k]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float lo = half_of(s0[g / 2], g % 2), hi = half_of(s1[g / 2], g % 2);
@@ -381,10 +450,10 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             float f[4] = {x[t][0] * lo, x[t][1] * lo, x[t][2] * hi, x[t][3] * hi};
-            if (masked) {  // (what is not reached may have any scale)
+            if constexpr (MASKED) {  // (what is not reached may have any scale)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (pos + r + (e >> 1) * 8 >= reach[t][e & 1]) f[e] = 0.0f;
+                if (hidden[t][e]) f[e] = 0.0f;
             }
             b0[t] = turned(pack2_bf16(f[0], f[1]));
             b1[t] = turned(pack2_bf16(f[2], f[3]));
@@ -392,8 +461,11 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
           // channels 4 r + i of the group, positions in pairs
           const uint32_t sel = g % 2 ? 0x7632 : 0x5410;
           const uint32_t y0 = __byte_perm(w[0][g / 2], w[1][g / 2], sel), y1 = __byte_perm(w[2][g / 2], w[3][g / 2], sel);
-          const uint32_t f0[4] = {whole_numbers<0>(y0), whole_numbers<1>(y0), whole_numbers<0>(y1), whole_numbers<1>(y1)};
-          const uint32_t f1[4] = {whole_numbers<2>(y0), whole_numbers<3>(y0), whole_numbers<2>(y1), whole_numbers<3>(y1)};
+          const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+          const uint32_t f0[4] = {whole_numbers<false>(y0), whole_numbers<true>(y0), whole_numbers<false>(y1),
+                                  whole_numbers<true>(y1)};
+          const uint32_t f1[4] = {whole_numbers<false>(z0), whole_numbers<true>(z0), whole_numbers<false>(z1),
+                                  whole_numbers<true>(z1)};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             mma(o[2 * g][t], f0, b0[t], b1[t]);
@@ -401,7 +473,22 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
           }
         }
       }
-      __syncwarp();  // the stage is free
+    };
+
+    constexpr int32_t kStep = kWarps * kSlice;
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(pos0 + i * kStep, page_of(pos0 + i * kStep), i * S::kStage);
+    int32_t ahead = pos0 + (kDepth - 1) * kStep, next_page = page_of(ahead);
+    uint32_t here = 0;  // the stage of the slice at hand
+    for (int32_t pos = pos0; pos < stop; pos += kStep) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      __syncwarp();  // this slice has come, and the one before has been read
+      fetch(ahead, next_page, here == 0 ? (kDepth - 1) * S::kStage : here - S::kStage);
+      ahead += kStep;
+      next_page = page_of(ahead);
+      if (pos + kSlice > visible) process(ring + here, pos, std::true_type{});
+      else process(ring + here, pos, std::false_type{});
+      here = here == (kDepth - 1) * S::kStage ? 0 : here + S::kStage;
     }
 
     // ---- the warps' results together
@@ -450,7 +537,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         const int g_col = col0 + col;
         if (g_col < cols) {
           const bool any = visible + g_col / group > 0;
-          const float scale = any ? 1.0f / sum : 0.0f;
+          const float scale = 64.0f / sum;  // (codes were read as n 2^-6)
           const int64_t row = seq * a.tokens + g_col / group;
           const int32_t h = head * group + g_col % group;
           const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
@@ -525,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Kv4AttentionArgs a, c
   const int32_t h = mt.head * group + g_col % group;
   const int64_t len = kda_guard(mt.seq, 1, a.N, a.err) ? a.seq_lens[mt.seq] : 0;
   const bool any = len - a.tokens + 1 + g_col / group > 0;
-  const float scale = 1.0f / sum;
+  const float scale = 64.0f / sum;  // (codes were read as n 2^-6)
   const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
   if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
     *reinterpret_cast<uint2*>(a.out + to) =
