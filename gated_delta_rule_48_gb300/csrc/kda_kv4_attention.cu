@@ -30,7 +30,7 @@
 //   - The order of codes in a row is that in which a lane needs them: 16 bytes of
 //     a key, 8 of a value, each with channels of all groups.
 //
-// Work: the slices of 16 positions of all (sequence, key head, 16 query rows)
+// Work: the slices of 32 positions of all (sequence, key head, 16 query rows)
 // form one line that is cut into equal parts, one per block, whatever the
 // sequences' lengths.  A block goes through its part unit by unit, its warps a
 // slice each in turn, with copies a few slices ahead; units that lie in one block
@@ -51,8 +51,9 @@ using sm100::smem_u32;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSlice = 16;        // positions of a slice
-constexpr int kDepth = 4;         // slices of a warp in flight
+constexpr int kSlice = 32;        // positions of a slice: two halves, for a page may end between them
+constexpr int kHalf = 16;
+constexpr int kDepth = 3;         // slices of a warp in flight
 constexpr float kLowest = -1e30f; // a maximum of nothing
 constexpr float kSlack = 8.0f;    // log2 of how far p may pass 1
 constexpr float kLn2 = 0.6931471805599453f;
@@ -153,7 +154,7 @@ __device__ __forceinline__ float half_of(uint32_t pair, int i) {
 }
 
 template <int G, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, 3)
 kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   using S = Shape<G, NT>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -324,39 +325,45 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     const int32_t* const pages = p.table + seq * p.ld_table;
     const int32_t place = (1 << p.page_shift) - 1;  // a position's bits in its page
     const int32_t head_rows = head << p.page_shift, page_rows = p.heads << p.page_shift;
-    const uint8_t* const from_k = p.k_codes + 16 * lane;
-    const uint8_t* const from_v = p.v_codes + 16 * lane;
-    constexpr int kS = S::kScaleBytes / 16;
-    const uint8_t* const from_s = reinterpret_cast<const uint8_t*>(lane < kS ? p.k_scales : p.v_scales) + 16 * (lane % kS);
+    // 16 lanes copy a half, each from its half's page
+    const int half = lane >> 4, of_half = lane & 15;
+    const uint8_t* const from_k = p.k_codes + 16 * of_half;
+    const uint8_t* const from_v = p.v_codes + 16 * of_half;
+    constexpr int kS = kHalf * 2 * G / 16;  // pieces of 16 bytes of a half's scales
+    const uint8_t* const from_s =
+        reinterpret_cast<const uint8_t*>(of_half < kS ? p.k_scales : p.v_scales) + 16 * (of_half % kS);
     constexpr int kChunks = S::kRow / 16;  // of a row
-    const uint32_t to_k = smem_u32(ring) + 16 * lane;
-    const uint32_t to_v = smem_u32(ring) + kSlice * S::kRow + lane / kChunks * S::kPitchV + lane % kChunks * 16;
-    const uint32_t to_s = smem_u32(ring) + kSlice * (S::kRow + S::kPitchV) + 16 * lane;
+    const uint32_t to_k = smem_u32(ring) + half * (kHalf * S::kRow) + 16 * of_half;
+    const uint32_t to_v = smem_u32(ring) + kSlice * S::kRow + (half * kHalf + of_half / kChunks) * S::kPitchV +
+                          of_half % kChunks * 16;
+    const uint32_t to_s = smem_u32(ring) + kSlice * (S::kRow + S::kPitchV) + (of_half < kS ? 0 : S::kScaleBytes) +
+                          half * (16 * kS) + 16 * (of_half % kS);
     const int32_t stop = pos0 + mine * (kWarps * kSlice);
-    auto page_of = [&](int32_t pos) -> int32_t {  // of a position of the warp's slices
+    // (the last slice's second half may lie behind the sequence's last position)
+    const int32_t held = static_cast<int32_t>(len);
+    auto page_of = [&](int32_t pos) -> int32_t {  // of this lane's half of a slice
+      const int32_t at_page = (pos + half * kHalf) >> p.page_shift;
       int32_t page = -1;
-      if (pos < stop && (pos >> p.page_shift) < p.width &&
-          kda_guard(seq * p.ld_table + (pos >> p.page_shift), 1, (a.N - 1) * p.ld_table + p.width, a.err))
-        page = pages[pos >> p.page_shift];
+      if (pos < stop && pos + half * kHalf < held &&
+          kda_guard(seq * p.ld_table + at_page, 1, (a.N - 1) * p.ld_table + p.width, a.err))
+        page = pages[at_page];
       return page;
     };
     auto fetch = [&](int32_t pos, int32_t page, uint32_t at_stage) {
-      if (pos < stop) {
-        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages)) {
-          const int64_t row = static_cast<int64_t>(page) * page_rows + (head_rows + (pos & place));
-          if (kda_guard(row, kSlice, kv4_rows(p), a.err)) {
-            const uint8_t* k = from_k + row * S::kRow;
-            const uint8_t* v = from_v + row * S::kRow;
+      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.n_pages)) {
+        const int64_t row = static_cast<int64_t>(page) * page_rows + (head_rows + ((pos + half * kHalf) & place));
+        if (kda_guard(row, kHalf, kv4_rows(p), a.err)) {
+          const uint8_t* k = from_k + row * S::kRow;
+          const uint8_t* v = from_v + row * S::kRow;
 #pragma unroll
-            for (int e = 0; e < kSlice * kChunks; e += 32) {
-              copy16(to_k + at_stage + 16 * e, k + 16 * e);
-              copy16(to_v + at_stage + e / kChunks * S::kPitchV, v + 16 * e);
-            }
-            if (lane < 2 * kS) copy16(to_s + at_stage, from_s + row * (2 * G));
+          for (int e = 0; e < kHalf * kChunks; e += 16) {
+            copy16(to_k + at_stage + 16 * e, k + 16 * e);
+            copy16(to_v + at_stage + e / kChunks * S::kPitchV, v + 16 * e);
           }
-        } else if (lane == 0) {
-          atomicOr(a.err, kDevErrPage);
+          if (of_half < 2 * kS) copy16(to_s + at_stage, from_s + row * (2 * G));
         }
+      } else if (pos < stop && pos + half * kHalf < held) {
+        atomicOr(a.err, kDevErrPage);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -364,18 +371,21 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     // One slice; MASKED: some column does not reach all of its positions.
     auto process = [&](const unsigned char* stage, int32_t pos, auto masked_c) {
       constexpr bool MASKED = decltype(masked_c)::value;
-      // ---- scores of positions r and r + 8
-      float x[NT][4];
-      {
+      // ---- scores of positions r and r + 8 of both halves
+      float x[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t k0[G], k1[G], s0[G / 2], s1[G / 2];
-        load_words<G>(stage + r * S::kRow + 4 * G * j, k0);
-        load_words<G>(stage + (r + 8) * S::kRow + 4 * G * j, k1);
-        load_words<G / 2>(stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * r, s0);
-        load_words<G / 2>(stage + kSlice * (S::kRow + S::kPitchV) + 2 * G * (r + 8), s1);
+        const unsigned char* keys = stage + h * (kHalf * S::kRow) + 4 * G * j;
+        const unsigned char* key_scales = stage + kSlice * (S::kRow + S::kPitchV) + h * (kHalf * 2 * G);
+        load_words<G>(keys + r * S::kRow, k0);
+        load_words<G>(keys + (r + 8) * S::kRow, k1);
+        load_words<G / 2>(key_scales + 2 * G * r, s0);
+        load_words<G / 2>(key_scales + 2 * G * (r + 8), s1);
         // what the 8 in n + 8 adds: the groups' scales times the offsets' four parts
         const uint32_t scales[4] = {s0[0], s1[0], G == 4 ? s0[G / 2 - 1] : 0u, G == 4 ? s1[G / 2 - 1] : 0u};
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma<false>(x[t], scales, offset[t][0], offset[t][1]);
+        for (int t = 0; t < NT; ++t) mma<false>(x[h][t], scales, offset[t][0], offset[t][1]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const uint32_t h0 = k0[g] >> 8, h1 = k1[g] >> 8;
@@ -387,32 +397,31 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
             float d[4];
             mma_f16<false>(d, f0, q[g][0][t]);
             mma_f16<true>(d, f1, q[g][1][t]);
-            x[t][0] = fmaf(d[0], lo, x[t][0]);
-            x[t][1] = fmaf(d[1], lo, x[t][1]);
-            x[t][2] = fmaf(d[2], hi, x[t][2]);
-            x[t][3] = fmaf(d[3], hi, x[t][3]);
+            x[h][t][0] = fmaf(d[0], lo, x[h][t][0]);
+            x[h][t][1] = fmaf(d[1], lo, x[h][t][1]);
+            x[h][t][2] = fmaf(d[2], hi, x[h][t][2]);
+            x[h][t][3] = fmaf(d[3], hi, x[h][t][3]);
           }
         }
       }
       // ---- softmax
-      bool hidden[NT][4];
+      auto hidden = [&](int h, int t, int e) { return pos + h * kHalf + (e >> 1) * 8 >= reach[t][e & 1]; };
       bool up = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (MASKED) {
-            hidden[t][e] = pos + (e >> 1) * 8 >= reach[t][e & 1];
-            if (hidden[t][e]) x[t][e] = -INFINITY;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (MASKED && hidden(h, t, e)) x[h][t][e] = -INFINITY;
+            up = up || x[h][t][e] > limit[t][e & 1];
           }
-          up = up || x[t][e] > limit[t][e & 1];
-        }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(x[t][e], x[t][e + 2]) * cc[t][e];
+            float top = fmaxf(fmaxf(x[0][t][e], x[0][t][e + 2]), fmaxf(x[1][t][e], x[1][t][e + 2])) * cc[t][e];
 #pragma unroll
             for (int w = 4; w < 32; w *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
             top = fmaxf(m[t][e], top);
@@ -428,32 +437,35 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
           }
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[t][e] = ex2(fmaf(x[t][e], cc[t][e & 1], -m[t][e & 1]));
-          l[t][e & 1] += x[t][e];
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[h][t][e] = ex2(fmaf(x[h][t][e], cc[t][e & 1], -m[t][e & 1]));
+            l[t][e & 1] += x[h][t][e];
+          }
       // ---- values
-      {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint32_t s0[G / 2], s1[G / 2], w[4][G / 2];
-        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + S::kScaleBytes;
+        const unsigned char* scales = stage + kSlice * (S::kRow + S::kPitchV) + S::kScaleBytes + h * (kHalf * 2 * G);
         load_words<G / 2>(scales + 2 * G * r, s0);
         load_words<G / 2>(scales + 2 * G * (r + 8), s1);
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // positions 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-          load_words<G / 2>(stage + kSlice * S::kRow + (2 * j + k / 2 * 8 + k % 2) * S::kPitchV + 2 * G * r, w[k]);
+          load_words<G / 2>(stage + kSlice * S::kRow + (h * kHalf + 2 * j + k / 2 * 8 + k % 2) * S::kPitchV + 2 * G * r, w[k]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float lo = half_of(s0[g / 2], g % 2), hi = half_of(s1[g / 2], g % 2);
           uint32_t b0[NT], b1[NT];
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float f[4] = {x[t][0] * lo, x[t][1] * lo, x[t][2] * hi, x[t][3] * hi};
+            float f[4] = {x[h][t][0] * lo, x[h][t][1] * lo, x[h][t][2] * hi, x[h][t][3] * hi};
             if constexpr (MASKED) {  // (what is not reached may have any scale)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (hidden[t][e]) f[e] = 0.0f;
+                if (hidden(h, t, e)) f[e] = 0.0f;
             }
             b0[t] = turned(pack2_bf16(f[0], f[1]));
             b1[t] = turned(pack2_bf16(f[2], f[3]));
