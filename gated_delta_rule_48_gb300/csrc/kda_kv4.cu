@@ -23,14 +23,42 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// max(., 2^-64) / 7, rounded once more to bf16.  A NaN stays one, an infinity too.
-__device__ __forceinline__ uint32_t scale_bits(float top) {
-  return from_f32<Bf16>(__fdiv_rn(max_nan(top, kAmaxMin), 7.0f)).bits;
+// The scale's bits from those of the largest magnitude (bf16; a NaN or an infinity
+// is larger than any number).  top * fl(1/7) rounds to the bf16 number that top / 7
+// does: of T / 7 with T of 8 bits no multiple of half a unit is nearer than 2^-12.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
+  const float v = __uint_as_float(top << 16);
+  return from_f32<Bf16>(max_nan(v, kAmaxMin) * (1.0f / 7.0f)).bits;
 }
-// n + 8; a quotient that is NaN (a group with an infinity or NaN) counts as 0
-__device__ __forceinline__ uint32_t code_of(float x, float scale) {
-  const float n = rintf(__fdiv_rn(x, scale));
-  return static_cast<uint32_t>(static_cast<int32_t>(n == n ? n : 0.0f) + 8);
+
+// Eight values' codes n + 8, n = x / s rounded half to even, for a finite scale s.
+//
+// x r, r = 1 / s as the hardware gives it, is x / s but for 2^-21.  x and s have 8
+// bits, so where x / s is not a half, it is 2^-11 or more away from one (for quotients
+// from 1/4 on; smaller ones are 0 anyway).  So x r is first rounded to multiples of
+// 2^-12, which makes halves exact, and then to a whole number: each time by adding a
+// number whose last bit has that value.  The whole number then is the low bits of the
+// sum's significand, and a product and sum puts it in its place.
+__device__ __forceinline__ uint32_t codes_of(const uint4& raw, uint32_t scale) {
+  constexpr float kFine = 1.5f * 2048.0f, kWhole = 1.5f * 8388608.0f + 8.0f;  // last bits 2^-12, 1
+  const float r = rcp(__uint_as_float(scale << 16));
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const f32x2 rr = pack2(r, r), fine = pack2(kFine, kFine), less = pack2(-kFine, -kFine), whole = pack2(kWhole, kWhole);
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 x = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    const f32x2 n = add2(add2(fma2(x, rr, fine), less), whole);
+    float lo, hi;
+    unpack2(n, lo, hi);
+    // (the bits above the lowest four, the same for all n, go away below)
+    word += (__float_as_uint(lo) << (8 * i)) + (__float_as_uint(hi) << (8 * i + 4));
+  }
+  constexpr uint32_t kHigh = 0x4b400008u;  // of kWhole, and so of every sum less n
+  constexpr uint32_t kAll = (kHigh << 0) + (kHigh << 4) + (kHigh << 8) + (kHigh << 12) + (kHigh << 16) +
+                            (kHigh << 20) + (kHigh << 24) + (kHigh << 28);
+  word = word - kAll + 0x88888888u;
+  return (scale & 0x7f80u) == 0x7f80u ? 0x88888888u : word;  // (a group with a NaN or an infinity)
 }
 
 // Words of codes of 8 channels each, one of every group: as they lie in a row of
@@ -80,22 +108,13 @@ __device__ __forceinline__ void quantise(const Kv4Pages& p, const Bf16* x, bool 
   uint32_t words[G], scales[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-    float v[8], top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(v[i]));
-    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t u = __vmaxu2(__vmaxu2(raw[g].x & 0x7fff7fffu, raw[g].y & 0x7fff7fffu),
+                                __vmaxu2(raw[g].z & 0x7fff7fffu, raw[g].w & 0x7fff7fffu));
+    uint32_t top = max(u >> 16, u & 0xffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     scales[g] = scale_bits(top);
-    const float scale = __uint_as_float(scales[g] << 16);
-    words[g] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) words[g] |= code_of(v[i], scale) << (4 * i);
+    words[g] = codes_of(raw[g], scales[g]);
   }
   const int64_t rows = kv4_rows(p);
   if (!valid || !kda_guard(row, 1, rows, err)) return;

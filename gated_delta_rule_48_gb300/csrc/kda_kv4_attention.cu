@@ -35,6 +35,8 @@
 // sequences' lengths.  A block goes through its part unit by unit, its warps a
 // slice each in turn, with copies a few slices ahead; units that lie in one block
 // are written out, the parts of others combined by a second launch.
+#include <string.h>
+
 #include <cmath>
 
 #include <algorithm>
@@ -63,7 +65,8 @@ struct Meta {
   int32_t last;       // the last block that has a part (-1: nothing to combine)
   int32_t slot;       // of the first block's part
   int32_t seq, head, col0;
-  int32_t pad[3];
+  int32_t visible;    // positions the first query reaches
+  int32_t pad[2];
 };
 
 template <int G, int NT>
@@ -175,6 +178,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   };
   auto slices_of = [&](int64_t n) { return (len_of(n) + kSlice - 1) / kSlice; };
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- sequences of no positions: zeros
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
     if (len_of(n) > 0) continue;
@@ -575,6 +579,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       mt.seq = static_cast<int32_t>(seq);
       mt.head = head;
       mt.col0 = col0;
+      mt.visible = visible;
       metas[b] = mt;
     }
     __syncthreads();  // the ring is filled again
@@ -582,20 +587,24 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   }
 }
 
-// The parts of a unit that several blocks worked on: block (b, column).
+// The parts of units that several blocks worked on: block b those of the unit that
+// begins in block b's part of the line and goes on behind it.  Four channels of a
+// column to a thread, several sets of threads share the parts.
+constexpr int kCombineThreads = 1024;
+
 template <int G, int NT>
-__global__ void __launch_bounds__(kThreads) combine_kernel(Kv4AttentionArgs a, const float* records, const Meta* metas) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Kv4AttentionArgs a, const float* records, const Meta* metas) {
   using S = Shape<G, NT>;
-  __shared__ float4 s_v[kThreads];
-  __shared__ float s_m[kThreads], s_l[kThreads];
-  constexpr int kLanes = S::D / 4, kSets = kThreads / kLanes;  // channels in fours; sets of parts
+  constexpr int kItems = S::kCols * (S::D / 4), kSets = kCombineThreads / kItems;
+  __shared__ float4 s_v[kSets - 1][kItems];
+  __shared__ float2 s_ml[kSets - 1][kItems];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the first kernel's end
   const Meta mt = metas[blockIdx.x];
   if (mt.last < 0) return;
   const int group = a.heads / a.pages.heads, cols = a.tokens * group;
-  const int col = blockIdx.y, g_col = mt.col0 + col;
-  if (g_col >= cols) return;
-  const int ch = threadIdx.x % kLanes * 4, set = threadIdx.x / kLanes;
-  const int64_t b0 = blockIdx.x;
+  const int item = threadIdx.x % kItems, set = threadIdx.x / kItems;
+  const int col = item / (S::D / 4), ch = item % (S::D / 4) * 4, g_col = mt.col0 + col;
+  const int b0 = blockIdx.x;
   float top = kLowest, sum = 0.0f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float m2, float l2, const float4& x) {
@@ -608,22 +617,23 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Kv4AttentionArgs a, c
     v.w = fmaf(x.w, k1, v.w * k0);
   };
 #pragma unroll 4
-  for (int64_t b = b0 + set; b <= mt.last; b += kSets) {
-    const float* record = records + (b * 2 + (b == b0 ? mt.slot : 0)) * S::kRecord;
-    add(record[S::kCols * S::D + 2 * col], record[S::kCols * S::D + 2 * col + 1],
-        *reinterpret_cast<const float4*>(record + col * S::D + ch));
+  for (int b = b0 + set; b <= mt.last; b += kSets) {
+    const float* record = records + (static_cast<int64_t>(b) * 2 + (b == b0 ? mt.slot : 0)) * S::kRecord;
+    const float2 ml = *reinterpret_cast<const float2*>(record + S::kCols * S::D + 2 * col);
+    add(ml.x, ml.y, *reinterpret_cast<const float4*>(record + col * S::D + ch));
   }
-  s_v[threadIdx.x] = v;
-  s_m[threadIdx.x] = top;
-  s_l[threadIdx.x] = sum;
+  if (set > 0) {
+    s_v[set - 1][item] = v;
+    s_ml[set - 1][item] = make_float2(top, sum);
+  }
   __syncthreads();
-  if (set != 0) return;
-  for (int i = 1; i < kSets; ++i) add(s_m[i * kLanes + threadIdx.x], s_l[i * kLanes + threadIdx.x], s_v[i * kLanes + threadIdx.x]);
+  if (set != 0 || g_col >= cols) return;
+#pragma unroll
+  for (int i = 0; i < kSets - 1; ++i) add(s_ml[i][item].x, s_ml[i][item].y, s_v[i][item]);
   const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
   const int64_t row = static_cast<int64_t>(mt.seq) * a.tokens + g_col / group;
   const int32_t h = mt.head * group + g_col % group;
-  const int64_t len = kda_guard(mt.seq, 1, a.N, a.err) ? a.seq_lens[mt.seq] : 0;
-  const bool any = len - a.tokens + 1 + g_col / group > 0;
+  const bool any = mt.visible + g_col / group > 0;
   const float scale = 64.0f / sum;  // (codes were read as n 2^-6)
   const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
   if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
@@ -653,8 +663,19 @@ kda_status run(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   kern<<<blocks, kThreads, S::kSmem, s>>>(a, rec, metas);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
-    combine_kernel<G, NT><<<dim3(blocks, S::kCols), kThreads, 0, s>>>(a, rec, metas);
-    e = cudaGetLastError();
+    // its blocks may come while the first kernel's last ones work, and wait for its end
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<G, NT>, a, static_cast<const float*>(rec),
+                           static_cast<const Meta*>(metas));
   }
   const cudaError_t ef = cudaFreeAsync(ws, s);
   if (e == cudaSuccess) e = ef;
