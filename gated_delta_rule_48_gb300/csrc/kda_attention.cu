@@ -45,17 +45,20 @@ constexpr int kThreads = 128 + kRows;    // control warps, then a thread per row
 constexpr int kLaunchRegs = 168, kRowRegs = 224, kRestRegs = 56;
 static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
               "register shares exceed the launch's");
+constexpr int kParts = 2;                // of a tile's P, handed over one by one
 constexpr float kSlack = 8.0f;           // log2 of how far p may pass 1
 
 template <int D>
 struct Shape {
   static constexpr int kBlocks = D / 64;                     // 128-byte column blocks of a row
   static constexpr uint32_t kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 10;          // of K's and V's tiles in turn
-  static constexpr uint32_t kSmem = (2 + kStages) * kTileBytes;
+  // V's tile j and K's tile j + 1 are copied, used and given back together
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kSmem = (3 + 2 * kStages) * kTileBytes;  // Q's two, K's first, the pairs
   // tensor memory: S (and P over it) of both tiles, then O
   static constexpr uint32_t kColS = 0, kColO = 2 * kTile;
   static_assert(kSmem + 1024 + 512 <= 227 * 1024, "memory of an SM");
+  static_assert(kSmem > 114 * 1024, "one block to an SM: each takes all of tensor memory");
 };
 
 struct Maps {
@@ -160,10 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   using G = Shape<D>;
   extern __shared__ __align__(1024) unsigned char smem[];  // Q's tiles, then the ring
-  __shared__ uint64_t q_full[2], kv_full[G::kStages], kv_empty[G::kStages];
-  __shared__ uint64_t s_full[2], p_full[2], o_full[2], v_here, v_ok;
+  __shared__ uint64_t q_full[2], k_full, kv_full[G::kStages], kv_empty[G::kStages], v_ok[G::kStages];
+  __shared__ uint64_t s_full[2], p_full[2][kParts], o_full[2], drained[2];
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort, s_infinite;
+  __shared__ volatile int s_infinite;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (a.cu_q && blockIdx.x == 0) {
@@ -223,17 +226,17 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      for (int h = 0; h < kParts; ++h) mbar_init(&p_full[i][h], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&drained[i], 1);
     }
+    mbar_init(&k_full, 1);
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 3);  // both tiles' products and the look through V
+      mbar_init(&v_ok[i], 1);
     }
-    mbar_init(&v_here, 1);
-    mbar_init(&v_ok, 2);
     mbar_fence_init();
-    s_abort = 0;
     s_infinite = 0;
   }
   if (warp == 1) {
@@ -244,42 +247,43 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  unsigned char* const ring = smem + 2 * G::kTileBytes;
-  auto timeout = [&]() {
-    atomicOr(a.err, kDevErrTimeout);
-    s_abort = 1;
-  };
+  unsigned char* const first_k = smem + 2 * G::kTileBytes;
+  unsigned char* const ring = first_k + G::kTileBytes;  // V, K; V, K
+  auto timeout = [&]() { atomicOr(a.err, kDevErrTimeout); };
   auto whole_warp = [](bool ok) { return __all_sync(0xffffffffu, ok); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == 0) {
-      // ---- copies: K 0, V 0, K 1, V 1 ... into the ring
+      // ---- copies
       const bool issues = elect_one();
-      if (issues) {
+      auto copy = [&](unsigned char* to, const CUtensorMap* map, int32_t head, int64_t row, uint64_t* bar) {
+#pragma unroll
+        for (int b = 0; b < G::kBlocks; ++b)
+          tma_load_3d(to + b * (kTile * 128), map, 64 * b, head, static_cast<int32_t>(row), bar);
+      };
+      if (issues && n_max > 0) {
+        mbar_arrive_expect_tx(&k_full, G::kTileBytes);
+        copy(first_k, &maps.k, u.kv_head, u.k0, &k_full);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (n_tiles[i] == 0) continue;
           mbar_arrive_expect_tx(&q_full[i], G::kTileBytes);
-#pragma unroll
-          for (int b = 0; b < G::kBlocks; ++b)
-            tma_load_3d(smem + i * G::kTileBytes + b * (kTile * 128), &maps.q, 64 * b, u.head0,
-                        static_cast<int32_t>(u.q0 + u.tok0 + i * (tokens / 2)), &q_full[i]);
+          copy(smem + i * G::kTileBytes, &maps.q, u.head0, u.q0 + u.tok0 + i * (tokens / 2), &q_full[i]);
         }
       }
       int at = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int64_t item = 0; item < 2 * n_max && ok; ++item) {
+      for (int64_t j = 0; j < n_max && ok; ++j) {
         ok = whole_warp(mbar_wait(&kv_empty[at], phase ^ 1));  // (the first round passes at once)
         if (!ok) break;
         if (issues) {
-          mbar_arrive_expect_tx(&kv_full[at], G::kTileBytes);
-          const int32_t row = static_cast<int32_t>(u.k0 + (item >> 1) * kTile);
-#pragma unroll
-          for (int b = 0; b < G::kBlocks; ++b)
-            tma_load_3d(ring + at * G::kTileBytes + b * (kTile * 128), item & 1 ? &maps.v : &maps.k, 64 * b,
-                        u.kv_head, row, &kv_full[at]);
+          unsigned char* const to = ring + at * (2 * G::kTileBytes);
+          const bool more = j + 1 < n_max;
+          mbar_arrive_expect_tx(&kv_full[at], more ? 2 * G::kTileBytes : G::kTileBytes);
+          copy(to, &maps.v, u.kv_head, u.k0 + j * kTile, &kv_full[at]);
+          if (more) copy(to + G::kTileBytes, &maps.k, u.kv_head, u.k0 + (j + 1) * kTile, &kv_full[at]);
         }
         if (++at == G::kStages) { at = 0; phase ^= 1; }
       }
@@ -291,118 +295,103 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
           if (++at == G::kStages) { at = 0; phase ^= 1; }
         }
       }
-    } else if (warp == 1) {
-      // ---- products
+    } else if (warp < 3) {
+      // ---- products, a warp to a tile.  S_i of the next keys comes behind O_i of
+      // these: P_i lies over S_i.
+      const int i = warp - 1;
       const bool issues = elect_one();
       constexpr uint32_t id_s = make_idesc(kFmtBF16, kTile, kTile, false, false);
       constexpr uint32_t id_o = make_idesc(kFmtBF16, kTile, D, false, true);
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), kTile * 128, 1024);
-      auto scores = [&](int i, int at) {  // S_i = Q_i K^T
-        const uint64_t q = q_desc + i * (G::kTileBytes >> 4), k = k_desc + at * (G::kTileBytes >> 4);
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + i * G::kTileBytes), 16, 1024);
+      const uint32_t t_s = tmem + G::kColS + i * kTile, t_o = tmem + G::kColO + i * D;
+      auto scores = [&](uint64_t k) {  // S_i = Q_i K^T
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t step = (s / 4) * (kTile * 128 >> 4) + (s % 4) * 2;
-          mma_f16_ss(tmem + G::kColS + i * kTile, q + step, k + step, id_s, s > 0);
+          mma_f16_ss(t_s, q_desc + step, k + step, id_s, s > 0);
         }
+        mma_commit(&s_full[i]);
       };
-      auto outputs = [&](int i, int at, bool add) {  // O_i += P_i V
-        const uint64_t v = v_desc + at * (G::kTileBytes >> 4);
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          mma_f16_ts(tmem + G::kColO + i * D, tmem + G::kColS + i * kTile + 8 * s, v + s * (2048 >> 4), id_o,
-                     add || s > 0);
-      };
-      struct Place {
-        int at = 0;
-        uint32_t phase = 0;
-        __device__ void next() {
-          if (++at == G::kStages) { at = 0; phase ^= 1; }
-        }
-      } here;  // of the next item
+      const int64_t mine = n_tiles[i];
+      int at = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      if (n_max > 0) {
-        ok = whole_warp(mbar_wait(&kv_full[here.at], here.phase));
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (n_tiles[i] == 0) continue;
-          ok = whole_warp(mbar_wait(&q_full[i], 0));
-          if (!ok) break;
-          tc_fence_after();
-          if (issues) {
-            scores(i, here.at);
-            mma_commit(&s_full[i]);
-          }
-        }
-        if (issues) mma_commit(&kv_empty[here.at]);
-        here.next();
+      if (mine > 0) {
+        ok = mbar_wait(&k_full, 0) && mbar_wait(&q_full[i], 0);
+        if (ok && issues) scores(smem_desc_sw128(smem_u32(first_k), 16, 1024));
       }
       for (int64_t j = 0; j < n_max && ok; ++j) {
-        const int v_at = here.at;
-        ok = whole_warp(mbar_wait(&kv_full[v_at], here.phase));
-        // looked through beside the softmax
-        const bool masked = j >= first_masked;
-        if (ok && masked && lane == 0) mbar_arrive(&v_here);
-        here.next();
-        const bool more = j + 1 < n_max;
-        if (ok && more) ok = whole_warp(mbar_wait(&kv_full[here.at], here.phase));
-        if (ok && masked) ok = whole_warp(mbar_wait(&v_ok, static_cast<uint32_t>(j - first_masked) & 1));
+        // (looked through, where some row does not reach all of V's tile)
+        ok = mbar_wait(j >= first_masked ? &v_ok[at] : &kv_full[at], phase);
+        if (j < mine) {
+          const uint32_t pair = smem_u32(ring + at * (2 * G::kTileBytes));
+          const uint64_t v = smem_desc_sw128(pair, kTile * 128, 1024);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || j >= n_tiles[i]) continue;
-          ok = whole_warp(mbar_wait(&p_full[i], static_cast<uint32_t>(j) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (issues) {
-            outputs(i, v_at, j > 0);
-            if (j + 1 < n_tiles[i]) {
-              scores(i, here.at);
-              mma_commit(&s_full[i]);
-            } else {
-              mma_commit(&o_full[i]);
+          for (int part = 0; part < kParts; ++part) {  // O_i += P_i V
+            ok = ok && mbar_wait(&p_full[i][part], static_cast<uint32_t>(j) & 1);
+            if (ok && issues) {
+              tc_fence_after();
+#pragma unroll
+              for (int s = part * (kTile / 16 / kParts); s < (part + 1) * (kTile / 16 / kParts); ++s)
+                mma_f16_ts(t_o, t_s + 8 * s, v + s * (2048 >> 4), id_o, j > 0 || s > 0);
             }
           }
+          if (ok && issues) {
+            if (j + 1 < mine) scores(smem_desc_sw128(pair + G::kTileBytes, 16, 1024));
+            else mma_commit(&o_full[i]);
+          }
         }
-        if (!ok) break;
-        if (issues) {
-          mma_commit(&kv_empty[v_at]);
-          if (more) mma_commit(&kv_empty[here.at]);
-        }
-        if (more) here.next();
+        if (ok && issues) mma_commit(&kv_empty[at]);
+        if (++at == G::kStages) { at = 0; phase ^= 1; }
       }
-      if (!ok) timeout();
+      if (!ok) {
+        timeout();
+        if (issues) {  // the products in flight end before their memory goes
+          mma_commit(&drained[i]);
+          mbar_wait(&drained[i], 0, 1u << 16);
+        }
+      }
+      __syncwarp();
     } else {
       // ---- V's tiles that some row does not reach all of: no infinity or NaN
       bool ok = true;
-      for (int64_t j = first_masked; j < n_max && ok; ++j) {
-        const int at = static_cast<int>((2 * j + 1) % G::kStages);
-        ok = whole_warp(mbar_wait(&v_here, static_cast<uint32_t>(j - first_masked) & 1));
+      int at = 0;
+      uint32_t phase = 0;
+      for (int64_t j = 0; j < n_max && ok; ++j) {
+        ok = whole_warp(mbar_wait(&kv_full[at], phase));
         if (!ok) break;
-        uint4* tile = reinterpret_cast<uint4*>(ring + at * G::kTileBytes);
-        constexpr int kVecs = G::kTileBytes / 16;
-        uint32_t sum[4] = {0, 0, 0, 0};
-        for (int e = threadIdx.x - 64; e < kVecs; e += 64) {
-          const uint4 w = tile[e];
-          sum[0] = times_zero(w.x, sum[0]);
-          sum[1] = times_zero(w.y, sum[1]);
-          sum[2] = times_zero(w.z, sum[2]);
-          sum[3] = times_zero(w.w, sum[3]);
-        }
-        // (a sum of zeros is 0 or -0)
-        if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0) {
-          for (int e = threadIdx.x - 64; e < kVecs; e += 64) {
-            uint4 w = tile[e];
-            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              x[i] = (finite_bf16(x[i]) ? x[i] & 0xffffu : 0u) | (finite_bf16(x[i] >> 16) ? x[i] & 0xffff0000u : 0u);
-            tile[e] = w;
+        if (j >= first_masked) {
+          uint4* tile = reinterpret_cast<uint4*>(ring + at * (2 * G::kTileBytes));
+          constexpr int kVecs = G::kTileBytes / 16;
+          uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 8
+          for (int e = lane; e < kVecs; e += 32) {
+            const uint4 w = tile[e];
+            sum[0] = times_zero(w.x, sum[0]);
+            sum[1] = times_zero(w.y, sum[1]);
+            sum[2] = times_zero(w.z, sum[2]);
+            sum[3] = times_zero(w.w, sum[3]);
           }
-          s_infinite = 1;
-          fence_proxy_async_smem();
+          // (a sum of zeros is 0 or -0)
+          if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0) {
+            for (int e = lane; e < kVecs; e += 32) {
+              uint4 w = tile[e];
+              uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = (finite_bf16(x[k]) ? x[k] & 0xffffu : 0u) | (finite_bf16(x[k] >> 16) ? x[k] & 0xffff0000u : 0u);
+              tile[e] = w;
+            }
+            s_infinite = 1;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ok);
+        if (lane == 0) {
+          mbar_arrive(&v_ok[at]);
+          mbar_arrive(&kv_empty[at]);
+        }
+        if (++at == G::kStages) { at = 0; phase ^= 1; }
       }
       if (!ok && lane == 0) timeout();
     }
@@ -458,25 +447,31 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         tmem_wait_st();
       }
       const float base = m == -INFINITY ? 0.0f : m * c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const f32x2 cc = pack2(c, c), less = pack2(-base, -base);
+      f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float packed[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float lo = ex2(fmaf(s[64 * k + 2 * e], c, -base));
-          const float hi = ex2(fmaf(s[64 * k + 2 * e + 1], c, -base));
-          sum[2 * (e % 2)] += lo;
-          sum[2 * (e % 2) + 1] += hi;
+          float lo, hi;
+          unpack2(fma2(pack2(s[64 * k + 2 * e], s[64 * k + 2 * e + 1]), cc, less), lo, hi);
+          lo = ex2(lo);
+          hi = ex2(hi);
+          sum[e % 2] = add2(sum[e % 2], pack2(lo, hi));
           packed[e] = __uint_as_float(pack2_bf16(lo, hi));
         }
         tmem_st32(t_s + 32 * k, packed);
+        if (kParts == 2 || k == 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[i][kParts == 2 ? k : 0]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
+      float lo, hi;
+      unpack2(add2(sum[0], sum[1]), lo, hi);
+      l += lo + hi;
     }
     // ---- output
     if (ok && tiles > 0) {
