@@ -45,6 +45,7 @@ constexpr int kThreads = 128 + kRows;    // control warps, then a thread per row
 constexpr int kLaunchRegs = 168, kRowRegs = 224, kRestRegs = 56;
 static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
               "register shares exceed the launch's");
+constexpr int kPartTiles = 4;            // the least of a unit's part of the keys
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
 constexpr float kSlack = 8.0f;           // log2 of how far p may pass 1
 
@@ -78,17 +79,41 @@ struct Unit {
   int32_t head0, kv_head;
   int32_t tiles[2];    // of keys, for each tile of rows
   int32_t masked;      // from this one on some row does not reach a tile's keys all
+  int32_t record;      // where a part of the keys is kept; -1: the unit has all of them
 
   // how many keys query `tok` of the sequence reaches
   __device__ __forceinline__ int32_t reach(int32_t tok, bool causal) const {
-    return causal ? max(0, len + min(0, tok + 1 - n_q)) : len;
+    return max(0, causal ? len + min(0, tok + 1 - n_q) : len);
   }
   __device__ __forceinline__ int32_t most() const { return max(tiles[0], tiles[1]); }
 };
 
+// Where a unit's keys may be shared by several blocks (a.splits > 1), the tiles of
+// keys that there are for an SM, about: the same for all lanes of a warp.
+__device__ int32_t tiles_per_sm(const AttentionArgs& a, int pack, int lane) {
+  if (a.splits == 1) return 0;
+  const int tokens = kRows / pack;
+  float sum = 0.0f;
+  for (int32_t n = lane; n < a.N; n += 32) {
+    int64_t q0, q1, k0, k1;
+    sequence_span(a.cu_q, a.N, a.Tq, n, q0, q1, a.err);
+    sequence_span(a.cu_k, a.N, a.Tk, n, k0, k1, a.err);
+    sum += static_cast<float>((q1 - q0 + tokens - 1) / tokens) * static_cast<float>((k1 - k0 + kTile - 1) / kTile);
+  }
+#pragma unroll
+  for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  return static_cast<int32_t>(fminf(sum * (a.heads / pack) / a.sm_count, 1e9f));
+}
+
 // The unit of block `index`; false: there is none.  Those with the most keys come
-// first: a causal sequence's last ones.
-__device__ bool find_unit(const AttentionArgs& a, int pack, int32_t index, Unit& u) {
+// first: a causal sequence's last ones.  With `splits`, block index % splits of the
+// blocks of unit index / splits: parts of at least kPartTiles tiles of keys and three
+// quarters of what an SM has to do; `parts` is how many there are.
+__device__ bool find_unit(const AttentionArgs& a, int pack, int32_t index, int32_t per_sm, Unit& u, int32_t& parts) {
+  const int32_t part = index % a.splits;
+  index /= a.splits;
+  parts = 1;
+  u.record = -1;
   const int tokens = kRows / pack;  // queries of a unit
   const int head_blocks = a.heads / pack;
   const int32_t slot = index / head_blocks, hb = index - slot * head_blocks;
@@ -129,6 +154,19 @@ __device__ bool find_unit(const AttentionArgs& a, int pack, int32_t index, Unit&
     const int32_t first = u.tok0 + i * (tokens / 2), last = min(first + tokens / 2, u.n_q) - 1;
     const int32_t keys = last >= first ? u.reach(last, a.causal) : 0;
     u.tiles[i] = keys / kTile + (keys % kTile != 0);
+  }
+  if (a.splits > 1) {
+    const int32_t most = u.most(), length = max(kPartTiles, static_cast<int32_t>(int64_t{3} * per_sm / 4));
+    parts = max(1, min(a.splits, (most + length - 1) / length));
+    if (part >= parts) return false;
+    if (parts > 1) {
+      const int32_t count = (most + parts - 1) / parts, first = min(part * count, most);
+      u.record = index * a.splits + part;
+      u.k0 += first * kTile;
+      u.len -= first * kTile;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) u.tiles[i] = max(0, min(u.tiles[i] - first, count));
+    }
   }
   u.masked = u.reach(u.tok0, a.causal) / kTile;
   return true;
@@ -235,6 +273,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* r) {
       : "memory");
 }
 
+// 32 bytes, a whole sector, at a multiple of 32.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // 0 for finite pairs of bf16, NaN in a half whose value is not.
 __device__ __forceinline__ uint32_t times_zero(uint32_t pair, uint32_t sum) {
   uint32_t r;
@@ -323,14 +368,17 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       int at = 0;
       uint32_t phase = 0, n = 0, asked = 0, k_uses = 0, q_uses[2] = {0, 0};
       bool ok = true, more = true;
-      int32_t index = blockIdx.x;
+      int32_t index = blockIdx.x, parts;
+      const int32_t per_sm = tiles_per_sm(a, pack, lane);
       while (more && ok) {
         if (index == 0 && a.cu_q) {
           check_cu_seqlens(a.cu_q, a.N, a.Tq, lane, 32, a.err);
           check_cu_seqlens(a.cu_k, a.N, a.Tk, lane, 32, a.err);
         }
         Unit u;
-        if (find_unit(a, pack, index, u)) {
+        const bool there = find_unit(a, pack, index, per_sm, u, parts);
+        if (a.splits > 1 && index % a.splits == 0 && lane == 0) a.parts[index / a.splits] = there ? parts : 0;
+        if (there) {
           ok = whole_warp(mbar_wait(&unit_empty[n & 1], ((n >> 1) & 1) ^ 1));  // (the first round passes at once)
           if (!ok) break;
           if (lane == 0) {
@@ -660,7 +708,8 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         if (!ok) break;
         tc_fence_after();
       }
-      const float scale = reach > 0 ? 1.0f / l : 0.0f;
+      const bool part = u.record >= 0;
+      const float scale = part ? 1.0f : reach > 0 ? 1.0f / l : 0.0f;
       const int64_t at = (static_cast<int64_t>(u.q0) + tok) * a.ld_out + static_cast<int64_t>(head) * D;
       const int64_t extent = (a.Tq - 1) * a.ld_out + static_cast<int64_t>(a.heads) * D;
 #pragma unroll 1
@@ -677,7 +726,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = reach > 0 ? o[e] * scale : 0.0f;
         if (s_infinite) {  // values taken out of V's tiles, for rows that reach them
-          for (int32_t t = u.masked * kTile; t < reach; ++t) {
+          for (int32_t t = u.masked * kTile; t < min(reach, tiles * kTile); ++t) {
             const int64_t from = (static_cast<int64_t>(u.k0) + t) * a.ld_v + static_cast<int64_t>(u.kv_head) * D + k;
             if (!kda_guard(from, 32, (a.Tk - 1) * a.ld_v + static_cast<int64_t>(a.kv_heads) * D, a.err)) continue;
 #pragma unroll
@@ -687,16 +736,36 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
             }
           }
         }
-        if (valid && kda_guard(at + k, 32, extent, a.err)) {
+        if (part) {
+          float* to = a.part_out + (static_cast<int64_t>(u.record) * kRows + i * kTile + row) * D + k;
+          if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(a.out + at + k + e) =
-                make_uint4(pack2_bf16(o[e], o[e + 1]), pack2_bf16(o[e + 2], o[e + 3]),
-                           pack2_bf16(o[e + 4], o[e + 5]), pack2_bf16(o[e + 6], o[e + 7]));
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(o[e + x]);
+              store32(to + e, w);
+            }
+          }
+        } else if (valid && kda_guard(at + k, 32, extent, a.err)) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) w[x] = pack2_bf16(o[e + 2 * x], o[e + 2 * x + 1]);
+            if (a.sectors) {
+              store32(a.out + at + k + e, w);
+            } else {
+              *reinterpret_cast<uint4*>(a.out + at + k + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(a.out + at + k + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
       }
       const int64_t e = (static_cast<int64_t>(u.q0) + tok) * a.heads + head;
-      if (a.lse && valid && kda_guard(e, 1, a.Tq * a.heads, a.err))
+      if (part) {
+        if (valid) a.part_ml[static_cast<int64_t>(u.record) * kRows + i * kTile + row] = make_float2(m, l);
+      } else if (a.lse && valid && kda_guard(e, 1, a.Tq * a.heads, a.err))
         a.lse[e] = reach > 0 ? (m == -INFINITY ? 0.0f : m) * a.scale + logf(l) : -INFINITY;
     }
     if (!ok && lane == 0) timeout();
@@ -705,6 +774,94 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// The parts of units whose keys several blocks shared: kJoinRows rows of a unit to a
+// block, four channels (or two) of a row to a lane.  The parts go to the block's warps
+// in turn (SHARED), or, where there are few, all to the warp of a row.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinRows = 8;
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int pack) {
+  constexpr int kPer = D / 32, kMine = SHARED ? kJoinRows : kJoinRows / kJoinWarps;  // rows of a warp
+  __shared__ float s_o[SHARED ? kJoinWarps : 1][kJoinRows][D];
+  __shared__ float2 s_ml[SHARED ? kJoinWarps : 1][kJoinRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t unit = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the first kernel's end
+  const int32_t parts = a.parts[unit];
+  if (parts < 2) return;
+  Unit u;
+  int32_t same;
+  AttentionArgs whole = a;
+  whole.splits = 1;
+  if (!find_unit(whole, pack, unit, 0, u, same)) return;
+  if (u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
+  const int row0 = blockIdx.y * kJoinRows + (SHARED ? 0 : warp * kMine);
+  const int64_t first = static_cast<int64_t>(unit) * a.splits * kRows + row0;
+  const float c = a.scale * kLog2e;
+  // (rows behind a sequence's last query hold anything, and go nowhere)
+  float m[kMine], l[kMine], o[kMine][kPer];
+#pragma unroll
+  for (int r = 0; r < kMine; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[r][e] = 0.0f;
+  }
+  auto add = [&](int r, const float2& ml, const float (&v)[kPer]) {
+    const float next = fmaxf(m[r], ml.x), base = next == -INFINITY ? 0.0f : next * c;
+    const float keep = ex2(fmaf(m[r], c, -base)), w = ex2(fmaf(ml.x, c, -base));
+    m[r] = next;
+    l[r] = fmaf(ml.y, w, l[r] * keep);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(v[e], w, o[r][e] * keep);
+  };
+#pragma unroll 2
+  for (int32_t p = SHARED ? warp : 0; p < parts; p += SHARED ? kJoinWarps : 1) {
+    const int64_t at = first + static_cast<int64_t>(p) * kRows;
+#pragma unroll
+    for (int r = 0; r < kMine; ++r) {
+      float v[kPer];
+      load_n<kPer>(a.part_out + (at + r) * D + kPer * lane, v);
+      add(r, a.part_ml[at + r], v);
+    }
+  }
+  auto put = [&](int row, int r) {
+    const int32_t tok = u.tok0 + row / pack, head = u.head0 + row % pack;
+    if (tok >= u.n_q) return;
+    const bool any = u.reach(tok, a.causal) > 0;
+    const float scale = 1.0f / l[r];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[r][e] = any ? o[r][e] * scale : 0.0f;
+    const int64_t at = (static_cast<int64_t>(u.q0) + tok) * a.ld_out + static_cast<int64_t>(head) * D + kPer * lane;
+    if (kda_guard(at, kPer, (a.Tq - 1) * a.ld_out + static_cast<int64_t>(a.heads) * D, a.err))
+      store_n<kPer>(a.out + at, o[r]);
+    const int64_t e = (static_cast<int64_t>(u.q0) + tok) * a.heads + head;
+    if (a.lse && lane == 0 && kda_guard(e, 1, a.Tq * a.heads, a.err))
+      a.lse[e] = any ? (m[r] == -INFINITY ? 0.0f : m[r]) * a.scale + logf(l[r]) : -INFINITY;
+  };
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int r = 0; r < kMine; ++r) {
+      store_n<kPer>(&s_o[warp][r][kPer * lane], o[r]);
+      if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    m[0] = -INFINITY;
+    l[0] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[0][e] = 0.0f;
+    for (int w = 0; w < kJoinWarps; ++w) {  // a row to a warp, in the parts' order of warps
+      float v[kPer];
+      load_n<kPer>(&s_o[w][warp][kPer * lane], v);
+      add(0, s_ml[w][warp], v);
+    }
+    put(row0 + warp, 0);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kMine; ++r) put(row0 + r, r);
+  }
 }
 
 // ---- host side
@@ -738,19 +895,20 @@ bool encode(CUtensorMap* m, const void* base, int d, int heads, int64_t tokens, 
 }
 
 template <int D>
-cudaError_t run(const AttentionArgs& a, cudaStream_t s) {
+kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   using G = Shape<D>;
   // heads of a group side by side in a tile: the largest power of two in the group
   const int group = a.heads / a.kv_heads, pack = std::min(group & -group, kTile);
   Maps maps;
   memset(&maps, 0, sizeof maps);
+  e = cudaErrorInvalidValue;
   if (!encode(&maps.q, a.q, D, a.heads, a.Tq, a.ld_q, static_cast<uint32_t>(pack),
               static_cast<uint32_t>(kTile / pack)))
-    return cudaErrorInvalidValue;
+    return KDA_OK;
   // (without keys no tile of them is copied)
   if (a.Tk > 0 && (!encode(&maps.k, a.k, D, a.kv_heads, a.Tk, a.ld_k, 1, kTile) ||
                    !encode(&maps.v, a.v, D, a.kv_heads, a.Tk, a.ld_v, 1, kTile)))
-    return cudaErrorInvalidValue;
+    return KDA_OK;
   constexpr auto kern = attention_kernel<D>;
   // a build that launches with fewer registers could never give the rows' warps
   // their share: it is not launched
@@ -758,25 +916,61 @@ cudaError_t run(const AttentionArgs& a, cudaStream_t s) {
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
   }();
-  if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
-  if (e != cudaSuccess) return e;
+  e = cudaErrorInvalidConfiguration;
+  if (regs < kLaunchRegs) return KDA_OK;
   const int64_t tokens = kRows / pack;
   const int64_t slots = a.cu_q ? a.Tq / tokens + a.N : (a.Tq / a.N + tokens - 1) / tokens * a.N;
-  const int64_t grid = slots * (a.heads / pack);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kern<<<static_cast<unsigned>(grid), kThreads, G::kSmem, s>>>(maps, a, pack);
-  return cudaGetLastError();
+  const int64_t units = slots * (a.heads / pack);
+  if (units > 0x7fffffffLL) return KDA_OK;
+  // With fewer units than two for each SM, the longest one's keys may keep its SM busy
+  // when the others are done: units may be cut into parts then, as many blocks as eight
+  // for each SM, no more parts than a sequence can have.  (8 x 263 queries of 32 heads
+  // behind 3900 keys on average, 280 units: 120 us whole.)
+  const int64_t longest = ((a.cu_k ? a.Tk : a.Tk / a.N) + kTile - 1) / kTile;
+  if (units < 2 * a.sm_count)
+    a.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(8 * a.sm_count / units, longest / kPartTiles)));
+  void* ws = nullptr;
+  if (a.splits > 1) {
+    const size_t rows = static_cast<size_t>(units) * a.splits * kRows;
+    const kda_status st = workspace_alloc(rows * (D * sizeof(float) + sizeof(float2)) + units * sizeof(int32_t), s, &ws);
+    if (st != KDA_OK) return st;
+    a.part_out = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_out + rows * D);
+    a.parts = reinterpret_cast<int32_t*>(a.part_ml + rows);
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
+  if (e == cudaSuccess) {
+    kern<<<static_cast<unsigned>(units * a.splits), kThreads, G::kSmem, s>>>(maps, a, pack);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && a.splits > 1) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(units), kRows / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = a.splits > kJoinWarps ? cudaLaunchKernelEx(&cfg, join_kernel<D, true>, a, pack)
+                              : cudaLaunchKernelEx(&cfg, join_kernel<D, false>, a, pack);
+  }
+  if (ws) {
+    const cudaError_t ef = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = ef;
+  }
+  return KDA_OK;
 }
 
 }  // namespace
 
-cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s) {
+kda_status launch_attention(const AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   prof_begin(s, "kda_attention_fwd");
-  const cudaError_t e = a.d == 128 ? run<128>(a, s) : run<64>(a, s);
+  const kda_status st = a.d == 128 ? run<128>(a, s, e) : run<64>(a, s, e);
   prof_end(s, "kda_attention_fwd");
-  return e;
+  return st;
 }
 
 }  // namespace kda

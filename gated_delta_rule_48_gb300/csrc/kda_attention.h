@@ -25,10 +25,19 @@ struct AttentionArgs {
   int32_t N, heads, kv_heads, d;
   float scale;
   bool causal;
+  bool sectors;             // every row of out starts on a 32-byte boundary
   int sm_count;
   int* err;
+  // Few units of rows: their keys shared by several blocks, up to `splits` of them
+  // (kda_attention.cu); a part's sums [unit * splits + part][256][d], each row's
+  // maximum and sum of p, and how many parts a unit has.
+  int32_t splits = 1;
+  float* part_out = nullptr;
+  float2* part_ml = nullptr;
+  int32_t* parts = nullptr;
 };
-cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t s);
+// Allocates its workspace, if any: a status of its own if that fails, else `e`.
+kda_status launch_attention(const AttentionArgs& a, cudaStream_t s, cudaError_t& e);
 
 // ---- the paged cache of 4-bit codes (kda_kv4.cu)
 constexpr int kKv4Group = 32;  // channels of a token and head that share a scale

@@ -194,9 +194,12 @@ extern "C" kda_status kda_attention_fwd(const void* q, int64_t ld_q, const void*
   a.d = d;
   a.scale = scale;
   a.causal = causal != 0;
+  a.sectors = aligned(out, 32) && a.ld_out % 16 == 0;
   KDA_TRY(device_sm_count(&a.sm_count));
   KDA_TRY(device_error_word(&a.err));
-  return launched(launch_attention(a, static_cast<cudaStream_t>(stream)), "attention launch");
+  cudaError_t e = cudaSuccess;
+  KDA_TRY(launch_attention(a, static_cast<cudaStream_t>(stream), e));
+  return launched(e, "attention launch");
 }
 
 extern "C" kda_status kda_kv4_write(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
