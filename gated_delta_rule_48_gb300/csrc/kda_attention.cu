@@ -88,76 +88,127 @@ struct Unit {
   __device__ __forceinline__ int32_t most() const { return max(tiles[0], tiles[1]); }
 };
 
-// Where a unit's keys may be shared by several blocks (a.splits > 1), the tiles of
-// keys that there are for an SM, about: the same for all lanes of a warp.
-__device__ int32_t tiles_per_sm(const AttentionArgs& a, int pack, int lane) {
-  if (a.splits == 1) return 0;
-  const int tokens = kRows / pack;
+// The sequences of a packed batch, up to 64 of them, two to a lane: where they lie,
+// and the first of their units, longest sequences (by keys) first.  Held by the warp
+// that hands out units: looked up in memory, one load behind the other, a unit took
+// some 3 us to find, and in the sequences' own order the longest came when it came.
+struct Line {
+  int32_t q0[2], n_q[2], k0[2], len[2], first[2];
+};
+constexpr int kLine = 64;
+
+__device__ __forceinline__ int32_t units_of(int32_t n_q, int shift) { return (n_q >> shift) + ((n_q & ((1 << shift) - 1)) != 0); }
+
+// `shift`: log2 of a unit's queries.  Also the tiles of keys that there are for an SM,
+// about, where units may be cut (a.splits > 1): the same for all lanes.
+__device__ void make_line(const AttentionArgs& a, int pack, int shift, int lane, Line& line, int32_t& per_sm) {
   float sum = 0.0f;
-  for (int32_t n = lane; n < a.N; n += 32) {
+  for (int32_t n = lane; n < a.N && (a.splits > 1 || n < kLine); n += 32) {
     int64_t q0, q1, k0, k1;
     sequence_span(a.cu_q, a.N, a.Tq, n, q0, q1, a.err);
     sequence_span(a.cu_k, a.N, a.Tk, n, k0, k1, a.err);
-    sum += static_cast<float>((q1 - q0 + tokens - 1) / tokens) * static_cast<float>((k1 - k0 + kTile - 1) / kTile);
+    sum += static_cast<float>((q1 - q0 + (1 << shift) - 1) >> shift) * static_cast<float>((k1 - k0 + kTile - 1) / kTile);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (n >> 5 == e) {
+        line.q0[e] = static_cast<int32_t>(q0);
+        line.n_q[e] = static_cast<int32_t>(q1 - q0);
+        line.k0[e] = static_cast<int32_t>(k0);
+        line.len[e] = static_cast<int32_t>(k1 - k0);
+      }
   }
 #pragma unroll
   for (int w = 16; w; w /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  return static_cast<int32_t>(fminf(sum * (a.heads / pack) / a.sm_count, 1e9f));
+  per_sm = static_cast<int32_t>(fminf(sum * (a.heads / pack) / a.sm_count, 1e9f));
+  if (!a.cu_q || a.N > kLine) return;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    line.first[e] = 0;
+    if (lane + 32 * e >= a.N) line.n_q[e] = line.len[e] = line.q0[e] = line.k0[e] = 0;
+  }
+  for (int n = 0; n < a.N; ++n) {
+    const int32_t len = __shfl_sync(0xffffffffu, n < 32 ? line.len[0] : line.len[1], n & 31);
+    const int32_t units = units_of(__shfl_sync(0xffffffffu, n < 32 ? line.n_q[0] : line.n_q[1], n & 31), shift);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int32_t own = lane + 32 * e;
+      if (len > line.len[e] || (len == line.len[e] && n < own)) line.first[e] += units;
+    }
+  }
 }
 
-// The unit of block `index`; false: there is none.  Those with the most keys come
-// first: a causal sequence's last ones.  With `splits`, block index % splits of the
-// blocks of unit index / splits: parts of at least kPartTiles tiles of keys and three
-// quarters of what an SM has to do; `parts` is how many there are.
-__device__ bool find_unit(const AttentionArgs& a, int pack, int32_t index, int32_t per_sm, Unit& u, int32_t& parts) {
-  const int32_t part = index % a.splits;
-  index /= a.splits;
+// The unit of block `index`, for a whole warp; false: there is none.  Those with the
+// most keys come first: the longest sequences, of a causal one its last queries.  With
+// `splits`, block index % splits of the blocks of unit index / splits: parts of at least
+// kPartTiles tiles of keys and three quarters of what an SM has to do; `parts` is how
+// many there are.
+__device__ bool find_unit(const AttentionArgs& a, int pack, int shift, int32_t index, const Line& line,
+                          int32_t per_sm, int lane, Unit& u, int32_t& parts) {
+  const int32_t part = a.splits > 1 ? index % a.splits : 0;
+  if (a.splits > 1) index /= a.splits;
   parts = 1;
   u.record = -1;
-  const int tokens = kRows / pack;  // queries of a unit
   const int head_blocks = a.heads / pack;
   const int32_t slot = index / head_blocks, hb = index - slot * head_blocks;
-  int32_t block, seq;
-  if (a.cu_q) {
-    // sequence n's units lie in slots [cu[n] / tokens + n, cu[n + 1] / tokens + n + 1):
-    // enough for its queries, wherever they start
-    int32_t lo = 0, hi = a.N - 1;
-    while (lo < hi) {
-      const int32_t mid = lo + ((hi - lo + 1) >> 1);
-      if (!kda_guard(mid, 1, static_cast<int64_t>(a.N) + 1, a.err)) break;
-      if (static_cast<int64_t>(a.cu_q[mid] / tokens) + mid <= slot) lo = mid; else hi = mid - 1;
-    }
-    seq = lo;
-    int32_t first = 0;
-    if (kda_guard(lo, 1, static_cast<int64_t>(a.N) + 1, a.err)) first = a.cu_q[lo];
-    const int64_t at = slot - (static_cast<int64_t>(first / tokens) + lo);
-    block = at < 0 || at > 0x7fffff ? -1 : static_cast<int32_t>(at);
+  int32_t block;
+  if (a.cu_q && a.N <= kLine) {
+    bool is[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      is[e] = slot >= line.first[e] && slot - line.first[e] < units_of(line.n_q[e], shift);
+    const uint32_t in0 = __ballot_sync(0xffffffffu, is[0]), in1 = __ballot_sync(0xffffffffu, is[1]);
+    if (!in0 && !in1) return false;
+    const int from = __ffs(in0 ? in0 : in1) - 1;
+    auto get = [&](const int32_t (&v)[2]) { return __shfl_sync(0xffffffffu, in0 ? v[0] : v[1], from); };
+    block = slot - get(line.first);
+    u.q0 = get(line.q0);
+    u.n_q = get(line.n_q);
+    u.k0 = get(line.k0);
+    u.len = get(line.len);
   } else {
-    seq = slot % a.N;
-    block = slot / a.N;
+    int32_t seq;
+    if (a.cu_q) {
+      // sequence n's units lie in slots [cu[n] / queries + n, cu[n + 1] / queries + n + 1):
+      // enough for its queries, wherever they start
+      int32_t lo = 0, hi = a.N - 1;
+      while (lo < hi) {
+        const int32_t mid = lo + ((hi - lo + 1) >> 1);
+        if (!kda_guard(mid, 1, static_cast<int64_t>(a.N) + 1, a.err)) break;
+        if (static_cast<int64_t>(a.cu_q[mid] >> shift) + mid <= slot) lo = mid; else hi = mid - 1;
+      }
+      seq = lo;
+      int32_t first = 0;
+      if (kda_guard(lo, 1, static_cast<int64_t>(a.N) + 1, a.err)) first = a.cu_q[lo];
+      const int64_t at = slot - (static_cast<int64_t>(first >> shift) + lo);
+      block = at < 0 || at > 0x7fffff ? -1 : static_cast<int32_t>(at);
+    } else {
+      seq = slot % a.N;
+      block = slot / a.N;
+    }
+    int64_t q0, q1, k0, k1;
+    sequence_span(a.cu_q, a.N, a.Tq, seq, q0, q1, a.err);
+    sequence_span(a.cu_k, a.N, a.Tk, seq, k0, k1, a.err);
+    u.q0 = static_cast<int32_t>(q0);
+    u.n_q = static_cast<int32_t>(q1 - q0);
+    u.k0 = static_cast<int32_t>(k0);
+    u.len = static_cast<int32_t>(k1 - k0);
   }
-  int64_t q0, q1, k0, k1;
-  sequence_span(a.cu_q, a.N, a.Tq, seq, q0, q1, a.err);
-  sequence_span(a.cu_k, a.N, a.Tk, seq, k0, k1, a.err);
-  u.q0 = static_cast<int32_t>(q0);
-  u.n_q = static_cast<int32_t>(q1 - q0);
-  u.k0 = static_cast<int32_t>(k0);
-  u.len = static_cast<int32_t>(k1 - k0);
-  const int32_t blocks = u.n_q / tokens + (u.n_q % tokens != 0);
+  const int32_t blocks = units_of(u.n_q, shift);
   if (block < 0 || block >= blocks) return false;
   u.live = 1;
-  u.tok0 = (blocks - 1 - block) * tokens;
+  u.tok0 = (blocks - 1 - block) << shift;
   u.head0 = hb * pack;
   u.kv_head = u.head0 / (a.heads / a.kv_heads);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int32_t first = u.tok0 + i * (tokens / 2), last = min(first + tokens / 2, u.n_q) - 1;
+    const int32_t first = u.tok0 + (i << (shift - 1)), last = min(first + (1 << (shift - 1)), u.n_q) - 1;
     const int32_t keys = last >= first ? u.reach(last, a.causal) : 0;
     u.tiles[i] = keys / kTile + (keys % kTile != 0);
   }
   if (a.splits > 1) {
     const int32_t most = u.most(), length = max(kPartTiles, static_cast<int32_t>(int64_t{3} * per_sm / 4));
     parts = max(1, min(a.splits, (most + length - 1) / length));
+    if (part == 0 && lane == 0) a.parts[index] = PartInfo{parts, u.q0, u.n_q, u.len, u.tok0, u.head0};
     if (part >= parts) return false;
     if (parts > 1) {
       const int32_t count = (most + parts - 1) / parts, first = min(part * count, most);
@@ -369,15 +420,18 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       uint32_t phase = 0, n = 0, asked = 0, k_uses = 0, q_uses[2] = {0, 0};
       bool ok = true, more = true;
       int32_t index = blockIdx.x, parts;
-      const int32_t per_sm = tiles_per_sm(a, pack, lane);
+      const int shift = 31 - __clz(tokens);
+      Line line;
+      int32_t per_sm;
+      make_line(a, pack, shift, lane, line, per_sm);
       while (more && ok) {
         if (index == 0 && a.cu_q) {
           check_cu_seqlens(a.cu_q, a.N, a.Tq, lane, 32, a.err);
           check_cu_seqlens(a.cu_k, a.N, a.Tk, lane, 32, a.err);
         }
         Unit u;
-        const bool there = find_unit(a, pack, index, per_sm, u, parts);
-        if (a.splits > 1 && index % a.splits == 0 && lane == 0) a.parts[index / a.splits] = there ? parts : 0;
+        const bool there = find_unit(a, pack, shift, index, line, per_sm, lane, u, parts);
+        if (!there && a.splits > 1 && index % a.splits == 0 && lane == 0) a.parts[index / a.splits].parts = 0;
         if (there) {
           ok = whole_warp(mbar_wait(&unit_empty[n & 1], ((n >> 1) & 1) ^ 1));  // (the first round passes at once)
           if (!ok) break;
@@ -789,14 +843,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t unit = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the first kernel's end
-  const int32_t parts = a.parts[unit];
-  if (parts < 2) return;
-  Unit u;
-  int32_t same;
-  AttentionArgs whole = a;
-  whole.splits = 1;
-  if (!find_unit(whole, pack, unit, 0, u, same)) return;
-  if (u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
+  const PartInfo u = a.parts[unit];
+  const int32_t parts = u.parts;
+  if (parts < 2 || u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
   const int row0 = blockIdx.y * kJoinRows + (SHARED ? 0 : warp * kMine);
   const int64_t first = static_cast<int64_t>(unit) * a.splits * kRows + row0;
   const float c = a.scale * kLog2e;
@@ -830,7 +879,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
   auto put = [&](int row, int r) {
     const int32_t tok = u.tok0 + row / pack, head = u.head0 + row % pack;
     if (tok >= u.n_q) return;
-    const bool any = u.reach(tok, a.causal) > 0;
+    const bool any = (a.causal ? u.len + min(0, tok + 1 - u.n_q) : u.len) > 0;
     const float scale = 1.0f / l[r];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[r][e] = any ? o[r][e] * scale : 0.0f;
@@ -932,11 +981,11 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   void* ws = nullptr;
   if (a.splits > 1) {
     const size_t rows = static_cast<size_t>(units) * a.splits * kRows;
-    const kda_status st = workspace_alloc(rows * (D * sizeof(float) + sizeof(float2)) + units * sizeof(int32_t), s, &ws);
+    const kda_status st = workspace_alloc(rows * (D * sizeof(float) + sizeof(float2)) + units * sizeof(PartInfo), s, &ws);
     if (st != KDA_OK) return st;
     a.part_out = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_out + rows * D);
-    a.parts = reinterpret_cast<int32_t*>(a.part_ml + rows);
+    a.parts = reinterpret_cast<PartInfo*>(a.part_ml + rows);
   }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
   if (e == cudaSuccess) {

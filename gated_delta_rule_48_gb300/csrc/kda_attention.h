@@ -12,6 +12,12 @@
 
 namespace kda {
 
+// A unit of rows whose keys several blocks share (kda_attention.cu).
+struct PartInfo {
+  int32_t parts;            // fewer than 2: it is not shared
+  int32_t q0, n_q, len, tok0, head0;
+};
+
 // ---- kda_attention_fwd (kda_attention.cu).  Leading dimensions in elements.
 struct AttentionArgs {
   const Bf16* q;            // [Tq, heads, d], tokens ld_q apart
@@ -30,11 +36,11 @@ struct AttentionArgs {
   int* err;
   // Few units of rows: their keys shared by several blocks, up to `splits` of them
   // (kda_attention.cu); a part's sums [unit * splits + part][256][d], each row's
-  // maximum and sum of p, and how many parts a unit has.
+  // maximum and sum of p, and each unit's rows and how many parts it has.
   int32_t splits = 1;
   float* part_out = nullptr;
   float2* part_ml = nullptr;
-  int32_t* parts = nullptr;
+  PartInfo* parts = nullptr;
 };
 // Allocates its workspace, if any: a status of its own if that fails, else `e`.
 kda_status launch_attention(const AttentionArgs& a, cudaStream_t s, cudaError_t& e);
