@@ -56,6 +56,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSlice = 32;        // positions of a slice: two halves, for a page may end between them
 constexpr int kHalf = 16;
 constexpr int kDepth = 3;         // slices of a warp in flight
+constexpr int kSoloSlices = 16;   // of a unit, on average: up to as many, a warp to a unit
 constexpr float kLowest = -1e30f; // a maximum of nothing
 constexpr float kSlack = 8.0f;    // log2 of how far p may pass 1
 constexpr float kLn2 = 0.6931471805599453f;
@@ -66,7 +67,8 @@ struct Meta {
   int32_t slot;       // of the first block's part
   int32_t seq, head, col0;
   int32_t visible;    // positions the first query reaches
-  int32_t pad[2];
+  int32_t solo;       // parts are of warps, not of blocks
+  int32_t pad;
 };
 
 template <int G, int NT>
@@ -162,7 +164,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   using S = Shape<G, NT>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_start[3];  // sequence, slices before it, all slices
+  __shared__ int64_t s_start[kWarps][2];  // of a part's first slice: the sequence, slices before it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, j = lane & 3;
   const Kv4Pages& p = a.pages;
@@ -179,7 +181,8 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   auto slices_of = [&](int64_t n) { return (len_of(n) + kSlice - 1) / kSlice; };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- sequences of no positions: zeros
+  // sequences of no positions: zeros
+  auto write_zeros = [&]() {
   for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
     if (len_of(n) > 0) continue;
     for (int e = threadIdx.x; e < a.tokens * a.heads * (S::D / 8); e += kThreads) {
@@ -192,8 +195,9 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         if (kda_guard(n * a.tokens * a.heads + e, 1, n_rows * a.heads, a.err))
           a.lse[n * a.tokens * a.heads + e] = -INFINITY;
   }
+  };
 
-  // ---- this block's part of the line
+  // ---- this block's part of the line (or the parts of its warps)
   const int64_t chunk = (a.N + kThreads - 1) / kThreads;
   const int64_t c0 = min(chunk * threadIdx.x, static_cast<int64_t>(a.N)), c1 = min(c0 + chunk, static_cast<int64_t>(a.N));
   int64_t own = 0;
@@ -216,28 +220,53 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     total += s_sum[w];
   }
   const int64_t all = total * per_seq;
-  // no more blocks than have two slices for each warp
-  const int64_t used = max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), all / (2 * kWarps)));
-  const int64_t b = blockIdx.x;
-  const int64_t part0 = b < used ? all * b / used : all, part1 = b < used ? all * (b + 1) / used : all;
-  if (threadIdx.x == 0) {
+  // Short units (up to kSoloSlices slices on average) go to single warps, each with a
+  // part of the line of its own: shared by a block's warps, most of a unit's time is
+  // spent before its first slice and behind its last.
+  const bool solo = all <= kSoloSlices * (per_seq * a.N);
+  const int workers = solo ? kWarps : 1, me = solo ? warp : 0;
+  const int64_t all_workers = static_cast<int64_t>(gridDim.x) * workers;
+  // no more parts than have two slices for each warp
+  const int64_t used = max(int64_t{1}, min(all_workers, all >> (solo ? 1 : 3)));
+  static_assert(kWarps == 4, "two slices for each warp");
+  // part n begins at all * n / used
+  const bool small = all >> 32 == 0;  // (a division of 64 bits takes some hundred instructions)
+  const int64_t share = small ? static_cast<uint32_t>(all) / static_cast<uint32_t>(used) : all / used;
+  const uint32_t over = static_cast<uint32_t>(all - share * used);
+  auto part_at = [&](int64_t n) {
+    return n < used ? share * n + over * static_cast<uint32_t>(n) / static_cast<uint32_t>(used) : all;
+  };
+  const int64_t b = static_cast<int64_t>(blockIdx.x) * workers + me;
+  const int64_t part0 = part_at(b), part1 = part_at(b + 1);
+  if (threadIdx.x < kWarps) {
     Meta none;
     none.last = -1;
-    metas[b] = none;
+    none.solo = solo;
+    metas[blockIdx.x * kWarps + threadIdx.x] = none;
   }
-  if (part0 >= part1) return;
-  if (part0 >= before * per_seq && part0 < (before + own) * per_seq) {
-    int64_t n = c0, at = before, count = slices_of(n);
-    while ((at + count) * per_seq <= part0) {
-      at += count;
-      count = slices_of(++n);
+  for (int w = 0; w < workers; ++w) {
+    const int64_t from = workers == 1 ? part0 : part_at(static_cast<int64_t>(blockIdx.x) * workers + w);
+    if (from >= before * per_seq && from < (before + own) * per_seq) {
+      int64_t n = c0, at = before, count = slices_of(n);
+      while ((at + count) * per_seq <= from) {
+        at += count;
+        count = slices_of(++n);
+      }
+      s_start[w][0] = n;
+      s_start[w][1] = at;
     }
-    s_start[0] = n;
-    s_start[1] = at;
   }
   __syncthreads();
-  int64_t seq = s_start[0], seq_first = s_start[1] * per_seq;  // the sequence's first slice of the line
+  if (part0 >= part1) {
+    write_zeros();
+    return;
+  }
+  int64_t seq = s_start[me][0], seq_first = s_start[me][1] * per_seq;  // the sequence's first slice of the line
 
+  auto work = [&](auto SOLO_c) {
+  constexpr bool SOLO = decltype(SOLO_c)::value;
+  constexpr int32_t stride = (SOLO ? 1 : kWarps) * kSlice;  // this warp's slices of a unit: first + mine0, and so on
+  const int mine0 = SOLO ? 0 : warp;
   unsigned char* const ring = smem + warp * (kDepth * S::kStage);
   const float c = a.scale * kLog2e;
   for (int64_t at = part0; at < part1;) {
@@ -246,9 +275,11 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       seq_first += slices * per_seq;
       slices = slices_of(++seq);
     }
-    const int64_t unit = (at - seq_first) / slices;  // of the sequence
+    const int64_t in_seq = at - seq_first;
+    const int64_t unit = ((in_seq | slices) >> 32) == 0  // of the sequence
+                             ? static_cast<uint32_t>(in_seq) / static_cast<uint32_t>(slices) : in_seq / slices;
     const int64_t unit_first = seq_first + unit * slices;
-    const int32_t head = static_cast<int32_t>(unit / blocks_c), col0 = static_cast<int32_t>(unit % blocks_c) * S::kCols;
+    const int32_t head = static_cast<int32_t>(unit) / blocks_c, col0 = (static_cast<int32_t>(unit) - head * blocks_c) * S::kCols;
     const int64_t first = at - unit_first, last = min(part1 - unit_first, slices);  // slices [first, last)
     const int64_t len = len_of(seq);
     const int32_t visible = static_cast<int32_t>(len) - a.tokens + 1;  // positions the first query reaches
@@ -323,9 +354,10 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       }
     }
 
-    // ---- this warp's slices: first + warp, + 4, ...
-    const int32_t mine = static_cast<int32_t>(max(int64_t{0}, (last - first - warp + kWarps - 1) / kWarps));
-    const int32_t pos0 = static_cast<int32_t>((first + warp) * kSlice);  // of the first one
+    // ---- this warp's slices: first + warp, + 4, ... (or all of them)
+    const int32_t left = static_cast<int32_t>(last - first) - mine0;
+    const int32_t mine = left <= 0 ? 0 : SOLO ? left : (left + kWarps - 1) / kWarps;
+    const int32_t pos0 = static_cast<int32_t>(first + mine0) * kSlice;  // of the first one
     const int32_t* const pages = p.table + seq * p.ld_table;
     const int32_t place = (1 << p.page_shift) - 1;  // a position's bits in its page
     const int32_t head_rows = head << p.page_shift, page_rows = p.heads << p.page_shift;
@@ -342,7 +374,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
                           of_half % kChunks * 16;
     const uint32_t to_s = smem_u32(ring) + kSlice * (S::kRow + S::kPitchV) + (of_half < kS ? 0 : S::kScaleBytes) +
                           half * (16 * kS) + 16 * (of_half % kS);
-    const int32_t stop = pos0 + mine * (kWarps * kSlice);
+    const int32_t stop = pos0 + mine * stride;
     // (the last slice's second half may lie behind the sequence's last position)
     const int32_t held = static_cast<int32_t>(len);
     auto page_of = [&](int32_t pos) -> int32_t {  // of this lane's half of a slice
@@ -491,64 +523,26 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       }
     };
 
-    constexpr int32_t kStep = kWarps * kSlice;
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(pos0 + i * kStep, page_of(pos0 + i * kStep), i * S::kStage);
-    int32_t ahead = pos0 + (kDepth - 1) * kStep, next_page = page_of(ahead);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(pos0 + i * stride, page_of(pos0 + i * stride), i * S::kStage);
+    int32_t ahead = pos0 + (kDepth - 1) * stride, next_page = page_of(ahead);
     uint32_t here = 0;  // the stage of the slice at hand
-    for (int32_t pos = pos0; pos < stop; pos += kStep) {
+    for (int32_t pos = pos0; pos < stop; pos += stride) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // this slice has come, and the one before has been read
       fetch(ahead, next_page, here == 0 ? (kDepth - 1) * S::kStage : here - S::kStage);
-      ahead += kStep;
+      ahead += stride;
       next_page = page_of(ahead);
       if (pos + kSlice > visible) process(ring + here, pos, std::true_type{});
       else process(ring + here, pos, std::false_type{});
       here = here == (kDepth - 1) * S::kStage ? 0 : here + S::kStage;
     }
 
-    // ---- the warps' results together
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    float* const parts = reinterpret_cast<float*>(smem);  // [warp][column][D + 4]: o, m, l
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int w = 4; w < 32; w *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
-        float* to = parts + (warp * S::kCols + 8 * t + 2 * j + e) * (S::D + 4);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {  // channels 32 g + 4 r + 0..3
-          *reinterpret_cast<float4*>(to + 32 * g + 4 * r) =
-              make_float4(o[2 * g][t][e], o[2 * g][t][e + 2], o[2 * g + 1][t][e], o[2 * g + 1][t][e + 2]);
-        }
-        if (r == 0) {
-          to[S::D] = m[t][e];
-          to[S::D + 1] = l[t][e];
-        }
-      }
-    __syncthreads();
     const bool complete = first == 0 && last == slices;
     const int slot = at == part0 ? 0 : 1;
     float* const record = records + (b * 2 + slot) * S::kRecord;
-    for (int e = threadIdx.x; e < S::kCols * (S::D / 4); e += kThreads) {
-      const int col = e / (S::D / 4), ch = e % (S::D / 4) * 4;
-      float top = kLowest, sum = 0.0f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[(w * S::kCols + col) * (S::D + 4) + S::D]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* from = parts + (w * S::kCols + col) * (S::D + 4);
-        const float keep = ex2(from[S::D] - top);
-        const float4 x = *reinterpret_cast<const float4*>(from + ch);
-        sum = fmaf(from[S::D + 1], keep, sum);
-        v.x = fmaf(x.x, keep, v.x);
-        v.y = fmaf(x.y, keep, v.y);
-        v.z = fmaf(x.z, keep, v.z);
-        v.w = fmaf(x.w, keep, v.w);
-      }
+    // four channels of a column: to the output, or to the part's record
+    auto put = [&](int col, int ch, const float4& v, float top, float sum) {
       if (complete) {
         const int g_col = col0 + col;
         if (g_col < cols) {
@@ -571,8 +565,64 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
           record[S::kCols * S::D + 2 * col + 1] = sum;
         }
       }
+    };
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 4; w < 32; w *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
+    if constexpr (SOLO) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < G; ++g)  // channels 32 g + 4 r + 0..3
+            put(8 * t + 2 * j + e, 32 * g + 4 * r,
+                make_float4(o[2 * g][t][e], o[2 * g][t][e + 2], o[2 * g + 1][t][e], o[2 * g + 1][t][e + 2]), m[t][e],
+                l[t][e]);
+    } else {
+    // ---- the warps' results together
+    __syncthreads();
+    float* const parts = reinterpret_cast<float*>(smem);  // [warp][column][D + 4]: o, m, l
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* to = parts + (warp * S::kCols + 8 * t + 2 * j + e) * (S::D + 4);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          *reinterpret_cast<float4*>(to + 32 * g + 4 * r) =
+              make_float4(o[2 * g][t][e], o[2 * g][t][e + 2], o[2 * g + 1][t][e], o[2 * g + 1][t][e + 2]);
+        if (r == 0) {
+          to[S::D] = m[t][e];
+          to[S::D + 1] = l[t][e];
+        }
+      }
+    __syncthreads();
+    for (int e = threadIdx.x; e < S::kCols * (S::D / 4); e += kThreads) {
+      const int col = e / (S::D / 4), ch = e % (S::D / 4) * 4;
+      float top = kLowest, sum = 0.0f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts[(w * S::kCols + col) * (S::D + 4) + S::D]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* from = parts + (w * S::kCols + col) * (S::D + 4);
+        const float keep = ex2(from[S::D] - top);
+        const float4 x = *reinterpret_cast<const float4*>(from + ch);
+        sum = fmaf(from[S::D + 1], keep, sum);
+        v.x = fmaf(x.x, keep, v.x);
+        v.y = fmaf(x.y, keep, v.y);
+        v.z = fmaf(x.z, keep, v.z);
+        v.w = fmaf(x.w, keep, v.w);
+      }
+      put(col, ch, v, top, sum);
     }
-    if (!complete && first == 0 && threadIdx.x == 0) {  // this block has the unit's first part
+    }
+    if (!complete && first == 0 && (SOLO ? lane : static_cast<int>(threadIdx.x)) == 0) {  // the unit's first part
       Meta mt;
       mt.last = static_cast<int32_t>(((unit_first + slices) * used - 1) / all);
       mt.slot = slot;
@@ -580,31 +630,34 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       mt.head = head;
       mt.col0 = col0;
       mt.visible = visible;
-      metas[b] = mt;
+      mt.solo = SOLO;
+      metas[SOLO ? b : b * kWarps] = mt;
     }
-    __syncthreads();  // the ring is filled again
+    if (SOLO) __syncwarp();
+    else __syncthreads();  // the ring is filled again
     at = unit_first + last;
   }
+  };
+  if (solo) work(std::true_type{});
+  else work(std::false_type{});
+  write_zeros();
 }
 
-// The parts of units that several blocks worked on: block b those of the unit that
-// begins in block b's part of the line and goes on behind it.  Four channels of a
-// column to a thread, several sets of threads share the parts.
+// The parts of units that several blocks (or warps) worked on: block b those of the
+// unit that begins in block b's part of the line (or in those of its warps) and goes
+// on behind it.  Four channels of a column to a thread.
 constexpr int kCombineThreads = 1024;
 
 template <int G, int NT>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Kv4AttentionArgs a, const float* records, const Meta* metas) {
+__global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4AttentionArgs a, const float* records, const Meta* metas) {
   using S = Shape<G, NT>;
   constexpr int kItems = S::kCols * (S::D / 4), kSets = kCombineThreads / kItems;
   __shared__ float4 s_v[kSets - 1][kItems];
   __shared__ float2 s_ml[kSets - 1][kItems];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the first kernel's end
-  const Meta mt = metas[blockIdx.x];
-  if (mt.last < 0) return;
   const int group = a.heads / a.pages.heads, cols = a.tokens * group;
   const int item = threadIdx.x % kItems, set = threadIdx.x / kItems;
-  const int col = item / (S::D / 4), ch = item % (S::D / 4) * 4, g_col = mt.col0 + col;
-  const int b0 = blockIdx.x;
+  const int col = item / (S::D / 4), ch = item % (S::D / 4) * 4;
   float top = kLowest, sum = 0.0f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float m2, float l2, const float4& x) {
@@ -616,31 +669,53 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Kv4AttentionAr
     v.z = fmaf(x.z, k1, v.z * k0);
     v.w = fmaf(x.w, k1, v.w * k0);
   };
+  auto add_parts = [&](const Meta& mt, int b0, int from, int by) {
+    top = kLowest;
+    sum = 0.0f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int b = b0 + set; b <= mt.last; b += kSets) {
-    const float* record = records + (static_cast<int64_t>(b) * 2 + (b == b0 ? mt.slot : 0)) * S::kRecord;
-    const float2 ml = *reinterpret_cast<const float2*>(record + S::kCols * S::D + 2 * col);
-    add(ml.x, ml.y, *reinterpret_cast<const float4*>(record + col * S::D + ch));
-  }
-  if (set > 0) {
-    s_v[set - 1][item] = v;
-    s_ml[set - 1][item] = make_float2(top, sum);
-  }
-  __syncthreads();
-  if (set != 0 || g_col >= cols) return;
+    for (int b = b0 + from; b <= mt.last; b += by) {
+      const float* record = records + (static_cast<int64_t>(b) * 2 + (b == b0 ? mt.slot : 0)) * S::kRecord;
+      const float2 ml = *reinterpret_cast<const float2*>(record + S::kCols * S::D + 2 * col);
+      add(ml.x, ml.y, *reinterpret_cast<const float4*>(record + col * S::D + ch));
+    }
+  };
+  auto put = [&](const Meta& mt) {
+    const int g_col = mt.col0 + col;
+    if (g_col >= cols) return;
+    const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
+    const int64_t row = static_cast<int64_t>(mt.seq) * a.tokens + g_col / group;
+    const int32_t h = mt.head * group + g_col % group;
+    const bool any = mt.visible + g_col / group > 0;
+    const float scale = 64.0f / sum;  // (codes were read as n 2^-6)
+    const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
+    if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
+      *reinterpret_cast<uint2*>(a.out + to) =
+          any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale)) : make_uint2(0, 0);
+    if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
+      a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+  };
+  const Meta first = metas[blockIdx.x * kWarps];
+  if (!first.solo) {  // (of a block: all sets of threads share the parts)
+    if (first.last < 0) return;
+    add_parts(first, blockIdx.x, set, kSets);
+    if (set > 0) {
+      s_v[set - 1][item] = v;
+      s_ml[set - 1][item] = make_float2(top, sum);
+    }
+    __syncthreads();
+    if (set != 0) return;
 #pragma unroll
-  for (int i = 0; i < kSets - 1; ++i) add(s_ml[i][item].x, s_ml[i][item].y, s_v[i][item]);
-  const int64_t n_rows = static_cast<int64_t>(a.N) * a.tokens;
-  const int64_t row = static_cast<int64_t>(mt.seq) * a.tokens + g_col / group;
-  const int32_t h = mt.head * group + g_col % group;
-  const bool any = mt.visible + g_col / group > 0;
-  const float scale = 64.0f / sum;  // (codes were read as n 2^-6)
-  const int64_t to = row * a.ld_out + static_cast<int64_t>(h) * S::D + ch;
-  if (kda_guard(to, 4, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
-    *reinterpret_cast<uint2*>(a.out + to) =
-        any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale)) : make_uint2(0, 0);
-  if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
-    a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+    for (int i = 0; i < kSets - 1; ++i) add(s_ml[i][item].x, s_ml[i][item].y, s_v[i][item]);
+    put(first);
+    return;
+  }
+  for (int w = set; w < kWarps; w += kSets) {  // (of its warps: one to a set)
+    const Meta mt = metas[blockIdx.x * kWarps + w];
+    if (mt.last < 0) continue;
+    add_parts(mt, blockIdx.x * kWarps + w, 0, 1);
+    put(mt);
+  }
 }
 
 template <int G, int NT>
@@ -655,8 +730,8 @@ kda_status run(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   }();
   const int blocks = a.sm_count * std::max(resident, 1);
   void* ws = nullptr;
-  const size_t records = sizeof(float) * 2 * blocks * S::kRecord;
-  const kda_status st = workspace_alloc(records + sizeof(Meta) * blocks, s, &ws);
+  const size_t records = sizeof(float) * 2 * blocks * kWarps * S::kRecord;
+  const kda_status st = workspace_alloc(records + sizeof(Meta) * blocks * kWarps, s, &ws);
   if (st != KDA_OK) return st;
   float* rec = static_cast<float*>(ws);
   Meta* metas = reinterpret_cast<Meta*>(static_cast<unsigned char*>(ws) + records);

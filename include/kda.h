@@ -715,7 +715,7 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * sequence's rows are then unspecified.  n_heads is a multiple of the cache's
  * n_kv_heads.  scale is positive and finite.  N = 0 or n_tokens = 0 are no-ops.
  * Long sequences are shared by several blocks; that takes a workspace of up to
- * 13 MB, allocated and freed stream-ordered on `stream`.
+ * 31 MB, allocated and freed stream-ordered on `stream`.
  */
 kda_status kda_kv4_attention(const void *q, int64_t ld_q,
                              const kda_kv4_cache *cache,
