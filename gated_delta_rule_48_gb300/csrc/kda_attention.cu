@@ -48,6 +48,9 @@ static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
 constexpr int kPartTiles = 4;            // the least of a unit's part of the keys
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
 constexpr float kSlack = 8.0f;           // log2 of how far p may pass 1
+// From here on what c m loses by its rounding counts (from 2^31 on p would be 0 or
+// infinite): m is taken off the scores before c is multiplied in.
+constexpr float kLarge = 1048576.0f;
 
 template <int D>
 struct Shape {
@@ -679,6 +682,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       // all of the tile's rows reach these tiles whole
       const int32_t whole = u.reach(u.tok0 + i * (tokens / 2), a.causal) / kTile;
       float m = -INFINITY, l = 0.0f;
+      bool large = false;  // a maximum of the warp's rows: |c m| > kLarge
       for (int32_t j = 0; j < tiles; ++j) {
         ok = whole_warp(mbar_wait(&s_full[i], tile & 1));
         if (!ok) break;
@@ -711,10 +715,12 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         }
         if (j == 0) {
           m = most;
+          large = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * c) > kLarge);
         } else if (__any_sync(0xffffffffu, (most - m) * c > kSlack)) {
           const float next = fmaxf(m, most);
           const float keep = next == -INFINITY ? 1.0f : ex2((m - next) * c);
           m = next;
+          large = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * c) > kLarge);
           l *= keep;
 #pragma unroll 1
           for (int k = 0; k < D; k += 32) {
@@ -727,7 +733,13 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
           tmem_wait_st();
         }
         ++tile;
-        const float base = m == -INFINITY ? 0.0f : m * c;
+        float base = m == -INFINITY ? 0.0f : m * c;
+        if (large) {
+          const float less = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int k = 0; k < kTile; ++k) s[k] -= less;
+          base = 0.0f;
+        }
         const f32x2 cc = pack2(c, c), less = pack2(-base, -base);
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
         auto hand_over = [&](int part) {
@@ -845,7 +857,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the first kernel's end
   const PartInfo u = a.parts[unit];
   const int32_t parts = u.parts;
-  if (parts < 2 || u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
+  if (parts < 2) return;
+  // (a unit that was not reached because a wait ran out has anything here)
+  if (parts > a.splits || u.q0 < 0 || u.n_q > a.Tq - u.q0 || u.tok0 < 0 || u.head0 < 0 || u.head0 > a.heads - pack) return;
+  if (u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
   const int row0 = blockIdx.y * kJoinRows + (SHARED ? 0 : warp * kMine);
   const int64_t first = static_cast<int64_t>(unit) * a.splits * kRows + row0;
   const float c = a.scale * kLog2e;
@@ -859,8 +874,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
     for (int e = 0; e < kPer; ++e) o[r][e] = 0.0f;
   }
   auto add = [&](int r, const float2& ml, const float (&v)[kPer]) {
-    const float next = fmaxf(m[r], ml.x), base = next == -INFINITY ? 0.0f : next * c;
-    const float keep = ex2(fmaf(m[r], c, -base)), w = ex2(fmaf(ml.x, c, -base));
+    const float next = fmaxf(m[r], ml.x), base = next == -INFINITY ? 0.0f : next;
+    const float keep = ex2((m[r] - base) * c), w = ex2((ml.x - base) * c);
     m[r] = next;
     l[r] = fmaf(ml.y, w, l[r] * keep);
 #pragma unroll

@@ -21,7 +21,8 @@ kda_status check_heads(int32_t heads, int32_t kv_heads, int32_t d) {
 }
 
 kda_status check_scale(float scale) {
-  if (!(scale > 0.0f) || std::isinf(scale))
+  // (scale log2 e is a number of 32 bits too)
+  if (!(scale > 0.0f) || std::isinf(scale * 1.5f))
     return bad(KDA_ERR_INVALID_ARGUMENT, "scale=%g is not positive and finite", scale);
   return KDA_OK;
 }
@@ -57,6 +58,9 @@ kda_status check_cache(const kda_kv4_cache* c, const int32_t* table, int64_t ld_
   const int32_t size = c->page_size;
   if (size < 16 || size > 65536 || (size & (size - 1)) != 0)
     return bad(KDA_ERR_UNSUPPORTED, "page_size=%d is not a power of two from 16 to 65536", size);
+  if (static_cast<int64_t>(c->n_kv_heads) * size > 1 << 30 ||
+      static_cast<int64_t>(c->n_pages) * c->n_kv_heads > (1LL << 48) / size)
+    return bad(KDA_ERR_UNSUPPORTED, "n_pages=%d of n_kv_heads=%d and page_size=%d", c->n_pages, c->n_kv_heads, size);
   const struct { const void* p; const char* n; } arrays[] = {{c->k_codes, "k_codes"},
                                                              {c->k_scales, "k_scales"},
                                                              {c->v_codes, "v_codes"},

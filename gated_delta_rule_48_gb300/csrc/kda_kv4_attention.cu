@@ -57,8 +57,11 @@ constexpr int kSlice = 32;        // positions of a slice: two halves, for a pag
 constexpr int kHalf = 16;
 constexpr int kDepth = 3;         // slices of a warp in flight
 constexpr int kSoloSlices = 16;   // of a unit, on average: up to as many, a warp to a unit
-constexpr float kLowest = -1e30f; // a maximum of nothing
+constexpr float kLowest = -3e38f; // a maximum of nothing (-infinity less itself is NaN)
 constexpr float kSlack = 8.0f;    // log2 of how far p may pass 1
+// From here on a maximum's rounding counts (from 2^31 on p would be 0 or infinite):
+// the products it is taken from are rounded as it was.
+constexpr float kLarge = 1048576.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Where a block's part of a unit lies that is not whole.
@@ -183,18 +186,17 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // sequences of no positions: zeros
   auto write_zeros = [&]() {
-  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
-    if (len_of(n) > 0) continue;
-    for (int e = threadIdx.x; e < a.tokens * a.heads * (S::D / 8); e += kThreads) {
-      const int64_t at = (n * a.tokens + e / (a.heads * (S::D / 8))) * a.ld_out + e % (a.heads * (S::D / 8)) * 8;
-      if (kda_guard(at, 8, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
-        *reinterpret_cast<uint4*>(a.out + at) = make_uint4(0, 0, 0, 0);
+    const int width = a.heads * (S::D / 8);  // pieces of 16 bytes of a token
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+      if (len_of(n) > 0) continue;
+      for (int64_t row = n * a.tokens; row < (n + 1) * a.tokens; ++row)
+        for (int e = threadIdx.x; e < width; e += kThreads)
+          if (kda_guard(row * a.ld_out + 8 * e, 8, (n_rows - 1) * a.ld_out + a.heads * S::D, a.err))
+            *reinterpret_cast<uint4*>(a.out + row * a.ld_out + 8 * e) = make_uint4(0, 0, 0, 0);
+      if (!a.lse) continue;
+      for (int64_t e = n * a.tokens * a.heads + threadIdx.x; e < (n + 1) * a.tokens * a.heads; e += kThreads)
+        if (kda_guard(e, 1, n_rows * a.heads, a.err)) a.lse[e] = -INFINITY;
     }
-    if (a.lse)
-      for (int e = threadIdx.x; e < a.tokens * a.heads; e += kThreads)
-        if (kda_guard(n * a.tokens * a.heads + e, 1, n_rows * a.heads, a.err))
-          a.lse[n * a.tokens * a.heads + e] = -INFINITY;
-  }
   };
 
   // ---- this block's part of the line (or the parts of its warps)
@@ -310,10 +312,11 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       // 2^k brings the largest magnitude into [2^14, 2^15); an infinity or NaN makes the row NaN
       const int k = min(141 - static_cast<int>(top >> 7), 126);
       const float up = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-      // 2^-k and the 2^24 of codes read as f16
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23) * 0x1p24f;
-      cc[t][0] = c * __shfl_sync(0xffffffffu, down, 8 * j);
-      cc[t][1] = c * __shfl_sync(0xffffffffu, down, 8 * j + 4);
+      // 2^-k, the 2^24 of codes read as f16, and c: never 0, which times a hidden score's
+      // infinity would be NaN (queries of zeros and a tiny scale come to it)
+      const float down = fmaxf(c * (__uint_as_float(static_cast<uint32_t>(127 - k) << 23) * 0x1p24f), 0x1p-126f);
+      cc[t][0] = __shfl_sync(0xffffffffu, down, 8 * j);
+      cc[t][1] = __shfl_sync(0xffffffffu, down, 8 * j + 4);
       offset[t][0] = offset[t][1] = 0;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -343,6 +346,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         reach[t][e] = visible + (col0 + 8 * t + 2 * j + e) / group - r;
     }
     float o[2 * G][NT][4], m[NT][2], l[NT][2], limit[NT][2];
+    bool large = false;  // a column's |m| > kLarge
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -453,6 +457,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
             up = up || x[h][t][e] > limit[t][e & 1];
           }
       if (__any_sync(0xffffffffu, up)) {
+        bool any_large = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -463,6 +468,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
             top = fmaxf(m[t][e], top);
             const float keep = ex2(m[t][e] - top);
             m[t][e] = top;
+            any_large = any_large || fabsf(top) > kLarge;
             limit[t][e] = (top + kSlack) / cc[t][e];
             l[t][e] *= keep;
 #pragma unroll
@@ -471,14 +477,25 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
               o[g][t][e + 2] *= keep;
             }
           }
+        large = __any_sync(0xffffffffu, any_large);
       }
+      auto less = [&](auto f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][t][e] = f(x[h][t][e], cc[t][e & 1], m[t][e & 1]);
+      };
+      if (large) less([](float x, float cc, float m) { return __fsub_rn(__fmul_rn(x, cc), m); });
+      else less([](float x, float cc, float m) { return fmaf(x, cc, -m); });
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[h][t][e] = ex2(fmaf(x[h][t][e], cc[t][e & 1], -m[t][e & 1]));
+            x[h][t][e] = ex2(x[h][t][e]);
             l[t][e & 1] += x[h][t][e];
           }
       // ---- values

@@ -510,6 +510,8 @@ PyObject* attention_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (k.dim() != q.dim() || kh.d != qh.d)
       refuse("k must have q's dimensions and head size, got %s", shape_of(k.sizes()).c_str());
     same_shape(v, k.sizes(), "v");
+    if (q.dim() > 3 && k.size(0) != q.size(0))
+      refuse("q has %lld sequences, k %lld", (long long)q.size(0), (long long)k.size(0));
     const Tensor& cq = tensor(a[3], "cu_seqlens_q", true);
     const Tensor& ck = tensor(a[4], "cu_seqlens_k", true);
     if (ck.defined() && !cq.defined()) refuse("cu_seqlens_k is given but cu_seqlens_q is not");

@@ -656,7 +656,8 @@ kda_status kda_attention_fwd(const void *q, int64_t ld_q, const void *k,
  * end) of 32-bit word j G + g of a row of k_codes is the code of channel
  * 32 g + 8 j + i, and nibble i of 16-bit word r G + g of a row of v_codes that
  * of channel 32 g + 4 r + i.
- * page_size is a power of two from 16 to 65536, d is 64 or 128.
+ * page_size is a power of two from 16 to 65536, d is 64 or 128, page_size *
+ * n_kv_heads at most 2^30, and n_pages times that at most 2^48.
  */
 typedef struct {
     void *k_codes, *k_scales, *v_codes, *v_scales;
@@ -713,7 +714,9 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * q and out start on a 16-byte boundary at every token.  A position without a
  * valid page (as in kda_kv4_write) is reported by kda_get_device_error, and its
  * sequence's rows are then unspecified.  n_heads is a multiple of the cache's
- * n_kv_heads.  scale is positive and finite.  N = 0 or n_tokens = 0 are no-ops.
+ * n_kv_heads.  scale is positive and finite; q and scale * q are below 2^112 in
+ * magnitude (else the query's rows are unspecified).  N = 0 or n_tokens = 0 are
+ * no-ops.
  * Long sequences are shared by several blocks; that takes a workspace of up to
  * 31 MB, allocated and freed stream-ordered on `stream`.
  */

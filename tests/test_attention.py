@@ -66,6 +66,26 @@ def test_sharp_and_flat_scores(std, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[300, 70], [5000]])
+def test_scores_beyond_whole_numbers_of_32_bits(lens):
+    """Scores of 2^24 to 2^100: one key has all of a row.  Keys of one value in all channels and
+    queries of signs, so that scores are multiples of powers of two, summed exactly."""
+    g = gen(21)
+    rows = 50
+    for power in (14, 20, 40, 100):
+        q = torch.where(torch.rand(rows, 4, 128, generator=g, device=DEV) < 0.5, -1.0, 1.0).bfloat16()
+        k = torch.zeros(sum(lens), 2, 128, dtype=torch.bfloat16, device=DEV)
+        at = torch.randperm(sum(lens), generator=torch.Generator().manual_seed(3)).to(DEV)
+        k[:, :, 0] = (2.0 ** power * (at % 251 - 125))[:, None].bfloat16()
+        v = randn(g, sum(lens), 2, 128, dtype=torch.bfloat16)
+        q_lens = [rows - 10, 10] if len(lens) > 1 else [rows]
+        out, lse = kb.kda_attention_fwd(q, k, v, cu_of(q_lens), cu_of(lens), scale=1.0, want_lse=True)
+        o, l, m, _ = reference(q, k, v, q_lens, lens, 1.0)
+        # (exact scores, whose differences are 0 or at least 2^power)
+        check(out, lse, (o, l, m, torch.zeros_like(l)), 128)
+
+
+@pytest.mark.gpu
 def test_a_long_sequence():
     q, k, v = qkv(gen(5), 20, 5000, 8, 1, 128)
     run(q, k, v, [20], [5000])
@@ -236,6 +256,54 @@ def test_streams_graphs_and_threads():
 
 
 @pytest.mark.gpu
+def test_shared_keys_in_graphs_and_threads():
+    """The calls that take a workspace: two captured graphs replayed side by side, two threads."""
+    q, k, v = qkv(gen(19), 40, 6000, 8, 1, 128)
+    cq, ck = cu_of([30, 10]), cu_of([4000, 2000])
+    graphs, outs, streams = [], [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        outs.append((torch.empty_like(q), torch.empty(40, 8, device=DEV)))
+        with torch.cuda.graph(graphs[-1]):
+            kb.kda_attention_fwd(q, k, v, cq, ck, out=outs[-1][0], lse=outs[-1][1])
+        streams.append(torch.cuda.Stream())
+    for q_lens, k_lens in (([30, 10], [4000, 2000]), ([40, 0], [0, 6000]), ([1, 39], [5999, 1])):
+        cq.copy_(cu_of(q_lens))
+        ck.copy_(cu_of(k_lens))
+        want = kb.kda_attention_fwd(q, k, v, cq, ck, want_lse=True)
+        check(*want, reference(q, k, v, q_lens, k_lens, 128 ** -0.5), 128)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for graph, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    results = [None] * 2
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                results[i] = kb.kda_attention_fwd(q, k, v, cq, ck)[0]
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert torch.equal(results[0], want[0]) and torch.equal(results[1], want[0])
+    assert kb.kda_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_batches_of_unlike_numbers_are_refused():
+    q, k = (torch.zeros(b, 8, 2, 64, dtype=torch.bfloat16, device=DEV) for b in (2, 4))
+    with pytest.raises(kb.KdaError, match="q has 2 sequences, k 4"):
+        kb.kda_attention_fwd(q, k, k)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("cu", [[0, 5, 4, 10], [1, 5, 8, 10], [0, 5, 8, 9], [0, 5, 8, 4000], [0, -7, 8, 10]])
 def test_malformed_cu_seqlens_are_reported(cu):
     q, k, v = qkv(gen(16), 10, 10, 2, 1, 64)
@@ -309,6 +377,10 @@ def call(**over):
 def test_refusals(over, word):
     assert call(**over) == 1
     assert word in kb.load().kda_last_error_message()
+
+
+def test_a_scale_that_overflows_is_refused():
+    assert call(scale=3e38) == 1 and b"scale" in kb.load().kda_last_error_message()
 
 
 def test_unsupported_and_empty():

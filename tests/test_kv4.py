@@ -230,6 +230,35 @@ def test_sharp_and_flat_scores(std, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("size,scale", [(0.0, 1e-20), (0.0, 1e-38), (2.0 ** -120, 1e-20), (2.0 ** 105, None)])
+def test_queries_of_zeros_and_of_extreme_sizes(size, scale):
+    lens = [40, 3, 700]
+    cache, table = filled(lens, 16, 2, 128)
+    q = randn(gen(3), 3, 2, 4, 128, dtype=torch.bfloat16) * size
+    q[:, 1, 0] = 0
+    out, lse = kb.kda_kv4_attention(q, cache, table, ints(*lens), want_lse=True, scale=scale)
+    check(out, lse, over_cache(q, cache, table, lens, 128 ** -0.5 if scale is None else scale), 128)
+
+
+@pytest.mark.gpu
+def test_short_sequences_in_graphs():
+    """Units of one warp each, replayed with lengths that make them the whole block's, and back."""
+    cache, table = filled([900, 60, 700, 50], 16, 2, 128)
+    q = randn(gen(5), 4, 2, 8, 128, dtype=torch.bfloat16)
+    sl = ints(30, 60, 1, 50)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    with torch.cuda.graph(graph):
+        kb.kda_kv4_attention(q, cache, table, sl, out=out)
+    for lens in ([30, 60, 1, 50], [900, 60, 700, 50], [0, 0, 0, 1], [0, 0, 0, 0], [900, 0, 0, 0]):
+        sl.copy_(ints(*lens))
+        out.fill_(7.0)
+        graph.replay()
+        ref = over_cache(q, cache, table, lens, 128 ** -0.5)
+        check(out, None, ref, 128)
+    assert kb.kda_get_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_lengths_below_zero_count_as_none():
     cache, table = filled([20, 20], 16, 2, 64)
     q = randn(gen(1), 2, 4, 64, dtype=torch.bfloat16)
@@ -453,3 +482,10 @@ def test_unsupported_and_empty(name, base):
     for over in (dict(d=96), dict(d=256), dict(page_size=8), dict(page_size=48), dict(page_size=1 << 17)):
         assert call(name, base, over) == 2
     assert call(name, base, dict(N=0, T=0) if base is SPAN else dict(N=0)) == 0
+
+
+@pytest.mark.parametrize("name,base", [("kda_kv4_write", SPAN), ("kda_kv4_read", SPAN), ("kda_kv4_attention", ATTN)])
+def test_caches_whose_rows_could_not_be_counted_are_refused(name, base):
+    for over in (dict(n_kv_heads=32768, page_size=65536), dict(n_kv_heads=16384, page_size=65536, n_pages=(1 << 18) + 1)):
+        assert call(name, base, over) == 2
+        assert b"n_kv_heads=" in kb.load().kda_last_error_message()
