@@ -7,14 +7,29 @@
 // maximum passes m by more than 2^8 (in p), m moves up and o and l are scaled;
 // below that p only grows, which costs bf16 and 32 bits no precision.
 //
-// A block takes 256 rows of queries, as two tiles of 128 (tensor memory's lanes),
-// and goes over its keys 128 at a time.  Rows are tokens x query heads of one key
-// head (as many as a power of two divides the group): heads of a group share the
-// keys' tiles, and short sequences fill the rows.  Both products run on tcgen05:
-// S = Q K^T into tensor memory; four warps per tile, a row to a thread, turn S
-// into P in bf16 over it; O += P V with P read from tensor memory.  While one
-// tile's softmax runs, the other's products do.  One warp issues the copies (TMA),
-// one the products.
+// A unit of work is 256 rows of queries, as two tiles of 128 (tensor memory's lanes),
+// over their keys, 128 at a time.  Rows are tokens x query heads of one key head (as
+// many as a power of two divides the group): heads of a group share the keys' tiles,
+// and short sequences fill the rows.  Both products run on tcgen05: S = Q K^T into
+// tensor memory; four warps per tile, a row to a thread, turn S into P in bf16 over it;
+// O += P V with P read from tensor memory.  One warp finds units and issues the copies
+// (TMA), one per tile its products (a single one for both had to wait for each tile's
+// softmax before it could look after the other: 199 us instead of 177 for 128 tiles of
+// keys on every SM), one looks through V (below).
+//
+// A block stays on its SM and asks for further units (cluster launch control), so that
+// one unit's first copies run beside the last one's output.  Units go out with the most
+// keys first.  Few units are cut along the keys, up to eight blocks for each SM, and a
+// second launch joins the parts (32 queries over 65,536 keys, 8 x 128 channels: 0.7 ms
+// whole, 37 us cut).
+//
+// Bound: for long sequences the products and the softmax beside them.  Two tiles by
+// 128 keys are 2048 cycles of products (d = 128); the tensor pipe is busy 84 % of a
+// full wave's time, at 1.56 to 1.7 PFLOP/s of 1.9 (32,768 causal tokens of 16 heads:
+// 2.6 to 2.8 ms, at the power limit).  With d = 64 it is the exponentials: 16 a cycle
+// and SM, 128 x 256 of them to 1024 cycles of products.  For short ones it is the units'
+// ends: 4 x 4096 tokens of 32 heads 410 us (1.33 PFLOP/s), 100 tokens 10.6 us, most of it
+// the way from the launch to the first product and from the last one to the output.
 //
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
 // type); the sum l is of the unrounded p, in 32 bits.
@@ -682,7 +697,6 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       // all of the tile's rows reach these tiles whole
       const int32_t whole = u.reach(u.tok0 + i * (tokens / 2), a.causal) / kTile;
       float m = -INFINITY, l = 0.0f;
-      bool large = false;  // a maximum of the warp's rows: |c m| > kLarge
       for (int32_t j = 0; j < tiles; ++j) {
         ok = whole_warp(mbar_wait(&s_full[i], tile & 1));
         if (!ok) break;
@@ -713,33 +727,33 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
           if (!ok) break;
           tc_fence_after();
         }
-        if (j == 0) {
-          m = most;
-          large = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * c) > kLarge);
-        } else if (__any_sync(0xffffffffu, (most - m) * c > kSlack)) {
+        if (j == 0) m = most;
+        float base = m == -INFINITY ? 0.0f : m * c;
+        if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge)) {
           const float next = fmaxf(m, most);
-          const float keep = next == -INFINITY ? 1.0f : ex2((m - next) * c);
-          m = next;
-          large = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * c) > kLarge);
-          l *= keep;
+          if (j > 0 && __any_sync(0xffffffffu, next != m)) {
+            const float keep = next == -INFINITY ? 1.0f : ex2((m - next) * c);
+            l *= keep;
 #pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            float o[32];
-            tmem_part(t_o + k, o);
+            for (int k = 0; k < D; k += 32) {
+              float o[32];
+              tmem_part(t_o + k, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= keep;
-            tmem_st32(t_o + k, o);
+              for (int e = 0; e < 32; ++e) o[e] *= keep;
+              tmem_st32(t_o + k, o);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+          m = next;
+          base = m == -INFINITY ? 0.0f : m * c;
+          if (__any_sync(0xffffffffu, fabsf(base) > kLarge)) {
+            const float less = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) s[k] -= less;
+            base = 0.0f;
+          }
         }
         ++tile;
-        float base = m == -INFINITY ? 0.0f : m * c;
-        if (large) {
-          const float less = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-          for (int k = 0; k < kTile; ++k) s[k] -= less;
-          base = 0.0f;
-        }
         const f32x2 cc = pack2(c, c), less = pack2(-base, -base);
         f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
         auto hand_over = [&](int part) {

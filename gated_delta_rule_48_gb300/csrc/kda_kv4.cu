@@ -4,7 +4,10 @@
 //   s = bf16(max(max |x|, 2^-64) / 7) over 32 channels,  n = x / s rounded half
 //   to even, stored as n + 8;  read back: bf16(n s)
 //
-// Bound: bytes (2 read and 0.5625 written per value, or the reverse).  Four
+// Bound: bytes (2 read and 0.5625 written per value, or the reverse): 65,536 tokens
+// of 8 x 128 keys and values are read back in 57 us, 6.0 TB/s; 16,384
+// are written and read back in 39 us, 4.4 TB/s (partly from L2); 256 in 2.6 and 2.8,
+// latencies.  (Written with a division per value: twice the time.)  Four
 // lanes take a token and head: lane j reads channels 8 j .. 8 j + 7 of every
 // group, 16 bytes at a time, and ends up with 16 bytes of codes that lie side by
 // side; a group's maximum is that of its four lanes.
