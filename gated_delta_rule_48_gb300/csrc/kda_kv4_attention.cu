@@ -41,8 +41,10 @@
 // Measured, 8 key heads of 128 channels: 256 sequences of 4096 positions on average
 // and 32 query heads 244 us, 5.0 TB/s (73 % of a copy; issue slots 57 %, the ALU pipe
 // 50 %: about 300 instructions for 16 positions); one of 131,072 45 us, 3.4 TB/s, of
-// which some 15 are launches, first copies and the combination; 16 columns instead of 8
-// 119 us instead of 75 (64 x 4096): the products, the softmax and their registers.
+// which some 15 are launches, first copies and the combination; 16 columns instead
+// of 8 107 us instead of 75 (64 x 4096): the products, the softmax and their registers.
+// The next slice's scores before this one's values, so that one chain covers the
+// other, were slower (253 us instead of 243): its copies have a slice less of time.
 #include <string.h>
 
 #include <cmath>
@@ -166,8 +168,10 @@ __device__ __forceinline__ float half_of(uint32_t pair, int i) {
   return __uint_as_float(i ? pair & 0xffff0000u : pair << 16);
 }
 
+// (16 columns at three blocks an SM spill 0.6 KB a thread: 64 x 4096 with a draft of 4 took
+// 122 us instead of 107.)
 template <int G, int NT>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   using S = Shape<G, NT>;
   extern __shared__ __align__(128) unsigned char smem[];

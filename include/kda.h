@@ -718,7 +718,7 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * magnitude (else the query's rows are unspecified).  N = 0 or n_tokens = 0 are
  * no-ops.
  * Long sequences are shared by several blocks; that takes a workspace of up to
- * 31 MB, allocated and freed stream-ordered on `stream`.
+ * 21 MB, allocated and freed stream-ordered on `stream`.
  */
 kda_status kda_kv4_attention(const void *q, int64_t ld_q,
                              const kda_kv4_cache *cache,

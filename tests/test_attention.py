@@ -107,6 +107,28 @@ def test_keys_shared_by_several_blocks(q_lens, k_lens, causal, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads", [96, 128, 192, 256])
+def test_large_groups(heads):
+    """Few tokens to a tile, down to one; groups of more heads than a tile has rows."""
+    lens = [5, 0, 1, 140]
+    q, k, v = qkv(gen(heads), sum(lens), sum(lens), heads, 1, 64)
+    run(q, k, v, lens, lens)
+    q, k, v = qkv(gen(heads), 3, 2000, heads, 1, 128)
+    run(q, k, v, [1, 2], [700, 1300])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [64, 65, 100])
+def test_many_sequences_with_few_heads(n):
+    """More sequences than the line holds, some long enough to be cut."""
+    q_lens = [(7 * i) % 5 for i in range(n)]
+    k_lens = [(131 * i) % 400 if i % 33 else 3000 for i in range(n)]
+    q, k, v = qkv(gen(n), sum(q_lens), sum(k_lens), 2, 1, 128)
+    run(q, k, v, q_lens, k_lens)
+    run(q, k, v, q_lens, k_lens, causal=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 def test_infinite_values_in_one_part_of_the_keys(bad):
     q, k, v = qkv(gen(18), 40, 3000, 4, 1, 128)

@@ -218,6 +218,13 @@ def test_long_sequences(lens, heads, kv_heads, tokens, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,tokens", [(96, 1), (128, 1), (192, 2), (40, 5)])
+def test_large_groups_and_drafts(heads, tokens):
+    run([300, 0, 17, 2100], tokens, heads, 1, 128, 32)
+    run([30, 3], tokens, heads, 1, 64, 32)
+
+
+@pytest.mark.gpu
 def test_many_sequences():
     lens = [(37 * i) % 500 for i in range(300)]
     run(lens, 1, 4, 1, 128, 32)
