@@ -24,11 +24,11 @@
 // whole, 37 us cut).
 //
 // Bound: for long sequences the products and the softmax beside them.  Two tiles by
-// 128 keys are 2048 cycles of products (d = 128); the tensor pipe is busy 84 % of a
-// full wave's time, at 1.56 to 1.7 PFLOP/s of 1.9 (32,768 causal tokens of 16 heads:
-// 2.6 to 2.8 ms, at the power limit).  With d = 64 it is the exponentials: 16 a cycle
+// 128 keys are 2048 cycles of products (d = 128); a full wave (2432 queries over 16,384
+// keys, 16 heads, not causal) takes 179 us, 1.82 PFLOP/s of 1.9, 32,768 causal tokens of
+// 16 heads 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.  With d = 64 it is the exponentials: 16 a cycle
 // and SM, 128 x 256 of them to 1024 cycles of products.  For short ones it is the units'
-// ends: 4 x 4096 tokens of 32 heads 410 us (1.33 PFLOP/s), 100 tokens 10.6 us, most of it
+// ends: 4 x 4096 tokens of 32 heads 375 to 415 us (1.33 to 1.47 PFLOP/s), 100 tokens 10.6 us, most of it
 // the way from the launch to the first product and from the last one to the output.
 //
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
@@ -157,13 +157,19 @@ __device__ void make_line(const AttentionArgs& a, int pack, int shift, int lane,
 
 // The unit of block `index`, for a whole warp; false: there is none.  Those with the
 // most keys come first: the longest sequences, of a causal one its last queries.  With
-// `splits`, block index % splits of the blocks of unit index / splits: parts of at least
-// kPartTiles tiles of keys and three quarters of what an SM has to do; `parts` is how
-// many there are.
+// `splits`, one of a unit's parts: of at least kPartTiles tiles of keys and three
+// quarters of what an SM has to do; `parts` is how many there are.  Of packed sequences
+// all parts of a unit come side by side, longest units first (8 parts of prompts behind
+// their keys: 103 us, 119 with all first parts first); of a uniform batch all first parts
+// come first (512 queries behind 7000 keys: 65 us, 85 side by side, where blocks that had
+// no part went from one to the next while the last units waited).
 __device__ bool find_unit(const AttentionArgs& a, int pack, int shift, int32_t index, const Line& line,
                           int32_t per_sm, int lane, Unit& u, int32_t& parts) {
-  const int32_t part = a.splits > 1 ? index % a.splits : 0;
-  if (a.splits > 1) index /= a.splits;
+  int32_t part = 0;
+  if (a.splits > 1) {
+    part = a.cu_q ? index % a.splits : index / a.units;
+    index = a.cu_q ? index / a.splits : index % a.units;
+  }
   parts = 1;
   u.record = -1;
   const int head_blocks = a.heads / pack;
@@ -449,7 +455,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         }
         Unit u;
         const bool there = find_unit(a, pack, shift, index, line, per_sm, lane, u, parts);
-        if (!there && a.splits > 1 && index % a.splits == 0 && lane == 0) a.parts[index / a.splits].parts = 0;
+        if (!there && a.splits > 1 && a.cu_q && index % a.splits == 0 && lane == 0) a.parts[index / a.splits].parts = 0;
         if (there) {
           ok = whole_warp(mbar_wait(&unit_empty[n & 1], ((n >> 1) & 1) ^ 1));  // (the first round passes at once)
           if (!ok) break;
@@ -1005,8 +1011,21 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   // for each SM, no more parts than a sequence can have.  (8 x 263 queries of 32 heads
   // behind 3900 keys on average, 280 units: 120 us whole.)
   const int64_t longest = ((a.cu_k ? a.Tk : a.Tk / a.N) + kTile - 1) / kTile;
-  if (units < 2 * a.sm_count)
-    a.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(8 * a.sm_count / units, longest / kPartTiles)));
+  if (units < 2 * a.sm_count) {
+    int64_t splits = std::min(8 * a.sm_count / units, longest / kPartTiles);
+    if (!a.cu_q) {
+      // No more than find_unit will make of these lengths; none where each unit has an SM
+      // and about the mean's length.  (152 units of 128 tiles of keys: 183 us whole, 227 in
+      // halves.)
+      const int64_t n_q = a.Tq / a.N, len = a.Tk / a.N, work = units * longest / a.sm_count;
+      const int64_t length = std::max<int64_t>(kPartTiles, 3 * work / 4);
+      const double mean = !a.causal ? len : n_q <= len ? len - 0.5 * n_q : 0.5 * len * len / n_q;
+      splits = std::min(splits, (longest + length - 1) / length);
+      if (units <= a.sm_count && len <= 1.25 * mean * units / a.sm_count) splits = 1;
+    }
+    a.splits = static_cast<int32_t>(std::max<int64_t>(1, splits));
+    a.units = static_cast<int32_t>(units);
+  }
   void* ws = nullptr;
   if (a.splits > 1) {
     const size_t rows = static_cast<size_t>(units) * a.splits * kRows;

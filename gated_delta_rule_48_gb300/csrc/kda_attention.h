@@ -37,7 +37,7 @@ struct AttentionArgs {
   // Few units of rows: their keys shared by several blocks, up to `splits` of them
   // (kda_attention.cu); a part's sums [unit * splits + part][256][d], each row's
   // maximum and sum of p, and each unit's rows and how many parts it has.
-  int32_t splits = 1;
+  int32_t splits = 1, units = 0;
   float* part_out = nullptr;
   float2* part_ml = nullptr;
   PartInfo* parts = nullptr;
