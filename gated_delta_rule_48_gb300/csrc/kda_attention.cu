@@ -26,17 +26,18 @@
 // Bound: for long sequences the products and the softmax beside them.  Two tiles by
 // 128 keys are 2048 cycles of products (d = 128); a full wave (2432 queries over 16,384
 // keys, 16 heads, not causal) takes 179 us, 1.82 PFLOP/s of 1.9, 32,768 causal tokens of
-// 16 heads 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.  With d = 64 it is the exponentials: 16 a cycle
-// and SM, 128 x 256 of them to 1024 cycles of products.  For short ones it is the units'
-// ends: 4 x 4096 tokens of 32 heads 375 to 415 us (1.33 to 1.47 PFLOP/s), 100 tokens 10.6 us, most of it
-// the way from the launch to the first product and from the last one to the output.
+// 16 heads 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.
+// With d = 64 it is the exponentials: 16 a cycle and SM, 128 x 256 of them to 1024 cycles
+// of products.  For short ones it is the units' ends: 4 x 4096 tokens of 32 heads 375 to
+// 415 us (1.33 to 1.47 PFLOP/s), 100 tokens 10.6 us, most of it the way from the launch
+// to the first product and from the last one to the output.
 //
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
 // type); the sum l is of the unrounded p, in 32 bits.
 //
 // Keys outside a query's reach get p = 0, and 0 times a value's infinity or NaN
-// would be NaN: in tiles that reach past a row's last key two warps look through
-// V's tile before it is used.  Where they find such values they put zeros there,
+// would be NaN: in tiles that reach past a row's last key a warp looks through
+// V's tile before it is used.  Where it finds such values it puts zeros there,
 // and rows that do reach them get them added at the end.
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -107,6 +107,14 @@ def test_keys_shared_by_several_blocks(q_lens, k_lens, causal, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,tq,tk", [(3, 200, 1500), (1, 1100, 1100), (2, 600, 130), (5, 33, 2049)])
+def test_uniform_batches_cut_into_parts(n, tq, tk, causal):
+    q, k, v = qkv(gen(tq), n * tq, n * tk, 4, 2, 128)
+    run(q, k, v, [tq] * n, [tk] * n, causal, packed=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [96, 128, 192, 256])
 def test_large_groups(heads):
     """Few tokens to a tile, down to one; groups of more heads than a tile has rows."""
