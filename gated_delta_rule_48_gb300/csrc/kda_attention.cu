@@ -64,8 +64,11 @@ static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
 constexpr int kPartTiles = 4;            // the least of a unit's part of the keys
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
 constexpr float kSlack = 8.0f;           // log2 of how far p may pass 1
-// From here on what c m loses by its rounding counts (from 2^31 on p would be 0 or
-// infinite): m is taken off the scores before c is multiplied in.
+constexpr float kLn2 = 0.6931471805599453f;
+// Up to here p = 2^(c s - b) with b = c m rounded once: all of a row's p, and its l and o,
+// have the same factor 2^(c m - b), at most 2^(1/32), which o / l and log l + b take off
+// again.  From here on that factor grows (from 2^31 on p would be 0 or infinite): m is taken
+// off the scores before c is multiplied in.
 constexpr float kLarge = 1048576.0f;
 
 template <int D>
@@ -88,6 +91,29 @@ struct Shape {
 struct Maps {
   CUtensorMap q, k, v;
 };
+
+// What a row's p lack: p = 2^(c (s - less) - base), for the maximum m of its scores so far
+// (or, where the slack has let p pass 1, an earlier one).
+struct Base {
+  float less, base;
+};
+__device__ __forceinline__ Base base_of(float m, float c) {
+  const float b = m == -INFINITY ? 0.0f : __fmul_rn(m, c);  // (never one with a sum behind it)
+  const bool large = fabsf(b) > kLarge;
+  return Base{large ? m : 0.0f, large ? 0.0f : b};
+}
+// The factor from p's of maximum `from` to those of `to`, `to` not below: by what was taken
+// off them, with its roundings (by c m itself keys behind a move of m, or of another part,
+// would weigh up to 4 % more or less than those before).  0 without a score so far.
+__device__ __forceinline__ float rescale(float from, float to, float c) {
+  const Base a = base_of(from, c), b = base_of(to, c);
+  return from == -INFINITY ? 0.0f : ex2(fmaf(a.less - b.less, c, a.base - b.base));
+}
+
+__device__ __forceinline__ float log_of_sum(float m, float l, float scale) {
+  const Base off = base_of(m, scale * kLog2e);
+  return off.less * scale + fmaf(off.base, kLn2, logf(l));
+}
 
 // What a block works on: 256 rows of a sequence.
 struct Unit {
@@ -739,7 +765,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge)) {
           const float next = fmaxf(m, most);
           if (j > 0 && __any_sync(0xffffffffu, next != m)) {
-            const float keep = next == -INFINITY ? 1.0f : ex2((m - next) * c);
+            const float keep = next == -INFINITY ? 1.0f : rescale(m, next, c);
             l *= keep;
 #pragma unroll 1
             for (int k = 0; k < D; k += 32) {
@@ -752,12 +778,11 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
             tmem_wait_st();
           }
           m = next;
-          base = m == -INFINITY ? 0.0f : m * c;
-          if (__any_sync(0xffffffffu, fabsf(base) > kLarge)) {
-            const float less = m == -INFINITY ? 0.0f : m;
+          const Base off = base_of(m, c);
+          base = off.base;
+          if (__any_sync(0xffffffffu, off.less != 0.0f)) {
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) s[k] -= less;
-            base = 0.0f;
+            for (int k = 0; k < kTile; ++k) s[k] -= off.less;
           }
         }
         ++tile;
@@ -853,7 +878,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       if (part) {
         if (valid) a.part_ml[static_cast<int64_t>(u.record) * kRows + i * kTile + row] = make_float2(m, l);
       } else if (a.lse && valid && kda_guard(e, 1, a.Tq * a.heads, a.err))
-        a.lse[e] = reach > 0 ? (m == -INFINITY ? 0.0f : m) * a.scale + logf(l) : -INFINITY;
+        a.lse[e] = reach > 0 ? log_of_sum(m, l, a.scale) : -INFINITY;
     }
     if (!ok && lane == 0) timeout();
   }
@@ -895,8 +920,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
     for (int e = 0; e < kPer; ++e) o[r][e] = 0.0f;
   }
   auto add = [&](int r, const float2& ml, const float (&v)[kPer]) {
-    const float next = fmaxf(m[r], ml.x), base = next == -INFINITY ? 0.0f : next;
-    const float keep = ex2((m[r] - base) * c), w = ex2((ml.x - base) * c);
+    const float next = fmaxf(m[r], ml.x), keep = rescale(m[r], next, c), w = rescale(ml.x, next, c);
     m[r] = next;
     l[r] = fmaf(ml.y, w, l[r] * keep);
 #pragma unroll
@@ -924,7 +948,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
       store_n<kPer>(a.out + at, o[r]);
     const int64_t e = (static_cast<int64_t>(u.q0) + tok) * a.heads + head;
     if (a.lse && lane == 0 && kda_guard(e, 1, a.Tq * a.heads, a.err))
-      a.lse[e] = any ? (m[r] == -INFINITY ? 0.0f : m[r]) * a.scale + logf(l[r]) : -INFINITY;
+      a.lse[e] = any ? log_of_sum(m[r], l[r], a.scale) : -INFINITY;
   };
   if constexpr (SHARED) {
 #pragma unroll
