@@ -91,7 +91,7 @@ struct Shape {
   static constexpr int kRing = kWarps * kDepth * kStage;
   static constexpr int kParts = kWarps * kCols * (D + 4) * 4;   // the warps' results, over the ring
   static constexpr int kSmem = kRing > kParts ? kRing : kParts;
-  static constexpr int kRecord = kCols * (D + 2);               // floats of a part: o, then m and l
+  static constexpr int kRecord = kCols * (D + 3);               // floats of a part: o, then m and l, then cc
 };
 
 // d += A B (or d = A B), bf16 operands.
@@ -556,7 +556,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     const int slot = at == part0 ? 0 : 1;
     float* const record = records + (b * 2 + slot) * S::kRecord;
     // four channels of a column: to the output, or to the part's record
-    auto put = [&](int col, int ch, const float4& v, float top, float sum) {
+    auto put = [&](int col, int ch, const float4& v, float top, float sum, float cc_of) {
       if (complete) {
         const int g_col = col0 + col;
         if (g_col < cols) {
@@ -570,13 +570,14 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
                 any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale))
                     : make_uint2(0, 0);
           if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
-            a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+            a.lse[row * a.heads + h] = any ? fmaf(top * cc_of, kLn2, logf(sum)) : -INFINITY;
         }
       } else {
         *reinterpret_cast<float4*>(record + col * S::D + ch) = v;
         if (ch == 0) {
           record[S::kCols * S::D + 2 * col] = top;
           record[S::kCols * S::D + 2 * col + 1] = sum;
+          record[S::kCols * (S::D + 2) + col] = cc_of;
         }
       }
     };
@@ -587,11 +588,9 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int w = 4; w < 32; w *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
-    // maxima of scores times c from here on
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[t][e] = m[t][e] == kLowest ? kLowest : m[t][e] * cc[t][e];
+    // (Parts are joined by differences of maxima, and cc then multiplied in, as above:
+    // between maxima that were multiplied first the weights of large scores were up to 4 %
+    // off at 2^20.)
     if constexpr (SOLO) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -601,11 +600,11 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
           for (int g = 0; g < G; ++g)  // channels 32 g + 4 r + 0..3
             put(8 * t + 2 * j + e, 32 * g + 4 * r,
                 make_float4(o[2 * g][t][e], o[2 * g][t][e + 2], o[2 * g + 1][t][e], o[2 * g + 1][t][e + 2]), m[t][e],
-                l[t][e]);
+                l[t][e], cc[t][e]);
     } else {
     // ---- the warps' results together
     __syncthreads();
-    float* const parts = reinterpret_cast<float*>(smem);  // [warp][column][D + 4]: o, m, l
+    float* const parts = reinterpret_cast<float*>(smem);  // [warp][column][D + 4]: o, m, l, cc
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -618,11 +617,13 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         if (r == 0) {
           to[S::D] = m[t][e];
           to[S::D + 1] = l[t][e];
+          to[S::D + 2] = cc[t][e];
         }
       }
     __syncthreads();
     for (int e = threadIdx.x; e < S::kCols * (S::D / 4); e += kThreads) {
       const int col = e / (S::D / 4), ch = e % (S::D / 4) * 4;
+      const float cc_of = parts[col * (S::D + 4) + S::D + 2];  // (of the column: the same in all warps)
       float top = kLowest, sum = 0.0f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -630,7 +631,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float* from = parts + (w * S::kCols + col) * (S::D + 4);
-        const float keep = ex2(from[S::D] - top);
+        const float keep = ex2((from[S::D] - top) * cc_of);
         const float4 x = *reinterpret_cast<const float4*>(from + ch);
         sum = fmaf(from[S::D + 1], keep, sum);
         v.x = fmaf(x.x, keep, v.x);
@@ -638,7 +639,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         v.z = fmaf(x.z, keep, v.z);
         v.w = fmaf(x.w, keep, v.w);
       }
-      put(col, ch, v, top, sum);
+      put(col, ch, v, top, sum, cc_of);
     }
     }
     if (!complete && first == 0 && (SOLO ? lane : static_cast<int>(threadIdx.x)) == 0) {  // the unit's first part
@@ -677,10 +678,10 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4Attentio
   const int group = a.heads / a.pages.heads, cols = a.tokens * group;
   const int item = threadIdx.x % kItems, set = threadIdx.x / kItems;
   const int col = item / (S::D / 4), ch = item % (S::D / 4) * 4;
-  float top = kLowest, sum = 0.0f;
+  float top = kLowest, sum = 0.0f, cc = 1.0f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float m2, float l2, const float4& x) {
-    const float next = fmaxf(top, m2), k0 = ex2(top - next), k1 = ex2(m2 - next);
+    const float next = fmaxf(top, m2), k0 = ex2((top - next) * cc), k1 = ex2((m2 - next) * cc);
     top = next;
     sum = fmaf(l2, k1, sum * k0);
     v.x = fmaf(x.x, k1, v.x * k0);
@@ -689,6 +690,8 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4Attentio
     v.w = fmaf(x.w, k1, v.w * k0);
   };
   auto add_parts = [&](const Meta& mt, int b0, int from, int by) {
+    // (a column's, the same in all parts)
+    cc = records[(static_cast<int64_t>(b0) * 2 + mt.slot) * S::kRecord + S::kCols * (S::D + 2) + col];
     top = kLowest;
     sum = 0.0f;
     v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4Attentio
       *reinterpret_cast<uint2*>(a.out + to) =
           any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale)) : make_uint2(0, 0);
     if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
-      a.lse[row * a.heads + h] = any ? fmaf(top, kLn2, logf(sum)) : -INFINITY;
+      a.lse[row * a.heads + h] = any ? fmaf(top * cc, kLn2, logf(sum)) : -INFINITY;
   };
   const Meta first = metas[blockIdx.x * kWarps];
   if (!first.solo) {  // (of a block: all sets of threads share the parts)
