@@ -3,9 +3,10 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j),  j < reach of i
 //
 // One pass over the keys with the running maximum m and sum l of a softmax:
-// p = 2^(c s - c m) with c = scale log2 e, o = sum p v / l.  Where a tile's
+// p = 2^(c s - c m - 8) with c = scale log2 e, o = sum p v / l.  Where a tile's
 // maximum passes m by more than 2^8 (in p), m moves up and o and l are scaled;
-// below that p only grows, which costs bf16 and 32 bits no precision.
+// below that p only grows, up to 1, which costs bf16 and 32 bits no precision.  (Without
+// the 8 p grew up to 2^8, and sums over values of 2^120 passed what 32 bits hold.)
 //
 // A unit of work is 256 rows of queries, as two tiles of 128 (tensor memory's lanes),
 // over their keys, 128 at a time.  Rows are tokens x query heads of one key head (as
@@ -63,11 +64,11 @@ static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
               "register shares exceed the launch's");
 constexpr int kPartTiles = 4;            // the least of a unit's part of the keys
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
-constexpr float kSlack = 8.0f;           // log2 of how far p may pass 1
+constexpr float kSlack = 8.0f;           // log2 of how far p may grow: from 2^-8 to 1
 constexpr float kLn2 = 0.6931471805599453f;
-// Up to here p = 2^(c s - b) with b = c m rounded once: all of a row's p, and its l and o,
-// have the same factor 2^(c m - b), at most 2^(1/32), which o / l and log l + b take off
-// again.  From here on that factor grows (from 2^31 on p would be 0 or infinite): m is taken
+// Up to here p = 2^(c s - b) with b = c m + 8 rounded once: all of a row's p, and its l and o,
+// have the same factor 2^(c m + 8 - b), at most 2^(1/32), which o / l and log l + b take
+// off again.  From here on that factor grows (from 2^31 on p would be 0 or infinite): m is taken
 // off the scores before c is multiplied in.
 constexpr float kLarge = 1048576.0f;
 
@@ -93,14 +94,14 @@ struct Maps {
 };
 
 // What a row's p lack: p = 2^(c (s - less) - base), for the maximum m of its scores so far
-// (or, where the slack has let p pass 1, an earlier one).
+// (or, where the slack has let p grow, an earlier one).
 struct Base {
   float less, base;
 };
 __device__ __forceinline__ Base base_of(float m, float c) {
-  const float b = m == -INFINITY ? 0.0f : __fmul_rn(m, c);  // (never one with a sum behind it)
+  const float b = m == -INFINITY ? 0.0f : fmaf(m, c, kSlack);
   const bool large = fabsf(b) > kLarge;
-  return Base{large ? m : 0.0f, large ? 0.0f : b};
+  return Base{large ? m : 0.0f, large ? kSlack : b};
 }
 // The factor from p's of maximum `from` to those of `to`, `to` not below: by what was taken
 // off them, with its roundings (by c m itself keys behind a move of m, or of another part,
@@ -110,9 +111,10 @@ __device__ __forceinline__ float rescale(float from, float to, float c) {
   return from == -INFINITY ? 0.0f : ex2(fmaf(a.less - b.less, c, a.base - b.base));
 }
 
+// (l as it would be without the slack: near 1 the logarithm is at its most exact.)
 __device__ __forceinline__ float log_of_sum(float m, float l, float scale) {
   const Base off = base_of(m, scale * kLog2e);
-  return off.less * scale + fmaf(off.base, kLn2, logf(l));
+  return off.less * scale + fmaf(off.base - kSlack, kLn2, logf(l * 256.0f));
 }
 
 // What a block works on: 256 rows of a sequence.
@@ -761,7 +763,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
           tc_fence_after();
         }
         if (j == 0) m = most;
-        float base = m == -INFINITY ? 0.0f : m * c;
+        float base = m == -INFINITY ? 0.0f : fmaf(m, c, kSlack);
         if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge)) {
           const float next = fmaxf(m, most);
           if (j > 0 && __any_sync(0xffffffffu, next != m)) {

@@ -1,6 +1,6 @@
 // A few query tokens of each sequence over the cache in 4 bits.
 //
-//   x = c sum_g s_tg sum_{c in g} q_c n_tc,   p = 2^(x - m),   o_c = sum_t p_t s'_tg n'_tc / sum_t p_t
+//   x = c sum_g s_tg sum_{c in g} q_c n_tc,   p = 2^(x - m - 8),   o_c = sum_t p_t s'_tg n'_tc / sum_t p_t
 //
 // with c = scale log2 e, a key's scales s and codes n, a value's s' and n', per
 // group g of 32 channels.
@@ -68,7 +68,7 @@ constexpr int kHalf = 16;
 constexpr int kDepth = 3;         // slices of a warp in flight
 constexpr int kSoloSlices = 16;   // of a unit, on average: up to as many, a warp to a unit
 constexpr float kLowest = -3e38f; // a maximum of nothing (-infinity less itself is NaN)
-constexpr float kSlack = 8.0f;    // log2 of how far p may pass 1
+constexpr float kSlack = 8.0f;    // log2 of how far p may grow, from 2^-8 to 1 (p s' is never above s')
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Where a block's part of a unit lies that is not whole.
@@ -492,7 +492,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[h][t][e] = ex2((x[h][t][e] - m[t][e & 1]) * cc[t][e & 1]);
+            x[h][t][e] = ex2(fmaf(x[h][t][e] - m[t][e & 1], cc[t][e & 1], -kSlack));
             l[t][e & 1] += x[h][t][e];
           }
       // ---- values
@@ -570,7 +570,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
                 any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale))
                     : make_uint2(0, 0);
           if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
-            a.lse[row * a.heads + h] = any ? fmaf(top * cc_of, kLn2, logf(sum)) : -INFINITY;
+            a.lse[row * a.heads + h] = any ? fmaf(top * cc_of, kLn2, logf(sum * 256.0f)) : -INFINITY;
         }
       } else {
         *reinterpret_cast<float4*>(record + col * S::D + ch) = v;
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4Attentio
       *reinterpret_cast<uint2*>(a.out + to) =
           any ? make_uint2(pack2_bf16(v.x * scale, v.y * scale), pack2_bf16(v.z * scale, v.w * scale)) : make_uint2(0, 0);
     if (a.lse && ch == 0 && kda_guard(row * a.heads + h, 1, n_rows * a.heads, a.err))
-      a.lse[row * a.heads + h] = any ? fmaf(top * cc, kLn2, logf(sum)) : -INFINITY;
+      a.lse[row * a.heads + h] = any ? fmaf(top * cc, kLn2, logf(sum * 256.0f)) : -INFINITY;
   };
   const Meta first = metas[blockIdx.x * kWarps];
   if (!first.solo) {  // (of a block: all sets of threads share the parts)

@@ -612,7 +612,8 @@ kda_status kda_ssm_scan_step(const void *x, int64_t ld_x, const void *dt,
  * lse of -infinity.  Keys and values a query does not reach have no influence,
  * whatever they hold.  Scores, maxima and sums are in 32 bits; p is rounded to
  * bf16 for the product with v (off by at most 2^-8 of each term), out is
- * rounded once.
+ * rounded once.  p is held at 1 or below, so sums over finite values are finite
+ * where the largest |v| times the number of keys reached is below 2^127.
  *
  * Tensors:
  *   q    bf16 [total_q, n_heads, d]      read   } every token's first value on
@@ -705,7 +706,9 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * query i of a sequence reaches positions 0 .. seq_lens[n] - n_tokens + i, and
  * none (zeros, an lse of -infinity) where that is negative.  Scores are sums
  * over whole numbers n in 32 bits, scaled per group; p * s of a value's group
- * is rounded to bf16 for the product with its n; out is rounded once.
+ * is rounded to bf16 for the product with its n; out is rounded once.  Sums over
+ * finite values are finite where the largest |n s| times the number of positions
+ * reached is below 2^132.
  *
  *   q         bf16 [N, n_tokens, n_heads, d], tokens ld_q apart      read
  *   seq_lens  i32 [N]                                                read
