@@ -732,7 +732,8 @@ def kda_attention_fwd(q, k, v, cu_seqlens_q=None, cu_seqlens_k=None, *, n_seqs=N
     apart; cu_seqlens_q: int32 [N + 1] (CUDA) or None; cu_seqlens_k: the same for keys, None where
     they are the queries'.  With fewer queries than keys the queries are their sequence's last ones.
     scale: 1 / sqrt(d) if None.  Returns (out, lse): out as q, lse f32 [Tq, heads] (the logarithms
-    of the sums) or None unless wanted or given.
+    of the sums) or None unless wanted or given.  n_seqs: the sequences of packed tokens of equal
+    lengths (without cu_seqlens; a uniform batch has B).
     """
     return _call(stream, "attention_fwd", q, k, v, cu_seqlens_q, cu_seqlens_k, n_seqs, bool(causal),
                  scale, bool(want_lse), out, lse)
@@ -752,7 +753,7 @@ def kda_kv4_write(k, v, cache, block_table, start=None, cu_seqlens=None, *, n_se
     k, v: bf16 [T, kv_heads, d] or [B, T_b, kv_heads, d]; cache: as :func:`kda_kv4_cache` makes it;
     block_table: int32 [N, max_pages], the pages of each sequence; start: int32 [N], the position of
     each sequence's first token (None: 0; negative: that sequence is left out); cu_seqlens: int32
-    [N + 1] or None (N = block_table's rows, or ``n_seqs``, of equal length).
+    [N + 1] or None (N = block_table's rows, or ``n_seqs``, of equal length; B is N).
     """
     _call(stream, "kv4_write", k, v, cache, block_table, start, cu_seqlens, n_seqs)
 

@@ -467,6 +467,7 @@ struct Heads {
 Heads heads_of(const Tensor& t, const char* name, const Tensor& x) {
   const int64_t n = t.dim();
   if (n < 3) refuse("%s must have at least 3 dimensions, got %s", name, shape_of(t.sizes()).c_str());
+  if (n > 4) refuse("%s must have 3 or 4 dimensions, got %s", name, shape_of(t.sizes()).c_str());
   of_type(t, at::kBFloat16, name, x);
   Heads h;
   h.heads = t.size(n - 2);
@@ -482,6 +483,11 @@ Heads heads_of(const Tensor& t, const char* name, const Tensor& x) {
   h.p = r.p;
   h.ld = r.ld;
   return h;
+}
+// Without cu_seqlens: a uniform batch [B, T_b, heads, d] has as many sequences as the call.
+void of_batch(const Tensor& t, const char* name, int64_t seqs) {
+  if (t.dim() > 3 && t.size(0) != seqs)
+    refuse("%s has %lld sequences, expected %lld", name, (long long)t.size(0), (long long)seqs);
 }
 const Tensor& on_gpu(const Tensor& t, const char* name) {
   if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
@@ -524,6 +530,7 @@ PyObject* attention_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ckp = static_cast<const int32_t*>(dense(ck, cq.sizes(), at::kInt, "cu_seqlens_k", q));
     } else {
       seqs = narrow(a[5] != Py_None ? integer(a[5]) : q.dim() > 3 ? q.size(0) : 1, "n_seqs");
+      of_batch(q, "q", seqs);
     }
     const Tensor out = output(a[9], q.sizes(), at::kBFloat16, q, "out");
     const Heads oh = heads_of(out, "out", q);
@@ -609,6 +616,7 @@ PyObject* kv4_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Pages p(a[2], a[3], k);
     of_cache(kh, p, "k");
     const Span s(a[4], a[5], a[6], p, k);
+    if (!s.cu) of_batch(k, "k", s.count);
     const Launch on(k);
     check(g_lib->kv4_write(kh.p, kh.ld, vh.p, vh.ld, &p.cache, p.table, p.ld, p.width, s.start, s.cu,
                            kh.tokens, s.count, on.stream));
@@ -635,6 +643,7 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       of_cache(h[i], p, name);
       if (h[i].tokens != tokens)
         refuse("%s has %lld tokens, expected %lld", name, (long long)h[i].tokens, (long long)tokens);
+      if (!s.cu) of_batch(made[i], name, s.count);
     }
     const Launch on(table);
     check(g_lib->kv4_read(h[0].p, h[0].ld, h[1].p, h[1].ld, &p.cache, p.table, p.ld, p.width, s.start, s.cu,
@@ -648,7 +657,6 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 8, [&]() -> PyObject* {
     const Tensor& q = on_gpu(tensor(a[0], "q"), "q");
     const Heads qh = heads_of(q, "q", q);
-    if (q.dim() > 4) refuse("q must have 3 or 4 dimensions, got %s", shape_of(q.sizes()).c_str());
     const Pages p(a[1], a[2], q);
     if (qh.d != p.cache.d) refuse("q has heads of %lld, the cache of %d", (long long)qh.d, p.cache.d);
     const int32_t seqs = narrow(q.size(0), "n_seqs");
