@@ -19,7 +19,8 @@
 //     ones after a power of two for each row (what is 2^30 times smaller than a row's
 //     largest value may round).  The 8 goes away with the accumulator's first
 //     value, one product of the groups' scales with -8 2^-24 sum_{c in g} q_c in four
-//     bf16 parts.
+//     bf16 parts.  (So a score's rounding goes by the sums of |q| (|n| + 16), not of
+//     |q n|: 2^-23 of them a step.)
 //   - A value's code is, as it stands, the bf16 number (n + 8) 2^-133 or 16 times
 //     that; one multiply-add makes it n 2^-6 exactly.  p, which it is multiplied by,
 //     needs the range of bf16.  (Leaving the 8 in and taking it off by a product with

@@ -704,11 +704,12 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * As kda_attention_fwd, causal, with the keys and values n * s of the cache's
  * first seq_lens[n] positions, the queries' own among them (written before):
  * query i of a sequence reaches positions 0 .. seq_lens[n] - n_tokens + i, and
- * none (zeros, an lse of -infinity) where that is negative.  Scores are sums
- * over whole numbers n in 32 bits, scaled per group; p * s of a value's group
- * is rounded to bf16 for the product with its n; out is rounded once.  Sums over
- * finite values are finite where the largest |n s| times the number of positions
- * reached is below 2^132.
+ * none (zeros, an lse of -infinity) where that is negative.  A score's part of a
+ * group is s (sum (n + 8) q - 8 sum q), in 32 bits: a score is off by no more than
+ * (d + 8) 2^-23 scale sum s sum |q| (|n| + 16), also where all n of a group but a
+ * single large one are 0.  p * s of a value's group is rounded to bf16 for the
+ * product with its n; out is rounded once.  Sums over finite values are finite
+ * where the largest |n s| times the number of positions reached is below 2^132.
  *
  *   q         bf16 [N, n_tokens, n_heads, d], tokens ld_q apart      read
  *   seq_lens  i32 [N]                                                read

@@ -86,3 +86,34 @@ def test_scores_beyond_whole_numbers_of_32_bits(power, n, sequences, heads, d):
     assert torch.allclose(o, want.expand_as(o), rtol=1e-12, atol=1e-12)
     wide = [t.expand(sequences, *t.shape) for t in (o, l, m)]
     check(out, lse, (*wide, torch.zeros_like(wide[1])), d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,sequences,heads", [(40, 3, 12), (500, 1, 3), (9000, 1, 8)])
+def test_groups_with_one_large_channel(n, sequences, heads, d):
+    """Keys with an outlier in every group, so that most codes are 0, and queries that are small there
+    and large elsewhere: sums of (n + 8) q less 8 sum q, whose terms are far larger than n q.  With X
+    the sum of s |q| (|n| + 16), scale included: at most d products and their sum, the d terms of
+    8 sum q and its parts, and the groups' products with s, 2^-23 of X or less each."""
+    g = gen(n + d)
+    k = randn(g, n, 1, d)
+    k[:, :, 5::32] = 70 * (1 + torch.rand(n, 1, d // 32, generator=g, device=DEV))
+    v = randn(g, n, 1, d, dtype=torch.bfloat16)
+    table, pages = paged([n], 16)
+    cache = kb.kda_kv4_cache(pages, 16, 1, d)
+    kb.kda_kv4_write(k.bfloat16(), v, cache, table)
+    q = randn(g, sequences, 1, heads, d, std=4.0)
+    q[..., 5::32] *= 0.002
+    q = q.bfloat16()
+    lens = torch.full((sequences,), n, dtype=torch.int32, device=DEV)
+    out, lse = kb.kda_kv4_attention(q, cache, table.expand(sequences, -1).contiguous(), lens, want_lse=True)
+    kd, vd = spans(cache, table, 0, 0, n)
+    scale = d ** -0.5
+    pos = torch.arange(n, device=DEV)
+    s = cache[1][table[0].long()[pos // 16], 0, pos % 16].double().repeat_interleave(32, 1)   # [n, d]
+    assert ((kd[:, 0] / s).abs() < 0.5).float().mean() > 0.9   # codes of 0
+    for i in range(sequences):
+        o, l, m, _ = attend(q[i], kd, vd, scale, [n])
+        X = scale * torch.einsum("hd,kd->hk", q[i, 0].double().abs(), kd[:, 0].abs() + 16 * s).amax(1)[None]
+        check(out[i], lse[i], (o, l, m, X), d)
