@@ -908,7 +908,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
   if (parts < 2) return;
   // (a unit that was not reached because a wait ran out has anything here)
   if (parts > a.splits || u.q0 < 0 || u.n_q > a.Tq - u.q0 || u.tok0 < 0 || u.head0 < 0 || u.head0 > a.heads - pack) return;
-  if (u.tok0 + static_cast<int>(blockIdx.y) * kJoinRows / pack >= u.n_q) return;
+  if (u.tok0 >= u.n_q) return;
+  const int32_t queries = u.n_q - u.tok0;  // from the unit's first one on
+  if (static_cast<int32_t>(blockIdx.y) * kJoinRows / pack >= queries) return;
   const int row0 = blockIdx.y * kJoinRows + (SHARED ? 0 : warp * kMine);
   const int64_t first = static_cast<int64_t>(unit) * a.splits * kRows + row0;
   const float c = a.scale * kLog2e;
@@ -939,8 +941,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
     }
   }
   auto put = [&](int row, int r) {
+    if (row / pack >= queries) return;
     const int32_t tok = u.tok0 + row / pack, head = u.head0 + row % pack;
-    if (tok >= u.n_q) return;
     const bool any = (a.causal ? u.len + min(0, tok + 1 - u.n_q) : u.len) > 0;
     const float scale = 1.0f / l[r];
 #pragma unroll
