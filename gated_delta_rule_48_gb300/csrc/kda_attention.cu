@@ -36,6 +36,13 @@
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
 // type); the sum l is of the unrounded p, in 32 bits.
 //
+// The tensor core adds to O with what lies some 2^-25 below it cut off: of 2^20 keys of
+// like weights the sum came out 0.5 % too small, of 2^22 2.3 %.  So after every 2^18 keys
+// of a unit O (and l) is moved to a sum in the block's own memory, and begins again at 0
+// (2^22 keys: within 0.03 %).  That is a kernel of its own (MOVES), for calls with that many
+// keys: with the move in it the softmax's loop is slower (32,768 tokens 2.60 ms instead of
+// 2.43, 164,000 keys of 40 packed sequences 278 us instead of 270).
+//
 // Keys outside a query's reach get p = 0, and 0 times a value's infinity or NaN
 // would be NaN: in tiles that reach past a row's last key a warp looks through
 // V's tile before it is used.  Where it finds such values it puts zeros there,
@@ -63,6 +70,8 @@ constexpr int kLaunchRegs = 168, kRowRegs = 224, kRestRegs = 56;
 static_assert(128 * kRestRegs + kRows * kRowRegs <= kThreads * kLaunchRegs,
               "register shares exceed the launch's");
 constexpr int kPartTiles = 4;            // the least of a unit's part of the keys
+constexpr int kMoveTiles = 2048;         // of keys, after which O is moved
+constexpr int kMaxPlaces = 1024;         // for it: as many as SMs, a block to each
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
 constexpr float kSlack = 8.0f;           // log2 of how far p may grow: from 2^-8 to 1
 constexpr float kLn2 = 0.6931471805599453f;
@@ -127,6 +136,7 @@ struct Unit {
   int32_t tiles[2];    // of keys, for each tile of rows
   int32_t masked;      // from this one on some row does not reach a tile's keys all
   int32_t record;      // where a part of the keys is kept; -1: the unit has all of them
+  int32_t place;       // where O is moved after kMoveTiles tiles; -1: there are no more
 
   // how many keys query `tok` of the sequence reaches
   __device__ __forceinline__ int32_t reach(int32_t tok, bool causal) const {
@@ -200,7 +210,7 @@ __device__ bool find_unit(const AttentionArgs& a, int pack, int shift, int32_t i
     index = a.cu_q ? index / a.splits : index % a.units;
   }
   parts = 1;
-  u.record = -1;
+  u.record = u.place = -1;
   const int head_blocks = a.heads / pack;
   const int32_t slot = index / head_blocks, hb = index - slot * head_blocks;
   int32_t block;
@@ -274,6 +284,25 @@ __device__ bool find_unit(const AttentionArgs& a, int pack, int shift, int32_t i
   }
   u.masked = u.reach(u.tok0, a.causal) / kTile;
   return true;
+}
+
+// Places for what is moved out of tensor memory, taken by blocks of any call for as long
+// as they run: there are no more blocks at a time than SMs, whatever the calls.
+__device__ int g_places[kMaxPlaces];
+
+__device__ __forceinline__ int take_place(int count) {
+  for (uint32_t t = 0; t < 1u << 20; ++t) {
+    const int at = static_cast<int>((blockIdx.x + t) % static_cast<uint32_t>(count));
+    if (atomicCAS(&g_places[at], 0, 1) == 0) {
+      __threadfence();  // (what a block before wrote there is behind it)
+      return at;
+    }
+  }
+  return -1;
+}
+__device__ __forceinline__ void give_place_back(int at) {
+  __threadfence();
+  atomicExch(&g_places[at], 0);
 }
 
 // Asks for a block of this grid that has not begun, to work on it in this one: 16
@@ -377,6 +406,42 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* r) {
       : "memory");
 }
 
+// This thread's row of O, with what was moved before added to it: moved to `sums` and set
+// to 0, or kept.  (Eight columns at a time: seldom done, and code beside the softmax's loop.)
+template <int D>
+__device__ __forceinline__ void move_sums(uint32_t t_o, float* sums, float keep, bool add, bool move) {
+#pragma unroll 1
+  for (int k = 0; k < D; k += 8) {
+    float o[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+        : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+        : "r"(t_o + k)
+        : "memory");
+    float4* const at = reinterpret_cast<float4*>(sums + k);
+    if (add) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 x = __ldcg(at + e);
+        o[4 * e] = fmaf(x.x, keep, o[4 * e]);
+        o[4 * e + 1] = fmaf(x.y, keep, o[4 * e + 1]);
+        o[4 * e + 2] = fmaf(x.z, keep, o[4 * e + 2]);
+        o[4 * e + 3] = fmaf(x.w, keep, o[4 * e + 3]);
+      }
+    }
+    if (move) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) __stcg(at + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(o[0]), "f"(o[1]),
+                 "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7]), "r"(t_o + k)
+                 : "memory");
+  }
+  tmem_wait_st();
+}
+
 // 32 bytes, a whole sector, at a multiple of 32.
 __device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -392,7 +457,7 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t pair, uint32_t sum) {
 }
 __device__ __forceinline__ bool finite_bf16(uint32_t bits) { return (bits & 0x7f80u) != 0x7f80u; }
 
-template <int D>
+template <int D, bool MOVES>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   using G = Shape<D>;
@@ -405,6 +470,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   __shared__ __align__(16) uint4 given;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_infinite;
+  __shared__ int s_place;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens = kRows / pack;
 
@@ -433,6 +499,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
     }
     mbar_fence_init();
     s_infinite = 0;
+    s_place = -1;
   }
   if (warp == 1) {
     tmem_alloc(&s_tmem, 512);
@@ -486,6 +553,14 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         const bool there = find_unit(a, pack, shift, index, line, per_sm, lane, u, parts);
         if (!there && a.splits > 1 && a.cu_q && index % a.splits == 0 && lane == 0) a.parts[index / a.splits].parts = 0;
         if (there) {
+          if (MOVES && u.most() > kMoveTiles) {
+            if (lane == 0 && s_place < 0) {
+              s_place = take_place(a.sm_count);
+              if (s_place < 0) timeout();
+            }
+            __syncwarp();
+            u.place = s_place;
+          }
           ok = whole_warp(mbar_wait(&unit_empty[n & 1], ((n >> 1) & 1) ^ 1));  // (the first round passes at once)
           if (!ok) break;
           if (lane == 0) {
@@ -718,6 +793,8 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
     const uint32_t t_o = tmem_addr(tmem, 32 * quad, G::kColO + i * D);
     const uint32_t t_p = tmem_addr(tmem, 32 * quad, G::kColP + i * G::kStepP);
     const float c = a.scale * kLog2e;
+    // this row's sums moved out of tensor memory, then the maximum they were taken with and l
+    auto sums_of = [&](int32_t place) { return a.moved + (static_cast<int64_t>(place) * kRows + i * kTile + row) * (D + 4); };
     uint32_t uses = 0, tile = 0;
     bool ok = true;
     Unit u;
@@ -764,7 +841,17 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         }
         if (j == 0) m = most;
         float base = m == -INFINITY ? 0.0f : fmaf(m, c, kSlack);
-        if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge)) {
+        const bool full = MOVES && j > 0 && j % kMoveTiles == 0 && u.place >= 0;  // (the same for all)
+        if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge || full)) {
+          if (full) {
+            float* const sums = sums_of(u.place);
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (j > kMoveTiles) ml = __ldcg(reinterpret_cast<const float2*>(sums + D));
+            const float keep = rescale(ml.x, m, c);
+            move_sums<D>(t_o, sums, keep, j > kMoveTiles, true);
+            __stcg(reinterpret_cast<float2*>(sums + D), make_float2(m, fmaf(ml.y, keep, l)));
+            l = 0.0f;
+          }
           const float next = fmaxf(m, most);
           if (j > 0 && __any_sync(0xffffffffu, next != m)) {
             const float keep = next == -INFINITY ? 1.0f : rescale(m, next, c);
@@ -821,6 +908,13 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         ok = whole_warp(mbar_wait(&o_full[i], uses++ & 1));
         if (!ok) break;
         tc_fence_after();
+      }
+      if (MOVES && u.place >= 0 && tiles > kMoveTiles) {
+        float* const sums = sums_of(u.place);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(sums + D));
+        const float keep = rescale(ml.x, m, c);
+        move_sums<D>(t_o, sums, keep, true, false);
+        l = fmaf(ml.y, keep, l);
       }
       const bool part = u.record >= 0;
       const float scale = part ? 1.0f : reach > 0 ? 1.0f / l : 0.0f;
@@ -888,6 +982,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (MOVES && threadIdx.x == 0 && s_place >= 0) give_place_back(s_place);
 }
 
 // The parts of units whose keys several blocks shared: kJoinRows rows of a unit to a
@@ -1007,7 +1102,10 @@ bool encode(CUtensorMap* m, const void* base, int d, int heads, int64_t tokens, 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+// Tiles of keys that a sequence may have (a packed one: all there are).
+int64_t most_tiles(const AttentionArgs& a) { return ((a.cu_k ? a.Tk : a.Tk / a.N) + kTile - 1) / kTile; }
+
+template <int D, bool MOVES>
 kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   using G = Shape<D>;
   // heads of a group side by side in a tile: the largest power of two in the group
@@ -1022,7 +1120,7 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   if (a.Tk > 0 && (!encode(&maps.k, a.k, D, a.kv_heads, a.Tk, a.ld_k, 1, kTile) ||
                    !encode(&maps.v, a.v, D, a.kv_heads, a.Tk, a.ld_v, 1, kTile)))
     return KDA_OK;
-  constexpr auto kern = attention_kernel<D>;
+  constexpr auto kern = attention_kernel<D, MOVES>;
   // a build that launches with fewer registers could never give the rows' warps
   // their share: it is not launched
   static const int regs = [] {
@@ -1039,7 +1137,7 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
   // when the others are done: units may be cut into parts then, as many blocks as eight
   // for each SM, no more parts than a sequence can have.  (8 x 263 queries of 32 heads
   // behind 3900 keys on average, 280 units: 120 us whole.)
-  const int64_t longest = ((a.cu_k ? a.Tk : a.Tk / a.N) + kTile - 1) / kTile;
+  const int64_t longest = most_tiles(a);
   if (units < 2 * a.sm_count) {
     int64_t splits = std::min(8 * a.sm_count / units, longest / kPartTiles);
     if (!a.cu_q) {
@@ -1056,13 +1154,20 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
     a.units = static_cast<int32_t>(units);
   }
   void* ws = nullptr;
-  if (a.splits > 1) {
-    const size_t rows = static_cast<size_t>(units) * a.splits * kRows;
-    const kda_status st = workspace_alloc(rows * (D * sizeof(float) + sizeof(float2)) + units * sizeof(PartInfo), s, &ws);
+  if (MOVES && a.sm_count > kMaxPlaces) return KDA_OK;
+  if (a.splits > 1 || MOVES) {
+    const size_t rows = a.splits > 1 ? static_cast<size_t>(units) * a.splits * kRows : 0;
+    const size_t places = MOVES ? static_cast<size_t>(a.sm_count) * kRows * (D + 4) : 0;
+    const kda_status st = workspace_alloc((places + rows * D) * sizeof(float) + rows * sizeof(float2) +
+                                              (rows ? units * sizeof(PartInfo) : 0), s, &ws);
     if (st != KDA_OK) return st;
-    a.part_out = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_out + rows * D);
-    a.parts = reinterpret_cast<PartInfo*>(a.part_ml + rows);
+    float* const at = static_cast<float*>(ws);
+    if (MOVES) a.moved = at;
+    if (a.splits > 1) {
+      a.part_out = at + places;
+      a.part_ml = reinterpret_cast<float2*>(a.part_out + rows * D);
+      a.parts = reinterpret_cast<PartInfo*>(a.part_ml + rows);
+    }
   }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
   if (e == cudaSuccess) {
@@ -1094,7 +1199,9 @@ kda_status run(AttentionArgs a, cudaStream_t s, cudaError_t& e) {
 
 kda_status launch_attention(const AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   prof_begin(s, "kda_attention_fwd");
-  const kda_status st = a.d == 128 ? run<128>(a, s, e) : run<64>(a, s, e);
+  const bool moves = most_tiles(a) > kMoveTiles;
+  const kda_status st = a.d == 128 ? (moves ? run<128, true>(a, s, e) : run<128, false>(a, s, e))
+                                   : (moves ? run<64, true>(a, s, e) : run<64, false>(a, s, e));
   prof_end(s, "kda_attention_fwd");
   return st;
 }

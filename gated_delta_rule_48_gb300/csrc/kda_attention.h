@@ -41,6 +41,9 @@ struct AttentionArgs {
   float* part_out = nullptr;
   float2* part_ml = nullptr;
   PartInfo* parts = nullptr;
+  // Units of many keys: what blocks move out of tensor memory (kda_attention.cu),
+  // [sm_count][256][d + 4]; null where no unit can have as many.
+  float* moved = nullptr;
 };
 // Allocates its workspace, if any: a status of its own if that fails, else `e`.
 kda_status launch_attention(const AttentionArgs& a, cudaStream_t s, cudaError_t& e);

@@ -39,6 +39,10 @@
 // short its warps have parts of their own instead (1000 sequences of 64 positions:
 // 124 us shared, 69 apart).
 //
+// The tensor core adds to a sum with what lies some 2^-25 below it cut off: of 2^20
+// positions of like weights to a warp the sum came out 0.5 % too small.  So every 2^17
+// positions a warp moves its sums to memory, adds them there, and begins again at 0.
+//
 // Measured, 8 key heads of 128 channels: 256 sequences of 4096 positions on average
 // and 32 query heads 244 us, 5.0 TB/s (73 % of a copy; issue slots 57 %, the ALU pipe
 // 50 %: about 300 instructions for 16 positions); one of 131,072 45 us, 3.4 TB/s, of
@@ -68,6 +72,7 @@ constexpr int kSlice = 32;        // positions of a slice: two halves, for a pag
 constexpr int kHalf = 16;
 constexpr int kDepth = 3;         // slices of a warp in flight
 constexpr int kSoloSlices = 16;   // of a unit, on average: up to as many, a warp to a unit
+constexpr int kMoveSlices = 4096; // of a warp in a unit, after which its sums are moved
 constexpr float kLowest = -3e38f; // a maximum of nothing (-infinity less itself is NaN)
 constexpr float kSlack = 8.0f;    // log2 of how far p may grow, from 2^-8 to 1 (p s' is never above s')
 constexpr float kLn2 = 0.6931471805599453f;
@@ -235,7 +240,8 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   // Short units (up to kSoloSlices slices on average) go to single warps, each with a
   // part of the line of its own: shared by a block's warps, most of a unit's time is
   // spent before its first slice and behind its last.
-  const bool solo = all <= kSoloSlices * (per_seq * a.N);
+  // (Never with so many slices to a warp that its sums would have to be moved.)
+  const bool solo = all <= kSoloSlices * (per_seq * a.N) && all <= int64_t{kMoveSlices} * kWarps * gridDim.x;
   const int workers = solo ? kWarps : 1, me = solo ? warp : 0;
   const int64_t all_workers = static_cast<int64_t>(gridDim.x) * workers;
   // no more parts than have two slices for each warp
@@ -542,7 +548,54 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
     for (int i = 0; i < kDepth - 1; ++i) fetch(pos0 + i * stride, page_of(pos0 + i * stride), i * S::kStage);
     int32_t ahead = pos0 + (kDepth - 1) * stride, next_page = page_of(ahead);
     uint32_t here = 0;  // the stage of the slice at hand
+    // Where this warp moves its sums, o and l: [sum][lane], then the columns' maxima that
+    // they were taken with.  (Of its eight records a block uses two otherwise.)
+    constexpr int kSums = 8 * G * NT, kMoved = S::kRecord * 6 / kWarps;
+    static_assert(32 * (kSums + 2 * NT) + S::kCols <= kMoved, "sums moved");
+    float* const moved = records + static_cast<int64_t>(gridDim.x) * 2 * S::kRecord +
+                         (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kMoved;
+    float* const moved_m = moved + 32 * (kSums + 2 * NT);
+    // what was moved added, by the maxima of now
+    auto add_moved = [&]() {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float keep = ex2((moved_m[8 * t + 2 * j + e] - m[t][e]) * cc[t][e]);
+          l[t][e] = fmaf(moved[(kSums + 2 * t + e) * 32 + lane], keep, l[t][e]);
+#pragma unroll
+          for (int g = 0; g < 2 * G; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& sum = o[g][t][e + 2 * h];
+              sum = fmaf(moved[((g * NT + t) * 4 + e + 2 * h) * 32 + lane], keep, sum);
+            }
+        }
+    };
+    int32_t move_at = SOLO ? stop : pos0 + min(mine, kMoveSlices) * stride;
     for (int32_t pos = pos0; pos < stop; pos += stride) {
+      if (!SOLO && pos == move_at) {
+        if (move_at - pos0 > kMoveSlices * stride) add_moved();
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int g = 0; g < 2 * G; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              moved[((g * NT + t) * 4 + e) * 32 + lane] = o[g][t][e];
+              o[g][t][e] = 0.0f;
+            }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            moved[(kSums + 2 * t + e) * 32 + lane] = l[t][e];
+            l[t][e] = 0.0f;
+            if (r == 0) moved_m[8 * t + 2 * j + e] = m[t][e];
+          }
+        }
+        __syncwarp();
+        move_at += min((stop - move_at) / stride, kMoveSlices) * stride;
+      }
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
       __syncwarp();  // this slice has come, and the one before has been read
       fetch(ahead, next_page, here == 0 ? (kDepth - 1) * S::kStage : here - S::kStage);
@@ -552,6 +605,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       else process(ring + here, pos, std::false_type{});
       here = here == (kDepth - 1) * S::kStage ? 0 : here + S::kStage;
     }
+    if (!SOLO && mine > kMoveSlices) add_moved();
 
     const bool complete = first == 0 && last == slices;
     const int slot = at == part0 ? 0 : 1;

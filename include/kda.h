@@ -630,7 +630,8 @@ kda_status kda_ssm_scan_step(const void *x, int64_t ld_x, const void *dt,
  * d is 64 or 128, else KDA_ERR_UNSUPPORTED.  n_heads is a multiple of
  * n_kv_heads.  scale is positive and finite.  total_q = 0 is a no-op.
  * Few queries over many keys are shared by several blocks; that takes a
- * workspace of up to 165 MB, allocated and freed stream-ordered on `stream`.
+ * workspace of up to 165 MB, and sums over more than 2^18 keys one of 21 MB,
+ * allocated and freed stream-ordered on `stream`.
  */
 kda_status kda_attention_fwd(const void *q, int64_t ld_q, const void *k,
                              int64_t ld_k, const void *v, int64_t ld_v,
