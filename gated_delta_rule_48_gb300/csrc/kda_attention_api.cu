@@ -35,8 +35,9 @@ kda_status check_wide(const char* name, const void* p, int64_t rows, int64_t ld,
   return KDA_OK;
 }
 
-// (a single row has no next one, whatever its distance)
-int64_t pitch_of(int64_t rows, int64_t ld) { return rows > 1 ? ld : (ld + 7) / 8 * 8; }
+// (a single row has no next one, whatever its distance: its own width does, which a tensor
+// map takes, where distances end at 2^40 bytes)
+int64_t pitch_of(int64_t rows, int64_t ld, int64_t cols) { return rows > 1 ? ld : cols; }
 
 kda_status check_sequences(const char* what, int64_t T, int32_t N, const int32_t* cu) {
   if (T < 0 || N < 0) return bad(KDA_ERR_INVALID_ARGUMENT, "%s=%lld n_seqs=%d", what, (long long)T, N);
@@ -105,8 +106,8 @@ kda_status check_span(const void* k, int64_t ld_k, const void* v, int64_t ld_v, 
   KDA_TRY(check_wide("v", v, T, ld_v, cols));
   KDA_TRY(check_rows("start", start, 1, 1, 4));
   KDA_TRY(check_rows("cu_seqlens", cu, 1, 1, 4));
-  ld_k = pitch_of(T, ld_k);
-  ld_v = pitch_of(T, ld_v);
+  ld_k = pitch_of(T, ld_k, cols);
+  ld_v = pitch_of(T, ld_v, cols);
   part[5] = rows_of("start", start, 1, N, N, 4);
   part[6] = rows_of("cu_seqlens", cu, 1, N + 1LL, N + 1LL, 4);
   part[7] = rows_of("k", k, T, ld_k, cols, 2);
@@ -170,10 +171,10 @@ extern "C" kda_status kda_attention_fwd(const void* q, int64_t ld_q, const void*
   KDA_TRY(check_rows("cu_seqlens_q", cu_seqlens_q, 1, 1, 4));
   KDA_TRY(check_rows("cu_seqlens_k", cu_seqlens_k, 1, 1, 4));
   AttentionArgs a;
-  a.ld_q = pitch_of(total_q, ld_q);
-  a.ld_k = pitch_of(total_k, ld_k);
-  a.ld_v = pitch_of(total_k, ld_v);
-  a.ld_out = pitch_of(total_q, ld_out);
+  a.ld_q = pitch_of(total_q, ld_q, wq);
+  a.ld_k = pitch_of(total_k, ld_k, wk);
+  a.ld_v = pitch_of(total_k, ld_v, wk);
+  a.ld_out = pitch_of(total_q, ld_out, wq);
   const Rows in[] = {rows_of("q", q, total_q, a.ld_q, wq, 2), rows_of("k", k, total_k, a.ld_k, wk, 2),
                      rows_of("v", v, total_k, a.ld_v, wk, 2),
                      rows_of("cu_seqlens_q", cu_seqlens_q, 1, n_seqs + 1LL, n_seqs + 1LL, 4),
@@ -256,8 +257,8 @@ extern "C" kda_status kda_kv4_attention(const void* q, int64_t ld_q, const kda_k
   KDA_TRY(check_wide("out", out, rows, ld_out, cols));
   KDA_TRY(check_rows("seq_lens", seq_lens, 1, 1, 4));
   KDA_TRY(check_rows("lse", lse, n_heads, n_heads, 4));
-  a.ld_q = pitch_of(rows, ld_q);
-  a.ld_out = pitch_of(rows, ld_out);
+  a.ld_q = pitch_of(rows, ld_q, cols);
+  a.ld_out = pitch_of(rows, ld_out, cols);
   in[5] = rows_of("seq_lens", seq_lens, 1, n_seqs, n_seqs, 4);
   in[6] = rows_of("q", q, rows, a.ld_q, cols, 2);
   const Rows outs[] = {rows_of("out", out, rows, a.ld_out, cols, 2),
