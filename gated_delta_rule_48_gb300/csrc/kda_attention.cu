@@ -628,6 +628,13 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
           units[n & 1].live = 0;
           mbar_arrive(&unit_full[n & 1]);
         }
+        // the ring's last stages are given back (by commits behind the one that the output
+        // waits for) before the block's memory goes
+        for (int i = 0; i < G::kStages && ok; ++i) {
+          ok = whole_warp(mbar_wait(&kv_empty[at], phase ^ 1));
+          if (++at == G::kStages) { at = 0; phase ^= 1; }
+        }
+        if (!ok) timeout();
       } else {
         timeout();
         // the copies in flight land before the block's memory goes
