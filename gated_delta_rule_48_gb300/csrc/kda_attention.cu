@@ -74,7 +74,7 @@ constexpr int kMoveTiles = 2048;         // of keys, after which O is moved
 constexpr int kMaxPlaces = 1024;         // for it: as many as SMs, a block to each
 // The wait for a block's next unit lasts as long as this one where a tile has no rows of
 // it, and a unit may have 2^24 tiles of keys, some 25 s.  Others last a few tiles.
-constexpr int kUnitWaits = 24;           // waits of 2 s
+constexpr uint32_t kUnitPolls = 24u << 20;  // of 2 us, as mbar_wait's
 constexpr int kHandOver = 4;             // pairs of p between a part's store and its handing over
 constexpr float kSlack = 8.0f;           // log2 of how far p may grow: from 2^-8 to 1
 constexpr float kLn2 = 0.6931471805599453f;
@@ -472,7 +472,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   __shared__ Unit units[2];
   __shared__ __align__(16) uint4 given;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_infinite, s_failed;
+  __shared__ volatile int s_infinite;
   __shared__ int s_place;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens = kRows / pack;
@@ -501,7 +501,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
       mbar_init(&v_ok[i], 1);
     }
     mbar_fence_init();
-    s_infinite = s_failed = 0;
+    s_infinite = 0;
     s_place = -1;
   }
   if (warp == 1) {
@@ -514,16 +514,11 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
   const uint32_t tmem = s_tmem;
   unsigned char* const first_k = smem + 2 * G::kTileBytes;
   unsigned char* const ring = first_k + G::kTileBytes;  // V, K; V, K
-  auto timeout = [&]() {
-    s_failed = 1;
-    atomicOr(a.err, kDevErrTimeout);
-  };
+  auto timeout = [&]() { atomicOr(a.err, kDevErrTimeout); };
   auto whole_warp = [](bool ok) { return __all_sync(0xffffffffu, ok); };
   // The block's unit number n, for all warps but the copying one.
   auto get_unit = [&](uint32_t n, Unit& u) {
-    bool there = false;
-    for (int w = 0; w < kUnitWaits && !there && !s_failed; ++w) there = mbar_wait(&unit_full[n & 1], (n >> 1) & 1);
-    if (!whole_warp(there)) return false;
+    if (!whole_warp(mbar_wait(&unit_full[n & 1], (n >> 1) & 1, kUnitPolls))) return false;
     u = units[n & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&unit_empty[n & 1]);
@@ -637,6 +632,10 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         if (!ok) timeout();
       } else {
         timeout();
+        if (lane == 0) {  // (who waits for a unit need not wait on)
+          units[n & 1].live = 0;
+          mbar_arrive(&unit_full[n & 1]);
+        }
         // the copies in flight land before the block's memory goes
         for (int i = 0; i < G::kStages; ++i) {
           mbar_wait(&kv_full[at], phase ^ 1, 1u << 16);
