@@ -41,7 +41,9 @@
 //
 // The tensor core adds to a sum with what lies some 2^-25 below it cut off: of 2^20
 // positions of like weights to a warp the sum came out 0.5 % too small.  So every 2^17
-// positions a warp moves its sums to memory, adds them there, and begins again at 0.
+// positions a warp moves its sums to memory, adds them there, and begins again at 0.  That
+// is a kernel of its own (MOVES), for tables of so many positions: others lost 1 to 3 % by
+// the code (64 x 4096 with drafts of 4: 111 us instead of 108).
 //
 // Measured, 8 key heads of 128 channels: 256 sequences of 4096 positions on average
 // and 32 query heads 244 us, 5.0 TB/s (73 % of a copy; issue slots 57 %, the ALU pipe
@@ -176,7 +178,7 @@ __device__ __forceinline__ float half_of(uint32_t pair, int i) {
 
 // (16 columns at three blocks an SM spill 0.6 KB a thread: 64 x 4096 with a draft of 4 took
 // 122 us instead of 107.)
-template <int G, int NT>
+template <int G, int NT, bool MOVES>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
   using S = Shape<G, NT>;
@@ -572,9 +574,9 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
             }
         }
     };
-    int32_t move_at = SOLO ? stop : pos0 + min(mine, kMoveSlices) * stride;
+    int32_t move_at = SOLO || !MOVES ? stop : pos0 + min(mine, kMoveSlices) * stride;
     for (int32_t pos = pos0; pos < stop; pos += stride) {
-      if (!SOLO && pos == move_at) {
+      if (MOVES && !SOLO && pos == move_at) {
         if (move_at - pos0 > kMoveSlices * stride) add_moved();
         __syncwarp();
 #pragma unroll
@@ -605,7 +607,7 @@ kv4_attention_kernel(Kv4AttentionArgs a, float* records, Meta* metas) {
       else process(ring + here, pos, std::false_type{});
       here = here == (kDepth - 1) * S::kStage ? 0 : here + S::kStage;
     }
-    if (!SOLO && mine > kMoveSlices) add_moved();
+    if (MOVES && !SOLO && mine > kMoveSlices) add_moved();
 
     const bool complete = first == 0 && last == slices;
     const int slot = at == part0 ? 0 : 1;
@@ -795,10 +797,10 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(Kv4Attentio
   }
 }
 
-template <int G, int NT>
+template <int G, int NT, bool MOVES>
 kda_status run(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   using S = Shape<G, NT>;
-  constexpr auto kern = kv4_attention_kernel<G, NT>;
+  constexpr auto kern = kv4_attention_kernel<G, NT, MOVES>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return KDA_OK;
   static const int resident = [] {
@@ -834,13 +836,20 @@ kda_status run(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   return KDA_OK;
 }
 
+// (a warp of a block sees a quarter of a sequence's slices)
+template <int G, int NT>
+kda_status pick(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
+  const int64_t positions = static_cast<int64_t>(a.pages.width) << a.pages.page_shift;
+  return positions > int64_t{kMoveSlices} * kWarps * kSlice ? run<G, NT, true>(a, s, e) : run<G, NT, false>(a, s, e);
+}
+
 }  // namespace
 
 kda_status launch_kv4_attention(const Kv4AttentionArgs& a, cudaStream_t s, cudaError_t& e) {
   const int cols = a.tokens * (a.heads / a.pages.heads);
   prof_begin(s, "kda_kv4_attention");
-  const kda_status st = a.pages.d == 128 ? (cols <= 8 ? run<4, 1>(a, s, e) : run<4, 2>(a, s, e))
-                                         : (cols <= 8 ? run<2, 1>(a, s, e) : run<2, 2>(a, s, e));
+  const kda_status st = a.pages.d == 128 ? (cols <= 8 ? pick<4, 1>(a, s, e) : pick<4, 2>(a, s, e))
+                                         : (cols <= 8 ? pick<2, 1>(a, s, e) : pick<2, 2>(a, s, e));
   prof_end(s, "kda_kv4_attention");
   return st;
 }
