@@ -21,17 +21,20 @@
 // A block stays on its SM and asks for further units (cluster launch control), so that
 // one unit's first copies run beside the last one's output.  Units go out with the most
 // keys first.  Few units are cut along the keys, up to eight blocks for each SM, and a
-// second launch joins the parts (32 queries over 65,536 keys, 8 x 128 channels: 0.7 ms
-// whole, 37 us cut).
+// second launch joins the parts (32 queries of 8 heads over 65,536 keys of one, 128
+// channels: 0.7 ms whole, 38 us cut).  The parts of a unit are equal, so sizes just above
+// a full wave of units do badly (2500 queries below).
 //
 // Bound: for long sequences the products and the softmax beside them.  Two tiles by
 // 128 keys are 2048 cycles of products (d = 128); a full wave (2432 queries over 16,384
-// keys, 16 heads, not causal) takes 179 us, 1.82 PFLOP/s of 1.9, 32,768 causal tokens of
-// 16 heads 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.
-// With d = 64 it is the exponentials: 16 a cycle and SM, 128 x 256 of them to 1024 cycles
-// of products.  For short ones it is the units' ends: 4 x 4096 tokens of 32 heads 375 to
-// 415 us (1.33 to 1.47 PFLOP/s), 100 tokens 10.6 us, most of it the way from the launch
-// to the first product and from the last one to the output.
+// keys, 16 heads, not causal) takes 179 us, 1.82 PFLOP/s of 1.9, but 2500 queries over
+// 16,452 282 us: 158 units in halves, three rounds.  32,768 causal tokens of 16 heads take
+// 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.  With d = 64
+// it is the exponentials: 16 a cycle and SM, 128 x 256 of them to 1024 cycles of products.
+// For short ones it is the units' ends: 4 x 4096 tokens of 32 heads 375 to 415 us (1.33 to
+// 1.47 PFLOP/s), 100 tokens 10.6 us, most of it the way from the launch to the first
+// product and from the last one to the output, 1024 tokens 36 us, of which the halves'
+// output and the join are a good part (2048, whole: 36 us).
 //
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
 // type); the sum l is of the unrounded p, in 32 bits.

@@ -6,8 +6,9 @@
 //
 // Bound: bytes (2 read and 0.5625 written per value, or the reverse): 65,536 tokens
 // of 8 x 128 keys and values are read back in 57 us, 6.0 TB/s; 16,384
-// are written and read back in 39 us, 4.4 TB/s (partly from L2); 256 in 2.6 and 2.8,
-// latencies.  (Written with a division per value: twice the time.)  Four
+// are written and read back in 39 us, 4.4 TB/s (partly from L2; the write 44 % of HBM's
+// rate: a block does one pass over 8 tokens behind a chain of lookups); 256 in 2.6 and
+// 2.8, latencies.  (Written with a division per value: twice the time.)  Four
 // lanes take a token and head: lane j reads channels 8 j .. 8 j + 7 of every
 // group, 16 bytes at a time, and ends up with 16 bytes of codes that lie side by
 // side; a group's maximum is that of its four lanes.

@@ -5,8 +5,8 @@
 // with c = scale log2 e, a key's scales s and codes n, a value's s' and n', per
 // group g of 32 channels.
 //
-// Bound: the cache's bytes (1.125 per channel of a token and head), and close to
-// them the instructions that take codes apart.  A step is a token or a few, so
+// Bound: the cache's bytes (1.125 per channel of a token and head), and beside
+// them the latency of taking codes apart.  A step is a token or a few, so
 // that there are 1 to 16 query rows (tokens x heads of a group) for each key: too
 // few for tensor memory's 128 lanes, and codes would have to go through shared
 // memory as bf16 first.  So the products are warp-wide ones (m16n8k16) with the
@@ -16,8 +16,8 @@
 //   - A key's code n + 8 in the low bits of a 16-bit half is the f16 number
 //     (n + 8) 2^-24 as it stands (a subnormal one), in bits 4..7 16 times that: two
 //     codes to an AND, and four bits' shift less.  The queries' bf16 values are f16
-//     ones after a power of two for each row (what is 2^30 times smaller than a row's
-//     largest value may round).  The 8 goes away with the accumulator's first
+//     ones after a power of two for each row (what is 2^28 times smaller than a row's
+//     largest value may round: odd channels are read 16 times as large).  The 8 goes away with the accumulator's first
 //     value, one product of the groups' scales with -8 2^-24 sum_{c in g} q_c in four
 //     bf16 parts.  (So a score's rounding goes by the sums of |q| (|n| + 16), not of
 //     |q n|: 2^-23 of them a step.)
@@ -47,9 +47,11 @@
 //
 // Measured, 8 key heads of 128 channels: 256 sequences of 4096 positions on average
 // and 32 query heads 244 us, 5.0 TB/s (73 % of a copy; issue slots 57 %, the ALU pipe
-// 50 %: about 300 instructions for 16 positions); one of 131,072 45 us, 3.4 TB/s, of
+// 50 %: about 300 instructions for 16 positions, three warps to a scheduler and no pipe
+// saturated: latency); one of 131,072 45 us, 3.4 TB/s, of
 // which some 15 are launches, first copies and the combination; 16 columns instead
-// of 8 107 us instead of 75 (64 x 4096): the products, the softmax and their registers.
+// of 8 107 us instead of 75 (64 x 4096): the products, the softmax and their registers,
+// two blocks an SM for three.
 // The next slice's scores before this one's values, so that one chain covers the
 // other, were slower (253 us instead of 243): its copies have a slice less of time.
 #include <string.h>

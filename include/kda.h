@@ -627,8 +627,10 @@ kda_status kda_ssm_scan_step(const void *x, int64_t ld_x, const void *dt,
  *        and lse are then unspecified).  cu_seqlens_k NULL = cu_seqlens_q; both
  *        NULL = n_seqs sequences of total_q / n_seqs queries and
  *        total_k / n_seqs keys.
- * d is 64 or 128, else KDA_ERR_UNSUPPORTED.  n_heads is a multiple of
- * n_kv_heads.  scale is positive and finite.  total_q = 0 is a no-op.
+ * d is 64 or 128, n_heads at most 65536, total_q and total_k below 2^31 and
+ * total_q * n_heads at most 2^37, else KDA_ERR_UNSUPPORTED.  n_heads is a
+ * multiple of n_kv_heads.  scale is positive and finite (scale * log2 e too).
+ * total_q = 0 is a no-op.
  * Few queries over many keys are shared by several blocks; that takes a
  * workspace of up to 165 MB, and sums over more than 2^18 keys one of 21 MB,
  * allocated and freed stream-ordered on `stream`.
@@ -684,7 +686,7 @@ typedef struct {
  * max_pages is reported by kda_get_device_error; it is not written, or its row
  * is left as it is.  Two tokens of one write must not have the same page and
  * place: what such a place then holds is unspecified.
- * T = 0 or N = 0 are valid.  Allocates nothing.
+ * T = 0 or N = 0 are valid; T is below 2^31.  Allocates nothing.
  */
 kda_status kda_kv4_write(const void *k, int64_t ld_k, const void *v,
                          int64_t ld_v, const kda_kv4_cache *cache,
@@ -720,8 +722,8 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * valid page (as in kda_kv4_write) is reported by kda_get_device_error, and its
  * sequence's rows are then unspecified.  n_heads is a multiple of the cache's
  * n_kv_heads.  scale is positive and finite; q and scale * q are below 2^112 in
- * magnitude (else the query's rows are unspecified).  N = 0 or n_tokens = 0 are
- * no-ops.
+ * magnitude (else the query's rows are unspecified).  N * n_tokens * n_heads is
+ * below 2^31.  N = 0 or n_tokens = 0 are no-ops.
  * Long sequences are shared by several blocks; that takes a workspace of up to
  * 21 MB, allocated and freed stream-ordered on `stream`.
  */
