@@ -22,7 +22,7 @@
 // one unit's first copies run beside the last one's output.  Units go out with the most
 // keys first.  Few units are cut along the keys, up to eight blocks for each SM, and a
 // second launch joins the parts (32 queries of 8 heads over 65,536 keys of one, 128
-// channels: 0.7 ms whole, 38 us cut).  The parts of a unit are equal, so sizes just above
+// channels: 0.7 ms whole, 32 us cut).  The parts of a unit are equal, so sizes just above
 // a full wave of units do badly (2500 queries below).
 //
 // Bound: for long sequences the products and the softmax beside them.  Two tiles by
@@ -134,7 +134,7 @@ __device__ __forceinline__ float log_of_sum(float m, float l, float scale) {
 
 // What a block works on: 256 rows of a sequence.
 struct Unit {
-  int32_t live;        // 0: no more
+  int32_t live;        // 0: no more; from 2 on: O is moved to place live - 2 (48 bytes in all)
   int32_t q0, n_q;     // the sequence's queries
   int32_t k0, len;     // and keys
   int32_t tok0;        // the unit's first query, in the sequence
@@ -142,7 +142,6 @@ struct Unit {
   int32_t tiles[2];    // of keys, for each tile of rows
   int32_t masked;      // from this one on some row does not reach a tile's keys all
   int32_t record;      // where a part of the keys is kept; -1: the unit has all of them
-  int32_t place;       // where O is moved after kMoveTiles tiles; -1: there are no more
 
   // how many keys query `tok` of the sequence reaches
   __device__ __forceinline__ int32_t reach(int32_t tok, bool causal) const {
@@ -216,7 +215,7 @@ __device__ bool find_unit(const AttentionArgs& a, int pack, int shift, int32_t i
     index = a.cu_q ? index / a.splits : index % a.units;
   }
   parts = 1;
-  u.record = u.place = -1;
+  u.record = -1;
   const int head_blocks = a.heads / pack;
   const int32_t slot = index / head_blocks, hb = index - slot * head_blocks;
   int32_t block;
@@ -565,7 +564,7 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
               if (s_place < 0) timeout();
             }
             __syncwarp();
-            u.place = s_place;
+            u.live = 2 + s_place;
           }
           ok = whole_warp(mbar_wait(&unit_empty[n & 1], ((n >> 1) & 1) ^ 1));  // (the first round passes at once)
           if (!ok) break;
@@ -858,10 +857,10 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         }
         if (j == 0) m = most;
         float base = m == -INFINITY ? 0.0f : fmaf(m, c, kSlack);
-        const bool full = MOVES && j > 0 && j % kMoveTiles == 0 && u.place >= 0;  // (the same for all)
+        const bool full = MOVES && j > 0 && j % kMoveTiles == 0 && u.live >= 2;  // (the same for all)
         if (__any_sync(0xffffffffu, (most - m) * c > kSlack || fabsf(base) > kLarge || full)) {
           if (full) {
-            float* const sums = sums_of(u.place);
+            float* const sums = sums_of(u.live - 2);
             float2 ml = make_float2(-INFINITY, 0.0f);
             if (j > kMoveTiles) ml = __ldcg(reinterpret_cast<const float2*>(sums + D));
             const float keep = rescale(ml.x, m, c);
@@ -926,8 +925,8 @@ attention_kernel(const __grid_constant__ Maps maps, AttentionArgs a, int pack) {
         if (!ok) break;
         tc_fence_after();
       }
-      if (MOVES && u.place >= 0 && tiles > kMoveTiles) {
-        float* const sums = sums_of(u.place);
+      if (MOVES && u.live >= 2 && tiles > kMoveTiles) {
+        float* const sums = sums_of(u.live - 2);
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(sums + D));
         const float keep = rescale(ml.x, m, c);
         move_sums<D>(t_o, sums, keep, true, false);
@@ -1035,21 +1034,83 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[r][e] = 0.0f;
   }
-  auto add = [&](int r, const float2& ml, const float (&v)[kPer]) {
-    const float next = fmaxf(m[r], ml.x), keep = rescale(m[r], next, c), w = rescale(ml.x, next, c);
-    m[r] = next;
-    l[r] = fmaf(ml.y, w, l[r] * keep);
+  if constexpr (SHARED) {
+    if (parts <= kJoinWarps) {  // a part to a warp: as it is
+      const int64_t at = first + static_cast<int64_t>(warp) * kRows;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(v[e], w, o[r][e] * keep);
-  };
+      for (int r = 0; r < kMine; ++r) {
+        if (warp >= parts) break;
+        load_n<kPer>(a.part_out + (at + r) * D + kPer * lane, o[r]);
+        const float2 ml = a.part_ml[at + r];
+        m[r] = ml.x;
+        l[r] = ml.y;
+      }
+    } else {
+      // This warp's parts: the maximum and the weight of a part by a lane, its sums by all
+      // lanes.  (A weight computed by all lanes for each part and row, and sums rescaled from
+      // part to part: 32 queries of 8 heads over 65,536 keys took 47 us instead of 32.  For few
+      // parts that is the faster way, 9.1 us instead of 9.6 for 128 units of two.)
+      auto part_ml = [&](int32_t p, int r) {
+        return p < parts ? a.part_ml[first + static_cast<int64_t>(p) * kRows + r] : make_float2(-INFINITY, 0.0f);
+      };
+      float2 ml[kMine];
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+        ml[r] = part_ml(warp + kJoinWarps * lane, r);
+        m[r] = ml[r].x;
+      }
+      for (int32_t p = warp + kJoinWarps * (lane + 32); p < parts; p += 32 * kJoinWarps) {
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) m[r] = fmaxf(m[r], part_ml(p, r).x);
+      }
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+#pragma unroll
+        for (int w = 16; w; w /= 2) m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], w));
+      }
+      for (int32_t p0 = warp; p0 < parts; p0 += 32 * kJoinWarps) {
+        float weight[kMine];
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
+          if (p0 != warp) ml[r] = part_ml(p0 + kJoinWarps * lane, r);
+          weight[r] = rescale(ml[r].x, m[r], c);
+          l[r] = fmaf(ml[r].y, weight[r], l[r]);
+        }
+        const int32_t count = min(32, (parts - p0 + kJoinWarps - 1) / kJoinWarps);
 #pragma unroll 2
-  for (int32_t p = SHARED ? warp : 0; p < parts; p += SHARED ? kJoinWarps : 1) {
-    const int64_t at = first + static_cast<int64_t>(p) * kRows;
+        for (int32_t i = 0; i < count; ++i) {
+          const int64_t at = first + static_cast<int64_t>(p0 + kJoinWarps * i) * kRows;
 #pragma unroll
-    for (int r = 0; r < kMine; ++r) {
-      float v[kPer];
-      load_n<kPer>(a.part_out + (at + r) * D + kPer * lane, v);
-      add(r, a.part_ml[at + r], v);
+          for (int r = 0; r < kMine; ++r) {
+            float v[kPer];
+            load_n<kPer>(a.part_out + (at + r) * D + kPer * lane, v);
+            const float w = __shfl_sync(0xffffffffu, weight[r], i);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(v[e], w, o[r][e]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+#pragma unroll
+        for (int w = 16; w; w /= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+      }
+    }
+  } else {
+#pragma unroll 2
+    for (int32_t p = 0; p < parts; ++p) {
+      const int64_t at = first + static_cast<int64_t>(p) * kRows;
+#pragma unroll
+      for (int r = 0; r < kMine; ++r) {
+        float v[kPer];
+        load_n<kPer>(a.part_out + (at + r) * D + kPer * lane, v);
+        const float2 ml = a.part_ml[at + r];
+        const float next = fmaxf(m[r], ml.x), keep = rescale(m[r], next, c), w = rescale(ml.x, next, c);
+        m[r] = next;
+        l[r] = fmaf(ml.y, w, l[r] * keep);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[r][e] = fmaf(v[e], w, o[r][e] * keep);
+      }
     }
   }
   auto put = [&](int row, int r) {
@@ -1073,14 +1134,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, int
       if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
     }
     __syncthreads();
-    m[0] = -INFINITY;
+    // a row to a warp, in the parts' order of warps, a warp's weight by a lane
+    const float2 of = s_ml[lane % kJoinWarps][warp];
+    m[0] = of.x;
+#pragma unroll
+    for (int w = kJoinWarps / 2; w; w /= 2) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], w));
+    const float weight = rescale(of.x, m[0], c), part_l = of.y * weight;
     l[0] = 0.0f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[0][e] = 0.0f;
-    for (int w = 0; w < kJoinWarps; ++w) {  // a row to a warp, in the parts' order of warps
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
       float v[kPer];
       load_n<kPer>(&s_o[w][warp][kPer * lane], v);
-      add(0, s_ml[w][warp], v);
+      l[0] += __shfl_sync(0xffffffffu, part_l, w);
+      const float by = __shfl_sync(0xffffffffu, weight, w);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[0][e] = fmaf(v[e], by, o[0][e]);
     }
     put(row0 + warp, 0);
   } else {
