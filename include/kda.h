@@ -715,7 +715,7 @@ kda_status kda_kv4_read(void *k, int64_t ld_k, void *v, int64_t ld_v,
  * where the largest |n s| times the number of positions reached is below 2^132.
  *
  *   q         bf16 [N, n_tokens, n_heads, d], tokens ld_q apart      read
- *   seq_lens  i32 [N]                                                read
+ *   seq_lens  i32 [N], at most 2^31 - 4096; below zero counts as 0   read
  *   out       bf16 [N, n_tokens, n_heads, d], tokens ld_out apart    written
  *   lse       f32 [N, n_tokens, n_heads], dense   written; NULL = not produced
  * q and out start on a 16-byte boundary at every token.  A position without a

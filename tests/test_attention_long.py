@@ -69,6 +69,34 @@ def test_calls_with_many_keys_side_by_side():
 
 
 @pytest.mark.gpu
+def test_captured_calls_with_many_keys():
+    """Two graphs replayed side by side, over keys that change."""
+    n, d = 300_000, 128
+    q = torch.zeros(1, 305, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device=DEV)
+    v = (0.5 + torch.rand(n, 1, d, generator=gen(3), device=DEV)).bfloat16()
+    kb.kda_attention_fwd(q, k, v)
+    graphs, outs, streams = [], [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        outs.append(torch.empty_like(q))
+        with torch.cuda.graph(graphs[-1]):
+            kb.kda_attention_fwd(q, k, v, out=outs[-1])
+        streams.append(torch.cuda.Stream())
+    for i in range(2):
+        v.copy_(0.5 + i + torch.rand(n, 1, d, generator=gen(i), device=DEV))
+        want = kb.kda_attention_fwd(q, k, v)[0]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for graph, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
+    assert kb.kda_get_device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads,d,n,rise", [(2, 64, 1 << 24, 0.0), (2, 128, 1 << 22, 0.0), (12, 128, (1 << 21) + 50, 0.5),
                                             (4, 64, (1 << 20) + 1234, 0.5)])
 def test_many_positions_of_like_weights(heads, d, n, rise):
