@@ -30,11 +30,12 @@
 // keys, 16 heads, not causal) takes 179 us, 1.82 PFLOP/s of 1.9, but 2500 queries over
 // 16,452 282 us: 158 units in halves, three rounds.  32,768 causal tokens of 16 heads take
 // 2.35 to 2.8 ms, 1.56 to 1.87 PFLOP/s, by how long the power limit has held.  With d = 64
-// it is the exponentials: 16 a cycle and SM, 128 x 256 of them to 1024 cycles of products.
-// For short ones it is the units' ends: 4 x 4096 tokens of 32 heads 375 to 415 us (1.33 to
-// 1.47 PFLOP/s), 100 tokens 10.6 us, most of it the way from the launch to the first
-// product and from the last one to the output, 1024 tokens 36 us, of which the halves'
-// output and the join are a good part (2048, whole: 36 us).
+// the floor is the exponentials: 16 a cycle and SM, 128 x 256 of them to 1024 cycles of
+// products.  For short ones it is the units' ends: 4 x 4096 tokens of 32 heads 375 to 415 us
+// (1.33 to 1.47 PFLOP/s), 2 x 4096 with d = 64 155 us (both pipes 40 % busy), 100 tokens
+// 10.6 us, most of it the way from the launch to the first product and from the last one to
+// the output, 1024 tokens 36 us, of which the halves' output and the join are a good part
+// (2048, whole: 36 us).
 //
 // P is rounded to bf16 because the tensor core multiplies bf16 by bf16 (V's
 // type); the sum l is of the unrounded p, in 32 bits.
@@ -83,8 +84,8 @@ constexpr float kSlack = 8.0f;           // log2 of how far p may grow: from 2^-
 constexpr float kLn2 = 0.6931471805599453f;
 // Up to here p = 2^(c s - b) with b = c m + 8 rounded once: all of a row's p, and its l and o,
 // have the same factor 2^(c m + 8 - b), at most 2^(1/32), which o / l and log l + b take
-// off again.  From here on that factor grows (from 2^31 on p would be 0 or infinite): m is taken
-// off the scores before c is multiplied in.
+// off again.  From here on that factor grows (from 2^31 on p would be 0 or infinite): m is
+// taken off the scores before c is multiplied in.
 constexpr float kLarge = 1048576.0f;
 
 template <int D>
